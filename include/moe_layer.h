@@ -222,8 +222,9 @@ int moe_experts_forward(const moe_desc* d, int32_t T, const void* x, const int32
 
 /*
  * Timing hook for profilers and benchmarks: the next moe_layer_forward,
- * moe_layer_forward_staged, moe_router_topk or moe_experts_forward call made
- * on this host thread launches its j-th kernel (j = 0, 1, ...) with events[2j]
+ * moe_layer_forward_staged, moe_router_topk or moe_experts_forward call, or
+ * call that enqueues work of moe_route.h or mxfp4.h, made on this host thread
+ * launches its j-th kernel (j = 0, 1, ...) with events[2j]
  * and events[2j+1] attached (hipExtLaunchKernel), so the runtime stamps them
  * with that dispatch's own start and end: hipEventElapsedTime of the pair is
  * the kernel's execution time.  Kernels beyond capacity / 2 launch untimed.

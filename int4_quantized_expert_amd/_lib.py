@@ -68,6 +68,38 @@ class GdnDesc(ctypes.Structure):
     ]
 
 
+class RouteDesc(ctypes.Structure):
+    """Descriptor of expert routing from scores (moe_route.h)."""
+    _fields_ = [
+        ("n_experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("n_groups", ctypes.c_int32),
+        ("top_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("logit_dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class MxProductDesc(ctypes.Structure):
+    """Descriptor of a product of microscaled 4-bit matrices (mxfp4.h)."""
+    _fields_ = [
+        ("n", ctypes.c_int32),
+        ("k", ctypes.c_int32),
+        ("a_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+        ("n_experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("pair_rows", ctypes.c_int32),
+        ("codes_off", ctypes.c_int64),
+        ("scales_off", ctypes.c_int64),
+        ("pool_bytes", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -145,6 +177,25 @@ def lib() -> ctypes.CDLL:
         L.moe_set_launch_events.restype = ctypes.c_int
         L.gdn_recurrence_forward.argtypes = [ctypes.POINTER(GdnDesc), i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]
         L.gdn_recurrence_forward.restype = ctypes.c_int
+        rp, mp = ctypes.POINTER(RouteDesc), ctypes.POINTER(MxProductDesc)
+        L.moe_route_forward.argtypes = [rp, i32, vp, i64, vp, vp, vp, vp]
+        L.moe_route_forward.restype = ctypes.c_int
+        L.moe_router_route.argtypes = [dp, rp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_router_route.restype = ctypes.c_int
+        L.mx_codes_bytes.argtypes = [i64, i64]
+        L.mx_codes_bytes.restype = i64
+        L.mx_scales_bytes.argtypes = [i64, i64]
+        L.mx_scales_bytes.restype = i64
+        L.mx_quantize.argtypes = [i32, i64, i64, vp, i64, vp, vp, vp]
+        L.mx_quantize.restype = ctypes.c_int
+        L.mx_dequantize.argtypes = [i32, i64, i64, vp, vp, vp, i64, vp]
+        L.mx_dequantize.restype = ctypes.c_int
+        L.mx_workspace_bytes.argtypes = [mp, i32]
+        L.mx_workspace_bytes.restype = sz
+        L.mx_linear_forward.argtypes = [mp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.mx_linear_forward.restype = ctypes.c_int
+        L.mx_experts_forward.argtypes = [mp, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.mx_experts_forward.restype = ctypes.c_int
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
@@ -303,6 +354,190 @@ def residual_add(T: int, H: int, act: str, x, y, x_next, stream=None) -> None:
 def status_check(ws, stream=None) -> None:
     """Blocking: raises MoeError(MOE_ERANGE) if a kernel skipped a pair since the last check."""
     _check(lib().moe_status_check(_ptr(ws), _stream(stream, ws)))
+
+
+# ---------------------------------------------------------------------------
+# Routing from scores (moe_route.h) and microscaled 4-bit operators (mxfp4.h).
+#
+# Where an argument is a torch tensor, its type, size and layout are checked
+# here against what the entry point will read or write, and the call runs on
+# the tensors' device; plain addresses are passed on as they are.
+
+MX_FP4 = 2
+MX_ACT_NONE, MX_ACT_SWIGLU = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+
+
+def _bad(msg: str):
+    raise MoeError(-1, msg)
+
+
+def _torch_dtype(code: int):
+    import torch
+    return torch.float32 if code == MOE_F32 else torch.bfloat16
+
+
+def _check_tensor(name: str, t, dtype, need: int) -> None:
+    """A contiguous device tensor of at least `need` elements of `dtype` (None and addresses pass)."""
+    if t is None or isinstance(t, int):
+        return
+    if t.dtype != dtype:
+        _bad(f"{name} is {t.dtype}, {dtype} expected")
+    if not t.is_contiguous():
+        _bad(f"{name} is not contiguous")
+    if t.numel() < need:
+        _bad(f"{name} has {t.numel()} elements, {need} needed")
+
+
+def _call_on(tensors, stream, fn, *args) -> None:
+    """fn(*args, stream) on the device that the tensors share."""
+    import torch
+    dev = None
+    for t in tensors:
+        if t is not None and not isinstance(t, int):
+            if t.device.type != "cuda":
+                _bad(f"a tensor is on {t.device}, not on a GPU")
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                _bad(f"tensors on {dev} and {t.device}")
+    if dev is None or dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)))
+
+
+def route_desc(n_experts, top_k, score="softmax", n_groups=1, top_groups=1, group_top=1, renormalize=True, scale=1.0,
+               logits="f32") -> RouteDesc:
+    """Descriptor of routing from scores: score "softmax" or "sigmoid", logits "f32" or "bf16"."""
+    return RouteDesc(n_experts, top_k, {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}[score], n_groups,
+                     top_groups, group_top, int(bool(renormalize)), {"f32": MOE_F32, "bf16": MOE_BF16}[logits],
+                     float(scale))
+
+
+def route(r: RouteDesc, T: int, logits, bias, topk_ids, topk_w, logits_stride=None, stream=None) -> None:
+    """Routing of T tokens from their logits (moe_route_forward).  logits: [T, n_experts], rows may be strided;
+    logits_stride (elements) defaults to the tensor's, for an address to n_experts."""
+    import torch
+    E, k = r.n_experts, r.top_k
+    if not isinstance(logits, int):
+        if logits.dim() != 2 or logits.shape[0] < T or logits.shape[1] < E or (E > 1 and logits.stride(1) != 1):
+            _bad(f"logits of shape {tuple(logits.shape)}, strides {logits.stride()}: rows of {E} adjacent values expected")
+        if logits.dtype != _torch_dtype(r.logit_dtype):
+            _bad(f"logits is {logits.dtype}, {_torch_dtype(r.logit_dtype)} expected")
+        if logits_stride is None:
+            logits_stride = logits.stride(0)
+        elif T > 1 and logits_stride != logits.stride(0):
+            _bad(f"logits_stride={logits_stride} differs from the tensor's {logits.stride(0)}")
+    elif logits_stride is None:
+        logits_stride = E
+    _check_tensor("bias", bias, torch.float32, E)
+    _check_tensor("topk_ids", topk_ids, torch.int32, T * k)
+    _check_tensor("topk_w", topk_w, torch.float32, T * k)
+    _call_on((logits, bias, topk_ids, topk_w), stream, lib().moe_route_forward, ctypes.byref(r), T, _ptr(logits),
+             logits_stride, _ptr(bias), _ptr(topk_ids), _ptr(topk_w))
+
+
+def router_route(d: MoeDesc, r: RouteDesc, T: int, x, router_w, bias, topk_ids, topk_w, ws, stream=None) -> None:
+    """router_topk with routing from scores: logits R x, then route (moe_router_route)."""
+    import torch
+    _check_tensor("bias", bias, torch.float32, r.n_experts)
+    _check_tensor("topk_ids", topk_ids, torch.int32, T * r.top_k)
+    _check_tensor("topk_w", topk_w, torch.float32, T * r.top_k)
+    _call_on((x, router_w, bias, topk_ids, topk_w, ws), stream, lib().moe_router_route, ctypes.byref(d),
+             ctypes.byref(r), T, _ptr(x), _ptr(router_w), _ptr(bias), _ptr(topk_ids), _ptr(topk_w), _ptr(ws),
+             _nbytes(ws))
+
+
+def mx_shapes(rows: int, cols: int) -> tuple[tuple[int, int], tuple[int, int]]:
+    """Shapes of the uint8 codes and scales tensors of an MX matrix [rows, cols]."""
+    if lib().mx_codes_bytes(rows, cols) < 0:
+        _bad(f"an MX matrix of {rows} x {cols} is negative or too large")
+    padded = -(-cols // 256) * 256
+    return (rows, padded // 2), (rows, padded // 32)
+
+
+def _mx_rows(name: str, t):
+    """(dtype code, rows, cols, row stride) of a 2-d tensor whose rows are adjacent values."""
+    import torch
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        _bad(f"{name} of shape {tuple(t.shape)}, strides {t.stride()}: a matrix with adjacent values in its rows expected")
+    code = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}.get(t.dtype)
+    if code is None:
+        _bad(f"{name} is {t.dtype}, float32 or bfloat16 expected")
+    return code, t.shape[0], t.shape[1], t.stride(0)
+
+
+def _check_mx(name: str, codes, scales, rows: int, cols: int) -> None:
+    import torch
+    (_, c), (_, s) = mx_shapes(rows, cols)
+    _check_tensor(f"{name} codes", codes, torch.uint8, rows * c)
+    _check_tensor(f"{name} scales", scales, torch.uint8, rows * s)
+
+
+def mx_quantize(x, codes, scales, stream=None) -> None:
+    """The rows of x (float32 or bfloat16 [rows, cols], rows may be strided) into an MX matrix."""
+    dtype, rows, cols, stride = _mx_rows("x", x)
+    _check_mx("the", codes, scales, rows, cols)
+    _call_on((x, codes, scales), stream, lib().mx_quantize, dtype, rows, cols, _ptr(x), stride, _ptr(codes),
+             _ptr(scales))
+
+
+def mx_dequantize(codes, scales, out, stream=None) -> None:
+    """The values that an MX matrix holds into out (float32 or bfloat16 [rows, cols], rows may be strided); exact."""
+    dtype, rows, cols, stride = _mx_rows("out", out)
+    _check_mx("the", codes, scales, rows, cols)
+    _call_on((codes, scales, out), stream, lib().mx_dequantize, dtype, rows, cols, _ptr(codes), _ptr(scales),
+             _ptr(out), stride)
+
+
+def mx_product_desc(n, k, a="bf16", out="bf16", act="none", n_experts=0, top_k=0, pair_rows=False, codes_off=0,
+                    scales_off=0, pool_bytes=0) -> MxProductDesc:
+    """Descriptor of a product; a: "f32", "bf16" or "mx"; act: "none" or "swiglu".  n_experts and the fields after
+    it are for mx_experts."""
+    return MxProductDesc(n, k, {"f32": MOE_F32, "bf16": MOE_BF16, "mx": MX_FP4}[a], {"f32": MOE_F32, "bf16": MOE_BF16}[out],
+                         {"none": MX_ACT_NONE, "swiglu": MX_ACT_SWIGLU}[act], n_experts, top_k, int(bool(pair_rows)),
+                         codes_off, scales_off, pool_bytes)
+
+
+def mx_workspace_bytes(d: MxProductDesc, T_max: int) -> int:
+    n = lib().mx_workspace_bytes(ctypes.byref(d), T_max)
+    if n == 0:
+        raise MoeError(-1, last_error())
+    return n
+
+
+def _check_a(d: MxProductDesc, a, a_scales, rows: int) -> None:
+    if d.a_dtype == MX_FP4:
+        _check_mx("a", a, a_scales, rows, d.k)
+    else:
+        _check_tensor("a", a, _torch_dtype(d.a_dtype), rows * d.k)
+
+
+def mx_linear(d: MxProductDesc, M: int, a, a_scales, w_codes, w_scales, out, ws, stream=None) -> None:
+    """out = a W^T for M rows of a (mx_linear_forward); a_scales is None unless a is an MX matrix."""
+    _check_a(d, a, a_scales, M)
+    _check_mx("w", w_codes, w_scales, d.n * (2 if d.act == MX_ACT_SWIGLU else 1), d.k)
+    _check_tensor("out", out, _torch_dtype(d.out_dtype), M * d.n)
+    _call_on((a, a_scales, w_codes, w_scales, out, ws), stream, lib().mx_linear_forward, ctypes.byref(d), M, _ptr(a),
+             _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), _ptr(out), _ptr(ws), _nbytes(ws))
+
+
+def mx_experts(d: MxProductDesc, T: int, a, a_scales, topk_ids, topk_w, slot_table, pool, out, ws, stream=None) -> None:
+    """Product by routed expert (mx_experts_forward); topk_w None: one output row per pair, else the weighted sums."""
+    import torch
+    pairs = T * d.top_k
+    _check_a(d, a, a_scales, pairs if d.pair_rows else T)
+    _check_tensor("topk_ids", topk_ids, torch.int32, pairs)
+    _check_tensor("topk_w", topk_w, torch.float32, pairs)
+    _check_tensor("slot_table", slot_table, torch.int64, d.n_experts)
+    if not isinstance(pool, int) and _nbytes(pool) < d.pool_bytes:
+        _bad(f"pool has {_nbytes(pool)} bytes, pool_bytes is {d.pool_bytes}")
+    _check_tensor("out", out, _torch_dtype(d.out_dtype), (pairs if topk_w is None else T) * d.n)
+    _call_on((a, a_scales, topk_ids, topk_w, slot_table, pool, out, ws), stream, lib().mx_experts_forward,
+             ctypes.byref(d), T, _ptr(a), _ptr(a_scales), _ptr(topk_ids), _ptr(topk_w), _ptr(slot_table), _ptr(pool),
+             _ptr(out), _ptr(ws), _nbytes(ws))
 
 
 class LaunchTimer:

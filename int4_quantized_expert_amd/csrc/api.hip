@@ -26,18 +26,6 @@ struct LaunchMarks {
 };
 thread_local LaunchMarks g_marks;
 
-// Scope of one API call that may consume the timing events: the destructor
-// publishes the count and clears the setting when the call ends, whichever
-// way it ends.
-struct MarkScope {
-  ~MarkScope() {
-    if (g_marks.cap > 0 && g_marks.n_out) *g_marks.n_out = g_marks.used;
-    g_marks.cap = 0;
-    g_marks.used = 0;
-    g_marks.n_out = nullptr;
-  }
-};
-
 int fail(int code, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -221,6 +209,13 @@ int api_ok() { return ok(); }
 }  // namespace moe
 
 namespace moe {
+MarkScope::~MarkScope() {
+  if (g_marks.cap > 0 && g_marks.n_out) *g_marks.n_out = g_marks.used;
+  g_marks.cap = 0;
+  g_marks.used = 0;
+  g_marks.n_out = nullptr;
+}
+
 bool next_launch_events(hipEvent_t* start, hipEvent_t* stop) {
   if (g_marks.used + 2 > g_marks.cap) return false;
   *start = g_marks.ev[g_marks.used];
@@ -250,7 +245,7 @@ int moe_workspace_init(void* workspace, size_t ws_bytes, void* stream) {
 
 int moe_router_topk(const moe_desc* d, int32_t T, const void* x, const void* router_w, int32_t* topk_ids,
                     float* topk_w, void* workspace, size_t ws_bytes, void* stream) {
-  MarkScope marks;
+  moe::MarkScope marks;
   int rc;
   if ((rc = check_desc(d)) || (rc = check_T(T))) return rc;
   if (!x || !router_w || !topk_ids || !topk_w) return fail(MOE_EINVAL, "NULL x, router_w, topk_ids or topk_w");
@@ -270,10 +265,43 @@ int moe_router_topk(const moe_desc* d, int32_t T, const void* x, const void* rou
   return finish(moe::launch_router_topk(c, topk_ids, topk_w));
 }
 
+int moe_router_route(const moe_desc* d, const moe_route_desc* r, int32_t T, const void* x, const void* router_w,
+                     const float* bias, int32_t* topk_ids, float* topk_w, void* workspace, size_t ws_bytes,
+                     void* stream) {
+  moe::MarkScope marks;
+  int rc;
+  if ((rc = check_desc(d)) || (rc = moe::check_route(r)) || (rc = check_T(T))) return rc;
+  if (r->n_experts != d->n_experts || r->top_k != d->top_k)
+    return fail(MOE_EINVAL, "the routing's n_experts=%d, top_k=%d differ from the layer's %d, %d", r->n_experts,
+                r->top_k, d->n_experts, d->top_k);
+  if (r->logit_dtype != MOE_F32) return fail(MOE_EINVAL, "logit_dtype must be MOE_F32: the router's logits are fp32");
+  if (!x || !router_w) return fail(MOE_EINVAL, "NULL x or router_w");
+  if (!aligned(x, 16) || !aligned(router_w, 16)) return fail(MOE_EINVAL, "x and router_w must be 16-byte aligned");
+  if ((rc = moe::check_route_out(r, T, bias, topk_ids, topk_w))) return rc;
+  moe::WsLayout L;
+  if ((rc = check_ws(*d, T, workspace, ws_bytes, &L))) return rc;
+  // the outputs are written while other tokens' logits are still read
+  const size_t n_o = static_cast<size_t>(T) * d->top_k * 4;
+  if (overlaps(topk_ids, n_o, workspace, L.total) || overlaps(topk_w, n_o, workspace, L.total))
+    return fail(MOE_EINVAL, "topk_ids or topk_w overlaps the workspace");
+  if (T == 0) return ok();
+  moe::Call c{};
+  c.d = *d;
+  c.T = T;
+  c.x = x;
+  c.router_w = router_w;
+  c.ws = static_cast<uint8_t*>(workspace);
+  c.L = L;
+  c.stream = static_cast<hipStream_t>(stream);
+  rc = moe::prefill_supported(*d, T) ? moe::launch_prefill_logits(c) : moe::launch_router_logits(c);
+  if (rc != MOE_OK) return finish(rc);
+  return moe::route_forward(r, T, c.ws + L.logits, d->n_experts, bias, topk_ids, topk_w, c.stream);
+}
+
 int moe_experts_forward(const moe_desc* d, int32_t T, const void* x, const int32_t* topk_ids, const float* topk_w,
                         const int64_t* slot_table, const void* pool_base, const void* shared_w, void* out,
                         void* workspace, size_t ws_bytes, void* stream) {
-  MarkScope marks;
+  moe::MarkScope marks;
   int rc;
   if ((rc = check_desc(d)) || (rc = check_T(T))) return rc;
   if (!x || !topk_ids || !topk_w || !slot_table || !pool_base || !shared_w || !out)
@@ -305,7 +333,7 @@ static int layer_forward(const moe_desc* d, int32_t T, const void* x, const void
                          const int64_t* slot_table, const void* pool_base, const void* shared_w, void* out,
                          void* workspace, size_t ws_bytes, int32_t* topk_ids, float* topk_w, void* stream,
                          bool allow_fused, void* x_next = nullptr) {
-  MarkScope marks;
+  moe::MarkScope marks;
   int rc;
   if ((rc = check_desc(d)) || (rc = check_T(T))) return rc;
   if (!x || !router_w || !slot_table || !pool_base || !shared_w || !out)
@@ -387,7 +415,7 @@ int moe_stack_forward(const moe_desc* d, int32_t n_layers, int32_t T, const void
                       const void* pool_base, const void* shared_w, int64_t shared_stride, void* out,
                       int64_t out_stride, void* x_chain, int64_t chain_stride, int32_t* topk_ids, float* topk_w,
                       void* workspace, size_t ws_bytes, void* stream) {
-  MarkScope marks;
+  moe::MarkScope marks;
   int rc;
   if ((rc = check_desc(d)) || (rc = check_T(T))) return rc;
   if (n_layers < 0 || n_layers > 4096) return fail(MOE_EINVAL, "n_layers=%d must be in [0, 4096]", n_layers);
@@ -544,7 +572,7 @@ int moe_layer_forward_noalloc(const moe_desc* d, int32_t T, const void* x, const
 int moe_layer_forward_scalar(const moe_desc* d, int32_t T, const void* x, const void* router_w,
                              const int64_t* slot_table, const void* pool_base, const void* shared_w, void* out,
                              void* workspace, size_t ws_bytes, int32_t* topk_ids, float* topk_w, void* stream) {
-  MarkScope marks;
+  moe::MarkScope marks;
   int rc;
   if ((rc = check_desc(d)) || (rc = check_T(T))) return rc;
   if (!x || !router_w || !slot_table || !pool_base || !shared_w || !out)

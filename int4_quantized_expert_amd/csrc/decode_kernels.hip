@@ -633,11 +633,9 @@ int launch_ws_init(uint8_t* ws, size_t bytes, hipStream_t stream) {
   return last_launch_error();
 }
 
-int launch_router_topk(const Call& c, int32_t* ids2, float* wts2) {
+int launch_router_logits(const Call& c) {
   const moe_desc& d = c.d;
   float* logits = reinterpret_cast<float*>(c.ws + c.L.logits);
-  int32_t* ids = reinterpret_cast<int32_t*>(c.ws + c.L.ids);
-  float* wts = reinterpret_cast<float*>(c.ws + c.L.wts);
   const int spr = d.hidden / kSegCodes;
   const int rpp = spr >= kWave ? 1 : kWave / spr;
   const int nsl = spr > kWave ? spr / kWave : 1;
@@ -648,7 +646,14 @@ int launch_router_topk(const Call& c, int32_t* ids2, float* wts2) {
   (void)nsl;
   if (d.act_dtype == kF32) ROUTER(kF32, 1); else ROUTER(kBF16, 1);
 #undef ROUTER
-  return launch_topk(c, logits, ids, wts, ids2, wts2);
+  return last_launch_error();
+}
+
+int launch_router_topk(const Call& c, int32_t* ids2, float* wts2) {
+  const int rc = launch_router_logits(c);
+  if (rc != MOE_OK) return rc;
+  return launch_topk(c, reinterpret_cast<float*>(c.ws + c.L.logits), reinterpret_cast<int32_t*>(c.ws + c.L.ids),
+                     reinterpret_cast<float*>(c.ws + c.L.wts), ids2, wts2);
 }
 
 int launch_topk(const Call& c, const float* logits, int32_t* ids, float* wts, int32_t* ids2, float* wts2) {

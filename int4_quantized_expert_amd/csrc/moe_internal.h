@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "moe_layer.h"
+#include "moe_route.h"
 #include "fused_common.h"
 
 namespace moe {
@@ -132,6 +133,13 @@ struct Call {
   hipStream_t stream;
 };
 
+// Scope of one API call that may consume the timing events: the destructor
+// publishes the count and clears the setting when the call ends, whichever
+// way it ends.
+struct MarkScope {
+  ~MarkScope();
+};
+
 // Takes the next pair of caller-supplied timing events (moe_set_launch_events)
 // for the kernel about to launch; false when none is armed.
 bool next_launch_events(hipEvent_t* start, hipEvent_t* stop);
@@ -149,6 +157,7 @@ inline void launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, uint3
     hipLaunchKernelGGL(kernel, grid, block, lds, s, static_cast<KArgs>(args)...);
 }
 
+int launch_router_logits(const Call& c);     // fp32 router logits into the workspace
 int launch_router_topk(const Call& c, int32_t* ids_dst, float* wts_dst);
 int launch_experts(const Call& c);
 // Pieces of the staged path the prefill path shares: per-token top-k of given
@@ -162,8 +171,15 @@ int launch_scalar(const Call& c);
 int launch_take_flags(uint32_t* flags, uint32_t* status, hipStream_t stream);
 int launch_residual(int act_dtype, const void* x, const float* y, void* x_next, int64_t n, hipStream_t stream);
 
+// Routing from scores (route.hip): descriptor and output checks, the launch.
+int check_route(const moe_route_desc* r);
+int check_route_out(const moe_route_desc* r, int32_t T, const float* bias, const int32_t* ids, const float* w);
+int route_forward(const moe_route_desc* r, int32_t T, const void* logits, int64_t stride, const float* bias,
+                  int32_t* ids, float* w, hipStream_t s);
+
 // Prefill path (many tokens): MFMA router and grouped expert GEMMs.
 bool prefill_supported(const moe_desc& d, int T);
+int launch_prefill_logits(const Call& c);
 int launch_prefill_router(const Call& c, int32_t* ids_dst, float* wts_dst);
 int launch_prefill_experts(const Call& c);
 

@@ -1,0 +1,86 @@
+// Device helpers of the microscaled 4-bit format (include/mxfp4.h).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.h"
+
+namespace moe {
+
+constexpr int kMxBlock = 32;    // values that share a scale
+constexpr int kMxPad = 256;     // columns a row is padded to: 128 bytes of codes
+
+__host__ __device__ inline int64_t mx_padded(int64_t cols) { return (cols + kMxPad - 1) / kMxPad * kMxPad; }
+
+// Scale byte of a block from the bits of its largest magnitude: the exponent
+// field less that of 4 (E2M1's largest power of two), at least 0 (2^-127);
+// 255 for a block with an infinity or a NaN.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t mag_bits) {
+  const uint32_t f = mag_bits >> 23;
+  return f >= 255u ? 255u : (f > 2u ? f - 2u : 0u);
+}
+
+// The power of two that a scale byte stands for (NaN for 255).  2^-127 is a
+// subnormal fp32 number.
+__device__ __forceinline__ float mx_scale_f32(uint32_t byte) {
+  return __uint_as_float(byte == 0u ? 0x00400000u : (byte == 255u ? 0x7fc00000u : byte << 23));
+}
+
+// Eight values over the block's power of two as eight codes, the first in the
+// lowest four bits.  The conversion divides by the power exactly, rounds to
+// nearest with ties to even and saturates at 6 (checked against the formula
+// over all exponents); a block of scale byte 255 gets zero codes.
+__device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], uint32_t byte) {
+  const float s = mx_scale_f32(byte);
+  uint32_t c = 0;
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], s, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], s, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], s, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], s, 3);
+  return byte == 255u ? 0u : c;
+}
+
+// Eight values from element c of a row of `cols`; zeros past its end.  The
+// row's start is aligned to the element only.
+template <int DT>
+__device__ __forceinline__ void mx_load8(const void* base, int64_t row, int64_t c, int64_t cols, float (&v)[8]) {
+  if constexpr (DT == kF32) {
+    const float* p = static_cast<const float*>(base) + row;
+    if (c + 8 <= cols) {
+      uint32_t w[8];
+      __builtin_memcpy(w, p + c, 32);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? p[c + i] : 0.f;
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + row;
+    if (c + 8 <= cols) {
+      uint32_t w[4];
+      __builtin_memcpy(w, p + c, 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? bf16_to_f32(p[c + i]) : 0.f;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t mx_mag8(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;   // as whole numbers NaN > inf > any number
+    m = b > m ? b : m;
+  }
+  return m;
+}
+
+}  // namespace moe

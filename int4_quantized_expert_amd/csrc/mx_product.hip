@@ -1,0 +1,584 @@
+// Products of microscaled 4-bit matrices, dense and by routed expert
+// (include/mxfp4.h).
+//
+// Mathematics.  v_mfma_scale_f32_16x16x128 multiplies 16 rows of W with 16
+// rows of A over 128 values of k and scales every 32 of them by the two rows'
+// powers of two.  Lane l holds 32 values (16 bytes) of row l mod 16 and their
+// scale; which 32 of the 128 is free as long as both operands agree.  A chunk
+// of 256 values (128 bytes of a row) is two such products: quarter l / 16
+// holds values 64 q .. 64 q + 63 of the chunk, 32 in each product, so that a
+// lane's 32 bytes and its two scale bytes are contiguous.  With W as the first
+// operand a lane's four results are four consecutive outputs of one row of A.
+#include <hip/hip_runtime.h>
+
+#include <cstdio>
+
+#include "mx_common.h"
+#include "mx_internal.h"
+#include "topk_wave.h"
+
+namespace moe {
+namespace {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+constexpr int kMxF4 = 2;                 // a_dtype code MX_FP4
+constexpr int kChunk = kMxPad;           // k values per step
+constexpr int kNarrowWaves = 8;
+constexpr int kDirectPairs = 128;        // pairs that the kernels group by themselves
+constexpr int kTileRows = 16;            // rows of A per tile of the grouped path
+
+enum Mode { kDense, kDirect, kTiles, kSum };
+
+// A tile of the grouped path: up to kTileRows pairs of one expert.
+struct MxTile {
+  int64_t off;    // the expert's blob in the pool; -1: unusable, the rows are zero
+  int32_t first;  // place of its first pair in the list
+  int32_t count;
+};
+
+struct MxArgs {
+  const void* a;
+  const uint8_t* as;
+  const uint8_t* wc;        // dense
+  const uint8_t* wsc;
+  const int64_t* slots;     // by expert
+  const uint8_t* pool;
+  int64_t codes_off, scales_off, need, pool_bytes;
+  const int32_t* ids;
+  const float* wts;
+  void* out;
+  uint32_t* flags;
+  const int32_t* plist;
+  const MxTile* tiles;
+  const int32_t* ntiles;
+  int M;                    // rows of A (dense), pairs
+  int N, K, chunks;
+  int nblk;                 // blocks along N; the grid is flat, these fastest
+  int T, k, E, pair_rows, out_bf16;
+};
+
+// The blob offset of expert e, -1 if the id or the slot is unusable.
+__device__ __forceinline__ int64_t blob_of(const int64_t* slots, int e, int E, int64_t need, int64_t pool_bytes) {
+  if (e < 0 || e >= E) return -1;
+  const int64_t off = slots[e];
+  return (off >= 0 && (off & 255) == 0 && off <= pool_bytes - need) ? off : -1;
+}
+
+__device__ __forceinline__ v4f mfma4(v4i a, v4i b, v4f c, int sa, int sb, int s) {
+  const v8i A = {a[0], a[1], a[2], a[3], 0, 0, 0, 0}, B = {b[0], b[1], b[2], b[3], 0, 0, 0, 0};
+  return s == 0 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, 0, sa, 0, sb)
+                : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, 1, sa, 1, sb);
+}
+
+// A lane's part of a row's chunk: two blocks of codes and their scale bytes
+// (in the low half of `sc`).
+struct Part {
+  v4i c[2];
+  int sc;
+};
+
+template <int SRC>
+__device__ __forceinline__ void load_part(const void* a, const uint8_t* as, int64_t row, bool on, int chunk, int q, int K,
+                                          int chunks, Part& p) {
+  if (!on) {
+    p.c[0] = p.c[1] = v4i{0, 0, 0, 0};
+    p.sc = 0;
+    return;
+  }
+  if constexpr (SRC == kMxF4) {
+    const v4i* c = reinterpret_cast<const v4i*>(static_cast<const uint8_t*>(a) + (row * chunks + chunk) * 128 + q * 32);
+    p.c[0] = c[0];
+    p.c[1] = c[1];
+    p.sc = *reinterpret_cast<const uint16_t*>(as + (row * chunks + chunk) * 8 + q * 2);
+  } else {
+    int sc = 0;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      float v[4][8];
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        mx_load8<SRC>(a, row * K, static_cast<int64_t>(chunk) * kChunk + q * 64 + b * 32 + i * 8, K, v[i]);
+        const uint32_t o = mx_mag8(v[i]);
+        m = o > m ? o : m;
+      }
+      const uint32_t byte = mx_scale_byte(m);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p.c[b][i] = static_cast<int>(mx_codes8(v[i], byte));
+      sc |= static_cast<int>(byte) << (8 * b);
+    }
+    p.sc = sc;
+  }
+}
+
+__device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
+
+__device__ __forceinline__ void store_out(void* out, int64_t i, float y, int bf16) {
+  if (bf16) static_cast<uint16_t*>(out)[i] = f32_to_bf16(y);
+  else static_cast<float*>(out)[i] = y;
+}
+
+// Few rows of A: a block forms 16 outputs of up to 16 rows (kSum: of one
+// token), its waves take the chunks of k in turn and their sums are joined in
+// LDS.  Bound by the reads of W; A is read (and quantised) by every block.
+//   kDense   rows 16 y .. of A
+//   kDirect  y is a pair; the block of the first pair of an expert
+//            takes all of that expert's pairs, the others end
+//   kTiles   y is a tile of the grouped list
+//   kSum     y is a token; its experts' products are summed with their weights
+template <int SRC, int ACT, int MODE>
+__global__ __launch_bounds__(kNarrowWaves* kWave) void k_mx_narrow(MxArgs a) {
+  constexpr int NM = ACT == MX_ACT_SWIGLU ? 2 : 1;
+  __shared__ __align__(16) float red[NM][kNarrowWaves][16][20];   // 20: four-float stores, fewer bank conflicts
+  __shared__ int32_t list[kDirectPairs];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int r = lane & 15, q = lane >> 4;
+  const int y = blockIdx.x / a.nblk, bx = blockIdx.x % a.nblk;
+  const int n0 = bx * 16;
+  const int wrow = n0 + r < a.N ? n0 + r : a.N - 1;   // a row past the end is read again and not stored
+
+  // where the rows come from, and where they go
+  int count = 0;
+  int64_t off = 0;
+  const int32_t* pairs = nullptr;
+  if constexpr (MODE == kDense) {
+    count = a.M - y * 16;
+    count = count < 16 ? count : 16;
+  } else if constexpr (MODE == kDirect) {
+    const int p = y, e = a.ids[p];
+    const uint64_t b0 = __ballot(lane < a.M && a.ids[lane < a.M ? lane : 0] == e);
+    const uint64_t b1 = __ballot(lane + kWave < a.M && a.ids[lane + kWave < a.M ? lane + kWave : 0] == e);
+    const int first = b0 ? __ffsll(static_cast<unsigned long long>(b0)) - 1 : kWave + __ffsll(static_cast<unsigned long long>(b1)) - 1;
+    if (first != p) return;
+    count = __popcll(b0) + __popcll(b1);
+    if (wave == 0) {
+      if ((b0 >> lane) & 1ull) list[__popcll(b0 & lane_mask_lt(lane))] = lane;
+      if ((b1 >> lane) & 1ull) list[__popcll(b0) + __popcll(b1 & lane_mask_lt(lane))] = lane + kWave;
+    }
+    __syncthreads();
+    pairs = list;
+    off = blob_of(a.slots, e, a.E, a.need, a.pool_bytes);
+    if (off < 0 && tid == 0 && bx == 0) atomicOr(a.flags, 1u);
+  } else if constexpr (MODE == kTiles) {
+    if (y >= *a.ntiles) return;
+    const MxTile t = a.tiles[y];
+    count = t.count;
+    off = t.off;
+    pairs = a.plist + t.first;
+  } else {
+    count = 1;
+  }
+
+  for (int g0 = 0; g0 < (MODE == kDirect ? count : 1); g0 += 16) {
+    const int here = MODE == kDirect ? (count - g0 < 16 ? count - g0 : 16) : count;
+    const bool on = r < here;
+    int64_t row = 0, dst = 0;
+    if constexpr (MODE == kDense) {
+      row = dst = static_cast<int64_t>(y) * 16 + r;
+    } else if constexpr (MODE == kDirect || MODE == kTiles) {
+      const int p = on ? pairs[g0 + r] : 0;
+      row = a.pair_rows ? p : p / a.k;
+      dst = p;
+    }
+    v4f acc[NM];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) acc[m] = v4f{0.f, 0.f, 0.f, 0.f};
+    const int tasks = MODE == kSum ? a.k * a.chunks : a.chunks;
+    if (off >= 0) {
+      for (int task = wave; task < tasks; task += kNarrowWaves) {
+        int chunk = task;
+        const uint8_t *wc = a.wc, *wsc = a.wsc;
+        float w = 1.f;
+        if constexpr (MODE == kSum) {
+          const int i = task / a.chunks;
+          chunk = task - i * a.chunks;
+          const int t = y;
+          const int e = a.ids[t * a.k + i];
+          const int64_t o = blob_of(a.slots, e, a.E, a.need, a.pool_bytes);
+          if (o < 0) {
+            if (lane == 0 && bx == 0) atomicOr(a.flags, 1u);
+            continue;
+          }
+          w = a.wts[t * a.k + i];
+          row = a.pair_rows ? t * a.k + i : t;
+          wc = a.pool + o + a.codes_off;
+          wsc = a.pool + o + a.scales_off;
+        } else if constexpr (MODE != kDense) {
+          wc = a.pool + off + a.codes_off;
+          wsc = a.pool + off + a.scales_off;
+        }
+        Part A, W[NM];
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+          load_part<kMxF4>(wc, wsc, wrow + m * static_cast<int64_t>(a.N), true, chunk, q, a.K, a.chunks, W[m]);
+        load_part<SRC>(a.a, a.as, row, on, chunk, q, a.K, a.chunks, A);
+        v4f d[NM];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+          d[m] = MODE == kSum ? v4f{0.f, 0.f, 0.f, 0.f} : acc[m];
+          d[m] = mfma4(W[m].c[0], A.c[0], d[m], W[m].sc, A.sc, 0);
+          d[m] = mfma4(W[m].c[1], A.c[1], d[m], W[m].sc, A.sc, 1);
+          if constexpr (MODE == kSum) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][i] = fmaf(w, d[m][i], acc[m][i]);
+          } else {
+            acc[m] = d[m];
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < NM; ++m) *reinterpret_cast<v4f*>(&red[m][wave][r][4 * q]) = acc[m];
+    __syncthreads();
+    if (tid < 256) {
+      const int tr = tid >> 4, n = tid & 15;
+      if (tr < here && n0 + n < a.N) {
+        float v[NM];
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+          v[m] = 0.f;
+#pragma unroll
+          for (int w = 0; w < kNarrowWaves; ++w) v[m] += red[m][w][tr][n];
+        }
+        int64_t to;
+        if constexpr (MODE == kDense) to = static_cast<int64_t>(y) * 16 + tr;
+        else if constexpr (MODE == kSum) to = y;
+        else to = pairs[g0 + tr];
+        store_out(a.out, to * a.N + n0 + n, NM == 2 ? silu(v[0]) * v[NM - 1] : v[0], a.out_bf16);
+      }
+    }
+    if (MODE == kDirect) __syncthreads();
+  }
+}
+
+// Pairs grouped by expert: one block counts, scans and places.  The order of
+// an expert's pairs does not change any result (every pair has its own column
+// of the product), so LDS atomics may hand out the places.
+constexpr int kGroupThr = 1024;
+
+__global__ __launch_bounds__(kGroupThr) void k_mx_group(MxArgs a, int P, int32_t* place, int32_t* plist, MxTile* tiles,
+                                                        int32_t* ntiles) {
+  __shared__ int32_t cnt[kMaxExperts + 1];       // the last: pairs whose id is unusable
+  __shared__ int32_t sum_p[kGroupThr / kWave], sum_t[kGroupThr / kWave];
+  __shared__ int32_t start[kMaxExperts + 1];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  for (int e = tid; e <= a.E; e += kGroupThr) cnt[e] = 0;
+  __syncthreads();
+  for (int p = tid; p < P; p += kGroupThr) {
+    const int id = a.ids[p];
+    place[p] = atomicAdd(&cnt[(id >= 0 && id < a.E) ? id : a.E], 1);
+  }
+  __syncthreads();
+  // exclusive scans of the pair and tile counts; the bucket of unusable ids
+  // (index E <= 1024, one past the threads at most) comes last
+  const int c = tid < a.E ? cnt[tid] : 0;
+  const int nt = (c + kTileRows - 1) / kTileRows;
+  int ip = c, it = nt;
+  for (int s = 1; s < kWave; s <<= 1) {
+    const int op = __shfl_up(ip, s), ot = __shfl_up(it, s);
+    if (lane >= s) { ip += op; it += ot; }
+  }
+  if (lane == kWave - 1) { sum_p[wave] = ip; sum_t[wave] = it; }
+  __syncthreads();
+  int bp = 0, bt = 0, tp = 0, tt = 0;
+  for (int w = 0; w < kGroupThr / kWave; ++w) {
+    if (w < wave) { bp += sum_p[w]; bt += sum_t[w]; }
+    tp += sum_p[w];
+    tt += sum_t[w];
+  }
+  const int sp = bp + ip - c, st = bt + it - nt;
+  if (tid < a.E) start[tid] = sp;
+  if (c > 0) {
+    const int64_t off = blob_of(a.slots, tid, a.E, a.need, a.pool_bytes);
+    if (off < 0) atomicOr(a.flags, 1u);
+    for (int i = 0; i < nt; ++i) {
+      const int left = c - i * kTileRows;
+      tiles[st + i] = MxTile{off, sp + i * kTileRows, left < kTileRows ? left : kTileRows};
+    }
+  }
+  const int lost = cnt[a.E], lost_t = (lost + kTileRows - 1) / kTileRows;
+  for (int i = tid; i < lost_t; i += kGroupThr) {
+    const int left = lost - i * kTileRows;
+    tiles[tt + i] = MxTile{-1, tp + i * kTileRows, left < kTileRows ? left : kTileRows};
+  }
+  if (tid == 0) {
+    *ntiles = tt + lost_t;
+    start[a.E] = tp;
+    if (lost) atomicOr(a.flags, 1u);
+  }
+  __syncthreads();
+  for (int p = tid; p < P; p += kGroupThr) {
+    const int id = a.ids[p];
+    plist[start[(id >= 0 && id < a.E) ? id : a.E] + place[p]] = p;
+  }
+}
+
+// out[t] = sum_i w[t, i] rows[t k + i], i ascending.
+__global__ __launch_bounds__(256) void k_mx_combine(const float* rows, const float* wts, int k, int N, void* out,
+                                                    int bf16) {
+  const int nblk = (N + 255) / 256;
+  const int64_t t = blockIdx.x / nblk;
+  const int n = (blockIdx.x % nblk) * 256 + threadIdx.x;
+  if (n >= N) return;
+  float y = 0.f;
+  for (int i = 0; i < k; ++i) y = fmaf(wts[t * k + i], rows[(t * k + i) * N + n], y);
+  store_out(out, t * N + n, y, bf16);
+}
+
+// ---------------------------------------------------------------------------
+
+int bad(const char* fmt, long long x = 0, long long y = 0) {
+  char buf[256];
+  snprintf(buf, sizeof(buf), fmt, x, y);
+  return api_fail(MOE_EINVAL, buf);
+}
+
+bool at(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int check_product(const mx_product_desc* d, bool experts) {
+  if (!d) return bad("product descriptor is NULL");
+  if (d->n < 1 || d->n > (1 << 20) || d->k < 1 || d->k > (1 << 20)) return bad("n=%lld and k=%lld must be in [1, 2^20]", d->n, d->k);
+  if (d->a_dtype != MOE_F32 && d->a_dtype != MOE_BF16 && d->a_dtype != MX_FP4)
+    return bad("a_dtype=%lld is not MOE_F32, MOE_BF16 or MX_FP4", d->a_dtype);
+  if (d->out_dtype != MOE_F32 && d->out_dtype != MOE_BF16) return bad("out_dtype=%lld is neither MOE_F32 nor MOE_BF16", d->out_dtype);
+  if (d->act != MX_ACT_NONE && d->act != MX_ACT_SWIGLU) return bad("act=%lld is not a MX_ACT_* code", d->act);
+  if (!experts) {
+    if (d->n_experts || d->top_k || d->pair_rows || d->codes_off || d->scales_off || d->pool_bytes)
+      return bad("the fields of a product by expert must be 0 for a dense one");
+    return MOE_OK;
+  }
+  if (d->n_experts < 1 || d->n_experts > kMaxExperts) return bad("n_experts=%lld must be in [1, 1024]", d->n_experts);
+  if (d->top_k < 1 || d->top_k > 64) return bad("top_k=%lld must be in [1, 64]", d->top_k);
+  if (d->pair_rows != 0 && d->pair_rows != 1) return bad("pair_rows=%lld must be 0 or 1", d->pair_rows);
+  if (d->codes_off < 0 || d->codes_off % 16 || d->scales_off < 0 || d->scales_off % 16 || d->codes_off > (int64_t(1) << 40) ||
+      d->scales_off > (int64_t(1) << 40))
+    return bad("codes_off=%lld and scales_off=%lld must be multiples of 16 in [0, 2^40]", d->codes_off, d->scales_off);
+  const int64_t rows = static_cast<int64_t>(d->n) * (d->act == MX_ACT_SWIGLU ? 2 : 1);
+  const int64_t nc = mx_codes_bytes(rows, d->k), ns = mx_scales_bytes(rows, d->k);
+  if (d->codes_off < d->scales_off + ns && d->scales_off < d->codes_off + nc) return bad("a blob's codes and scales overlap");
+  if (d->pool_bytes < d->codes_off + nc || d->pool_bytes < d->scales_off + ns)
+    return bad("pool_bytes=%lld is smaller than one blob", d->pool_bytes);
+  return MOE_OK;
+}
+
+int check_rows(const mx_product_desc& d, int32_t T, bool experts) {
+  if (T < 0 || T > (experts ? 65536 : (1 << 20))) return bad("%lld rows are negative or too many", T);
+  if (static_cast<int64_t>(T) * (experts ? d.top_k : 1) * ((d.n + 15) / 16) >= (int64_t(1) << 31))
+    return bad("%lld rows of %lld columns are too many for one launch", static_cast<long long>(T) * (experts ? d.top_k : 1), d.n);
+  if (experts && static_cast<int64_t>(T) * d.top_k >= (1 << 22)) return bad("T * top_k = %lld must be below 2^22", static_cast<long long>(T) * d.top_k);
+  return MOE_OK;
+}
+
+struct MxWs {
+  size_t codes, scales;      // A as an MX matrix
+  size_t place, plist, tiles, ntiles;
+  size_t rows;               // fp32 rows of the pairs
+  size_t total;
+  int max_tiles;
+};
+
+// The regions lie behind those at fixed offsets that moe_layer.h's calls keep
+// across calls (control words, tagged words), so that one workspace serves both.
+MxWs mx_ws(const mx_product_desc& d, int32_t T, bool experts) {
+  MxWs w{};
+  moe_desc any{};
+  any.hidden = any.inter = any.shared_inter = 64;
+  any.n_experts = any.top_k = 1;
+  size_t o = ws_layout(any, 0).logits;
+  auto take = [&](size_t bytes) { const size_t p = o; o += align256(bytes > 0 ? bytes : 1); return p; };
+  const int64_t P = static_cast<int64_t>(T) * (experts ? d.top_k : 1);
+  const int64_t rows = experts && !d.pair_rows ? T : P;
+  const bool quant = d.a_dtype != MX_FP4;
+  w.codes = take(quant ? mx_codes_bytes(rows, d.k) : 0);
+  w.scales = take(quant ? mx_scales_bytes(rows, d.k) : 0);
+  if (experts) {
+    w.place = take(P * 4);
+    w.plist = take(P * 4);
+    w.max_tiles = static_cast<int>((P < d.n_experts + 1 ? P : d.n_experts + 1) + P / kTileRows);
+    w.tiles = take(static_cast<size_t>(w.max_tiles) * sizeof(MxTile));
+    w.ntiles = take(4);
+    w.rows = take(static_cast<size_t>(P) * d.n * 4);
+  }
+  w.total = o;
+  return w;
+}
+
+int check_call(const mx_product_desc& d, const void* a, const void* as, int64_t rows, const void* out, int64_t out_rows,
+               const void* ws, size_t ws_bytes, const MxWs& L) {
+  if (!a || !out) return bad("NULL a or out");
+  if (d.a_dtype == MX_FP4) {
+    if (!as) return bad("a_scales is NULL");
+    if (!at(a, 16) || !at(as, 16)) return bad("codes and scales must be 16-byte aligned");
+  } else {
+    if (as) return bad("a_scales must be NULL unless a_dtype is MX_FP4");
+    if (!at(a, d.a_dtype == MOE_F32 ? 4 : 2)) return bad("a is not aligned to its element");
+  }
+  if (!at(out, d.out_dtype == MOE_F32 ? 4 : 2)) return bad("out is not aligned to its element");
+  if (!ws || !at(ws, 256)) return bad("workspace is NULL or not 256-byte aligned");
+  if (ws_bytes < L.total) {
+    char buf[160];
+    snprintf(buf, sizeof(buf), "workspace has %zu bytes, %zu needed", ws_bytes, L.total);
+    return api_fail(MOE_ENOMEM, buf);
+  }
+  const int64_t n_a = d.a_dtype == MX_FP4 ? mx_codes_bytes(rows, d.k) : rows * d.k * (d.a_dtype == MOE_F32 ? 4 : 2);
+  const int64_t n_as = d.a_dtype == MX_FP4 ? mx_scales_bytes(rows, d.k) : 0;
+  const int64_t n_o = out_rows * d.n * (d.out_dtype == MOE_F32 ? 4 : 2);
+  if (mx_overlaps(out, n_o, a, n_a) || mx_overlaps(out, n_o, as, n_as) || mx_overlaps(out, n_o, ws, ws_bytes) ||
+      mx_overlaps(a, n_a, ws, ws_bytes) || mx_overlaps(as, n_as, ws, ws_bytes))
+    return bad("out or the workspace overlaps another argument");
+  return MOE_OK;
+}
+
+int launched() {
+  const hipError_t e = hipGetLastError();
+  if (e == hipSuccess) return api_ok();
+  char buf[256];
+  snprintf(buf, sizeof(buf), "product launch failed: %s", hipGetErrorString(e));
+  return api_fail(MOE_EHIP, buf);
+}
+
+template <int SRC, int MODE>
+void narrow_act(const MxArgs& a, int act, dim3 grid, hipStream_t s) {
+  const dim3 block(kNarrowWaves * kWave);
+  if (act == MX_ACT_SWIGLU) launch_kernel(k_mx_narrow<SRC, MX_ACT_SWIGLU, MODE>, grid, block, 0, s, a);
+  else launch_kernel(k_mx_narrow<SRC, MX_ACT_NONE, MODE>, grid, block, 0, s, a);
+}
+
+template <int MODE>
+void narrow(MxArgs a, int src, int act, int ny, hipStream_t s) {
+  a.nblk = (a.N + 15) / 16;
+  const dim3 grid(static_cast<uint32_t>(a.nblk) * ny);
+  if (src == kF32) narrow_act<kF32, MODE>(a, act, grid, s);
+  else if (src == kBF16) narrow_act<kBF16, MODE>(a, act, grid, s);
+  else narrow_act<kMxF4, MODE>(a, act, grid, s);
+}
+
+MxArgs common_args(const mx_product_desc& d, const void* a, const void* as, void* out, void* ws) {
+  MxArgs g{};
+  g.a = a;
+  g.as = static_cast<const uint8_t*>(as);
+  g.out = out;
+  g.flags = static_cast<uint32_t*>(ws);
+  g.N = d.n;
+  g.K = d.k;
+  g.chunks = static_cast<int>(mx_padded(d.k) / kChunk);
+  g.out_bf16 = d.out_dtype == MOE_BF16;
+  return g;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+size_t mx_workspace_bytes(const mx_product_desc* d, int32_t T_max) {
+  using namespace moe;
+  const bool experts = d && d->n_experts != 0;
+  if (check_product(d, experts) != MOE_OK || check_rows(*d, T_max, experts) != MOE_OK) return 0;
+  return mx_ws(*d, T_max, experts).total;
+}
+
+int mx_linear_forward(const mx_product_desc* d, int32_t M, const void* a, const void* a_scales, const void* w_codes,
+                      const void* w_scales, void* out, void* workspace, size_t ws_bytes, void* stream) {
+  using namespace moe;
+  MarkScope marks;
+  int rc;
+  if ((rc = check_product(d, false)) || (rc = check_rows(*d, M, false))) return rc;
+  if (M == 0) return api_ok();
+  const MxWs L = mx_ws(*d, M, false);
+  if ((rc = check_call(*d, a, a_scales, M, out, M, workspace, ws_bytes, L))) return rc;
+  if (!w_codes || !w_scales || !at(w_codes, 16) || !at(w_scales, 16)) return bad("w_codes and w_scales must be 16-byte aligned and not NULL");
+  const int64_t wrows = static_cast<int64_t>(d->n) * (d->act == MX_ACT_SWIGLU ? 2 : 1);
+  const int64_t n_o = static_cast<int64_t>(M) * d->n * (d->out_dtype == MOE_F32 ? 4 : 2);
+  const int64_t n_c = mx_codes_bytes(wrows, d->k), n_s = mx_scales_bytes(wrows, d->k);
+  if (mx_overlaps(out, n_o, w_codes, n_c) || mx_overlaps(out, n_o, w_scales, n_s) ||
+      mx_overlaps(workspace, ws_bytes, w_codes, n_c) || mx_overlaps(workspace, ws_bytes, w_scales, n_s))
+    return bad("out or the workspace overlaps w_codes or w_scales");
+  MxArgs g = common_args(*d, a, a_scales, out, workspace);
+  g.M = M;
+  g.wc = static_cast<const uint8_t*>(w_codes);
+  g.wsc = static_cast<const uint8_t*>(w_scales);
+  narrow<kDense>(g, d->a_dtype, d->act, (M + 15) / 16, static_cast<hipStream_t>(stream));
+  return launched();
+}
+
+int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const void* a_scales,
+                       const int32_t* topk_ids, const float* topk_w, const int64_t* slot_table, const void* pool_base,
+                       void* out, void* workspace, size_t ws_bytes, void* stream) {
+  using namespace moe;
+  MarkScope marks;
+  int rc;
+  if ((rc = check_product(d, true)) || (rc = check_rows(*d, T, true))) return rc;
+  if (T == 0) return api_ok();
+  const MxWs L = mx_ws(*d, T, true);
+  const int P = T * d->top_k;
+  const int64_t rows = d->pair_rows ? P : T, out_rows = topk_w ? T : P;
+  if ((rc = check_call(*d, a, a_scales, rows, out, out_rows, workspace, ws_bytes, L))) return rc;
+  if (!topk_ids || !slot_table || !pool_base) return bad("NULL topk_ids, slot_table or pool_base");
+  if (!at(topk_ids, 4) || !at(topk_w, 4) || !at(slot_table, 8) || !at(pool_base, 256))
+    return bad("misaligned pointer (topk_ids/topk_w 4, slot_table 8, pool_base 256)");
+  const int64_t n_o = out_rows * d->n * (d->out_dtype == MOE_F32 ? 4 : 2), n_i = static_cast<int64_t>(P) * 4;
+  const int64_t n_t = static_cast<int64_t>(d->n_experts) * 8;
+  const void* ins[4] = {topk_ids, topk_w, slot_table, pool_base};
+  const int64_t in_n[4] = {n_i, n_i, n_t, d->pool_bytes};
+  for (int i = 0; i < 4; ++i)
+    if (mx_overlaps(out, n_o, ins[i], in_n[i]) || mx_overlaps(workspace, ws_bytes, ins[i], in_n[i]))
+      return bad("out or the workspace overlaps the routing, the slot table or the pool");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  MxArgs g = common_args(*d, a, a_scales, out, workspace);
+  const int64_t wrows = static_cast<int64_t>(d->n) * (d->act == MX_ACT_SWIGLU ? 2 : 1);
+  const int64_t end_c = d->codes_off + mx_codes_bytes(wrows, d->k), end_s = d->scales_off + mx_scales_bytes(wrows, d->k);
+  g.M = P;
+  g.T = T;
+  g.k = d->top_k;
+  g.E = d->n_experts;
+  g.pair_rows = d->pair_rows;
+  g.ids = topk_ids;
+  g.wts = topk_w;
+  g.slots = slot_table;
+  g.pool = static_cast<const uint8_t*>(pool_base);
+  g.codes_off = d->codes_off;
+  g.scales_off = d->scales_off;
+  g.need = end_c > end_s ? end_c : end_s;
+  g.pool_bytes = d->pool_bytes;
+  // a gated product is not linear in its sums, so the weighted sum of a token
+  // in one block is for the plain one
+  if (topk_w && T <= 8 && d->act == MX_ACT_NONE) {
+    narrow<kSum>(g, d->a_dtype, d->act, T, s);
+    return launched();
+  }
+  if (topk_w) {
+    g.out = ws + L.rows;
+    g.out_bf16 = 0;
+  }
+  if (P <= kDirectPairs) {
+    narrow<kDirect>(g, d->a_dtype, d->act, P, s);
+  } else {
+    int32_t* place = reinterpret_cast<int32_t*>(ws + L.place);
+    int32_t* plist = reinterpret_cast<int32_t*>(ws + L.plist);
+    MxTile* tiles = reinterpret_cast<MxTile*>(ws + L.tiles);
+    int32_t* ntiles = reinterpret_cast<int32_t*>(ws + L.ntiles);
+    launch_kernel(k_mx_group, dim3(1), dim3(kGroupThr), 0, s, g, P, place, plist, tiles, ntiles);
+    g.plist = plist;
+    g.tiles = tiles;
+    g.ntiles = ntiles;
+    int src = d->a_dtype;
+    if (src != MX_FP4) {
+      launch_mx_quantize(src, rows, d->k, a, d->k, ws + L.codes, ws + L.scales, s);
+      g.a = ws + L.codes;
+      g.as = ws + L.scales;
+      src = MX_FP4;
+    }
+    narrow<kTiles>(g, src, d->act, L.max_tiles, s);
+  }
+  if (topk_w)
+    launch_kernel(k_mx_combine, dim3(static_cast<uint32_t>((d->n + 255) / 256) * T), dim3(256), 0, s, reinterpret_cast<const float*>(ws + L.rows),
+                  topk_w, d->top_k, d->n, out, d->out_dtype == MOE_BF16);
+  return launched();
+}
+
+}  // extern "C"

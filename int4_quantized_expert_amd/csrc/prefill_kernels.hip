@@ -1168,17 +1168,21 @@ bool prefill_supported(const moe_desc& d, int T) {
 
 static int last_error() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP; }
 
-int launch_prefill_router(const Call& c, int32_t* ids2, float* wts2) {
+int launch_prefill_logits(const Call& c) {
   const moe_desc& d = c.d;
   float* logits = reinterpret_cast<float*>(c.ws + c.L.logits);
-  int32_t* ids = reinterpret_cast<int32_t*>(c.ws + c.L.ids);
-  float* wts = reinterpret_cast<float*>(c.ws + c.L.wts);
   const int nb = ((d.n_experts + 63) / 64) * ((c.T + 63) / 64);
   const dim3 grid(static_cast<unsigned>((nb + kXcds - 1) / kXcds * kXcds));
   launch_kernel(k_pf_router, grid, dim3(kThreads), 0, c.stream, static_cast<const uint16_t*>(c.x),
                 static_cast<const uint16_t*>(c.router_w), logits, c.T, d.hidden, d.n_experts);
-  if (last_error()) return MOE_EHIP;
-  return launch_topk(c, logits, ids, wts, ids2, wts2);
+  return last_error() ? MOE_EHIP : MOE_OK;
+}
+
+int launch_prefill_router(const Call& c, int32_t* ids2, float* wts2) {
+  const int rc = launch_prefill_logits(c);
+  if (rc != MOE_OK) return rc;
+  return launch_topk(c, reinterpret_cast<float*>(c.ws + c.L.logits), reinterpret_cast<int32_t*>(c.ws + c.L.ids),
+                     reinterpret_cast<float*>(c.ws + c.L.wts), ids2, wts2);
 }
 
 // Blocks for up to max_tiles tiles of n_rt row blocks, rounded up to a
