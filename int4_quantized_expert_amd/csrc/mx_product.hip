@@ -28,11 +28,10 @@ constexpr int kMxF4 = 2;                 // a_dtype code MX_FP4
 constexpr int kChunk = kMxPad;           // k values per step
 constexpr int kNarrowWaves = 8;
 constexpr int kDirectPairs = 128;        // pairs that the kernels group by themselves
-constexpr int kTileRows = 16;            // rows of A per tile of the grouped path
 
 enum Mode { kDense, kDirect, kTiles, kSum };
 
-// A tile of the grouped path: up to kTileRows pairs of one expert.
+// A tile of the grouped path: up to `tile` pairs of one expert.
 struct MxTile {
   int64_t off;    // the expert's blob in the pool; -1: unusable, the rows are zero
   int32_t first;  // place of its first pair in the list
@@ -55,6 +54,7 @@ struct MxArgs {
   const MxTile* tiles;
   const int32_t* ntiles;
   int M;                    // rows of A (dense), pairs
+  int arows;                // rows of A that exist
   int N, K, chunks;
   int nblk;                 // blocks along N; the grid is flat, these fastest
   int T, k, E, pair_rows, out_bf16;
@@ -254,12 +254,207 @@ __global__ __launch_bounds__(kNarrowWaves* kWave) void k_mx_narrow(MxArgs a) {
   }
 }
 
+// Many rows of A: a block forms BM rows of A x BN rows of W.  Both operands'
+// codes (128 bytes of a row per chunk) and scales (8 bytes) go to LDS with
+// direct loads, two chunks deep: while a chunk is multiplied the next one
+// arrives.  A row's eight 16-byte pieces are placed by piece ^ (row mod 8), so
+// that sixteen lanes reading one piece of sixteen rows hit different banks.
+//   rows of W past N and rows of A past M read as zeros (the buffer descriptors
+//   end there; a row's offset is in the lane's part of the address, which the
+//   bounds check compares with what the scalar part leaves) and are not stored; with SWIGLU the first half of a block's W
+//   rows are gate rows and the second half the up rows of the same outputs.
+template <int WM, int WN, int TM, int TN>
+struct TileCfg {
+  static constexpr int kWaves = WM * WN, kBM = WM * TM * 16, kBN = WN * TN * 16;
+  static constexpr int kCodes = (kBM + kBN) * 128, kScales = (kBM + kBN) * 8;
+  static constexpr int kStage = kCodes + kScales;
+  static constexpr size_t kLds = 2 * static_cast<size_t>(kStage);
+};
+
+__device__ __forceinline__ int64_t clamp32(int64_t n) { return n < 0xfffffff0ll ? n : 0xfffffff0ll; }
+
+template <int WM, int WN, int TM, int TN, int ACT, bool EXPERTS>
+__global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
+  using C = TileCfg<WM, WN, TM, TN>;
+  constexpr int NM = ACT == MX_ACT_SWIGLU ? 2 : 1;
+  constexpr int kCols = C::kBN / NM;                       // outputs of a block
+  constexpr int AI = C::kBM / 8, WI = C::kBN / 8;          // direct loads of codes per chunk: eight rows each
+  constexpr int AS = C::kBM / 32, WS = C::kBN / 32;        // of scales: 32 rows each
+  constexpr int PA = (AI + C::kWaves - 1) / C::kWaves, PW = (WI + C::kWaves - 1) / C::kWaves;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int r = lane & 15, q = lane >> 4;
+  const int wm = wave / WN, wn = wave % WN;
+  const int pitch = a.chunks * 128, spitch = a.chunks * 8;
+
+  // which tile: an XCD (blockIdx mod 8) runs a contiguous range of them, so
+  // that neighbours share rows through its L2
+  int mt, nb, count = 0;
+  int64_t blob = 0;
+  const int32_t* pairs = nullptr;
+  {
+    const int tiles = EXPERTS ? *a.ntiles : (a.M + C::kBM - 1) / C::kBM;
+    const int total = tiles * a.nblk, per = (total + 7) / 8;
+    const int idx = static_cast<int>(blockIdx.x & 7) * per + static_cast<int>(blockIdx.x >> 3);
+    if (static_cast<int>(blockIdx.x >> 3) >= per || idx >= total) return;
+    if constexpr (EXPERTS) {
+      mt = idx / a.nblk;
+      nb = idx % a.nblk;
+      const MxTile t = a.tiles[mt];
+      count = t.count;
+      blob = t.off;
+      pairs = a.plist + t.first;
+    } else {
+      // bands of eight row tiles, columns outermost inside a band
+      const int band = idx / (8 * a.nblk), in = idx % (8 * a.nblk);
+      const int high = tiles - band * 8 < 8 ? tiles - band * 8 : 8;
+      mt = band * 8 + in % high;
+      nb = in / high;
+      count = a.M - mt * C::kBM;
+    }
+  }
+  const int n0 = nb * kCols;
+  const int64_t m0 = static_cast<int64_t>(mt) * C::kBM;
+
+  v4f acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  if (blob >= 0) {
+    const uint8_t* wc = EXPERTS ? a.pool + blob + a.codes_off : a.wc;
+    const uint8_t* wsc = EXPERTS ? a.pool + blob + a.scales_off : a.wsc;
+    const int64_t left = a.N - n0;
+    u32x4 rw[NM], rws[NM];
+#pragma unroll
+    for (int m = 0; m < NM; ++m) {
+      const int64_t row = n0 + m * static_cast<int64_t>(a.N);
+      rw[m] = raw_rsrc(wc + row * pitch, clamp32(left * pitch));
+      rws[m] = raw_rsrc(wsc + row * spitch, clamp32(left * spitch));
+    }
+    const uint8_t* ab = static_cast<const uint8_t*>(a.a);
+    const u32x4 ra = EXPERTS ? raw_rsrc(ab, clamp32(static_cast<int64_t>(a.arows) * pitch))
+                             : raw_rsrc(ab + m0 * pitch, clamp32(static_cast<int64_t>(count) * pitch));
+    const u32x4 ras = EXPERTS ? raw_rsrc(a.as, clamp32(static_cast<int64_t>(a.arows) * spitch))
+                              : raw_rsrc(a.as + m0 * spitch, clamp32(static_cast<int64_t>(count) * spitch));
+    // a lane's place in a direct load: row lane / 8 of eight, piece lane mod 8;
+    // of scales: row lane / 2 of 32, word lane mod 2
+    const uint32_t piece = static_cast<uint32_t>(((lane & 7) ^ (lane >> 3)) << 4);
+    const uint32_t vw = static_cast<uint32_t>(lane >> 3) * pitch + piece;
+    const uint32_t vs = static_cast<uint32_t>(lane >> 1) * spitch + (lane & 1) * 4;
+    uint32_t va[PA], vas = vs;
+    if constexpr (EXPERTS) {
+      const auto row_at = [&](int i) {                     // source row of the tile's row i (clamped: zeros are not needed)
+        const int p = pairs[i < count ? i : count - 1];
+        return static_cast<uint32_t>(a.pair_rows ? p : p / a.k);
+      };
+#pragma unroll
+      for (int i = 0; i < PA; ++i) va[i] = row_at((wave + i * C::kWaves) * 8 + (lane >> 3)) * pitch + piece;
+      vas = row_at(wave * 32 + (lane >> 1)) * spitch + (lane & 1) * 4;
+    }
+
+    const auto fetch = [&](int chunk, int buf) {
+      uint8_t* st = smem + buf * C::kStage;
+#pragma unroll
+      for (int i = 0; i < PA; ++i) {
+        const int g = wave + i * C::kWaves;
+        if (AI % C::kWaves == 0 || g < AI) {
+          if constexpr (EXPERTS) lds_load<16>(ra, st + g * 1024, va[i], chunk * 128);
+          else lds_load<16>(ra, st + g * 1024, vw + g * 8 * pitch, chunk * 128);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < PW; ++i) {
+        const int g = wave + i * C::kWaves;
+        if (WI % C::kWaves == 0 || g < WI) {
+          const int m = NM == 2 && g >= WI / 2 ? 1 : 0;
+          lds_load<16>(m ? rw[NM - 1] : rw[0], st + (AI + g) * 1024, vw + (g - m * (WI / 2)) * 8 * pitch, chunk * 128);
+        }
+      }
+      uint8_t* ss = st + C::kCodes;
+      if (wave < AS) {
+        if constexpr (EXPERTS) lds_load<4>(ras, ss + wave * 256, vas, chunk * 8);
+        else lds_load<4>(ras, ss + wave * 256, vs + wave * 32 * spitch, chunk * 8);
+      }
+      for (int g = (wave + C::kWaves - AS % C::kWaves) % C::kWaves; g < WS; g += C::kWaves) {
+        const int m = NM == 2 && g >= WS / 2 ? 1 : 0;
+        lds_load<4>(m ? rws[NM - 1] : rws[0], ss + (AS + g) * 256, vs + (g - m * (WS / 2)) * 32 * spitch, chunk * 8);
+      }
+    };
+    static_assert(AS <= C::kWaves, "a wave loads at most one group of A's scales");
+
+    fetch(0, 0);
+    for (int chunk = 0; chunk < a.chunks; ++chunk) {
+      const int buf = chunk & 1;
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();   // the chunk has arrived everywhere, and the other stage is read to its end
+      if (chunk + 1 < a.chunks) fetch(chunk + 1, buf ^ 1);
+      const uint8_t* st = smem + buf * C::kStage;
+      const uint8_t* ss = st + C::kCodes;
+      int sa[TM], sw[TN];
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+        sa[i] = *reinterpret_cast<const uint16_t*>(ss + ((wm * TM + i) * 16 + r) * 8 + q * 2);
+      const auto wrow = [&](int j) {   // W rows of this wave's tile j: with SWIGLU gate and up tiles in turn
+        return NM == 1 ? (wn * TN + j) * 16 : (j & 1) * kCols + (wn * (TN / 2) + j / 2) * 16;
+      };
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        sw[j] = *reinterpret_cast<const uint16_t*>(ss + (C::kBM + wrow(j) + r) * 8 + q * 2);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int at = ((2 * q + s) ^ (r & 7)) << 4;
+        v4i fa[TM], fw[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) fw[j] = *reinterpret_cast<const v4i*>(st + (C::kBM + wrow(j) + r) * 128 + at);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) fa[i] = *reinterpret_cast<const v4i*>(st + ((wm * TM + i) * 16 + r) * 128 + at);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j) acc[i][j] = mfma4(fw[j], fa[i], acc[i][j], sw[j], sa[i], s);
+      }
+    }
+  }
+
+  // a lane holds four consecutive outputs of one row
+  const bool whole = (a.N & 3) == 0 && (reinterpret_cast<uintptr_t>(a.out) & (a.out_bf16 ? 7 : 15)) == 0;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int m = (wm * TM + i) * 16 + r;
+    if (m >= count) continue;
+    const int64_t to = (EXPERTS ? static_cast<int64_t>(pairs[m]) : m0 + m) * a.N;
+#pragma unroll
+    for (int j = 0; j < TN; j += NM) {
+      const int n = n0 + (NM == 1 ? (wn * TN + j) * 16 : (wn * (TN / 2) + j / 2) * 16) + 4 * q;
+      float y[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) y[x] = NM == 2 ? silu(acc[i][j][x]) * acc[i][j + NM - 1][x] : acc[i][j][x];
+      if (whole && n + 4 <= a.N) {
+        if (a.out_bf16) {
+          uint2 w;
+          w.x = f32_to_bf16(y[0]) | (static_cast<uint32_t>(f32_to_bf16(y[1])) << 16);
+          w.y = f32_to_bf16(y[2]) | (static_cast<uint32_t>(f32_to_bf16(y[3])) << 16);
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to + n) = w;
+        } else {
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to + n) = float4{y[0], y[1], y[2], y[3]};
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (n + x < a.N) store_out(a.out, to + n + x, y[x], a.out_bf16);
+      }
+    }
+  }
+}
+
 // Pairs grouped by expert: one block counts, scans and places.  The order of
 // an expert's pairs does not change any result (every pair has its own column
 // of the product), so LDS atomics may hand out the places.
 constexpr int kGroupThr = 1024;
 
-__global__ __launch_bounds__(kGroupThr) void k_mx_group(MxArgs a, int P, int32_t* place, int32_t* plist, MxTile* tiles,
+__global__ __launch_bounds__(kGroupThr) void k_mx_group(MxArgs a, int P, int kTileRows, int32_t* place, int32_t* plist, MxTile* tiles,
                                                         int32_t* ntiles) {
   __shared__ int32_t cnt[kMaxExperts + 1];       // the last: pairs whose id is unusable
   __shared__ int32_t sum_p[kGroupThr / kWave], sum_t[kGroupThr / kWave];
@@ -397,7 +592,7 @@ MxWs mx_ws(const mx_product_desc& d, int32_t T, bool experts) {
   if (experts) {
     w.place = take(P * 4);
     w.plist = take(P * 4);
-    w.max_tiles = static_cast<int>((P < d.n_experts + 1 ? P : d.n_experts + 1) + P / kTileRows);
+    w.max_tiles = static_cast<int>((P < d.n_experts + 1 ? P : d.n_experts + 1) + P / 16);
     w.tiles = take(static_cast<size_t>(w.max_tiles) * sizeof(MxTile));
     w.ntiles = take(4);
     w.rows = take(static_cast<size_t>(P) * d.n * 4);
@@ -456,6 +651,23 @@ void narrow(MxArgs a, int src, int act, int ny, hipStream_t s) {
   else narrow_act<kMxF4, MODE>(a, act, grid, s);
 }
 
+template <int WM, int WN, int TM, int TN, bool EXPERTS>
+int tile(MxArgs a, int act, int64_t tiles, hipStream_t s) {
+  using C = TileCfg<WM, WN, TM, TN>;
+  const int cols = act == MX_ACT_SWIGLU ? C::kBN / 2 : C::kBN;
+  a.nblk = (a.N + cols - 1) / cols;
+  const dim3 grid(static_cast<uint32_t>((tiles * a.nblk + 7) / 8 * 8)), block(C::kWaves * kWave);
+  const auto kernel = act == MX_ACT_SWIGLU ? &k_mx_tile<WM, WN, TM, TN, MX_ACT_SWIGLU, EXPERTS>
+                                           : &k_mx_tile<WM, WN, TM, TN, MX_ACT_NONE, EXPERTS>;
+  if (C::kLds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(C::kLds));
+    if (e != hipSuccess) return MOE_EHIP;
+  }
+  launch_kernel(kernel, grid, block, static_cast<uint32_t>(C::kLds), s, a);
+  return MOE_OK;
+}
+
 MxArgs common_args(const mx_product_desc& d, const void* a, const void* as, void* out, void* ws) {
   MxArgs g{};
   g.a = a;
@@ -501,8 +713,25 @@ int mx_linear_forward(const mx_product_desc* d, int32_t M, const void* a, const 
   g.M = M;
   g.wc = static_cast<const uint8_t*>(w_codes);
   g.wsc = static_cast<const uint8_t*>(w_scales);
-  narrow<kDense>(g, d->a_dtype, d->act, (M + 15) / 16, static_cast<hipStream_t>(stream));
-  return launched();
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (M <= 16) {
+    narrow<kDense>(g, d->a_dtype, d->act, 1, s);
+    return launched();
+  }
+  g.arows = M;
+  if (d->a_dtype != MX_FP4) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    launch_mx_quantize(d->a_dtype, M, d->k, a, d->k, ws + L.codes, ws + L.scales, s);
+    g.a = ws + L.codes;
+    g.as = ws + L.scales;
+  }
+  const auto tiles = [&](int bm, int bn) {
+    return static_cast<int64_t>((M + bm - 1) / bm) * ((wrows + bn - 1) / bn);
+  };
+  if (tiles(256, 256) >= 192) rc = tile<2, 4, 8, 4, false>(g, d->act, (M + 255) / 256, s);
+  else if (tiles(128, 128) >= 192) rc = tile<2, 2, 4, 4, false>(g, d->act, (M + 127) / 128, s);
+  else rc = tile<1, 4, 4, 2, false>(g, d->act, (M + 63) / 64, s);
+  return rc == MOE_OK ? launched() : api_fail(MOE_EHIP, "the product kernel's LDS size was refused");
 }
 
 int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const void* a_scales,
@@ -562,7 +791,10 @@ int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const
     int32_t* plist = reinterpret_cast<int32_t*>(ws + L.plist);
     MxTile* tiles = reinterpret_cast<MxTile*>(ws + L.tiles);
     int32_t* ntiles = reinterpret_cast<int32_t*>(ws + L.ntiles);
-    launch_kernel(k_mx_group, dim3(1), dim3(kGroupThr), 0, s, g, P, place, plist, tiles, ntiles);
+    g.arows = static_cast<int>(rows);
+    // tiles of 64 pairs; 16 where the experts have few each or A passes 4 GiB
+    const bool wide = P >= 8 * d->n_experts && rows * (mx_padded(d->k) / 2) < (int64_t(1) << 32) - 65536;
+    launch_kernel(k_mx_group, dim3(1), dim3(kGroupThr), 0, s, g, P, wide ? 64 : 16, place, plist, tiles, ntiles);
     g.plist = plist;
     g.tiles = tiles;
     g.ntiles = ntiles;
@@ -573,7 +805,12 @@ int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const
       g.as = ws + L.scales;
       src = MX_FP4;
     }
-    narrow<kTiles>(g, src, d->act, L.max_tiles, s);
+    if (wide) {
+      const int64_t most = (P < d->n_experts + 1 ? P : d->n_experts + 1) + static_cast<int64_t>(P) / 64;
+      if (tile<1, 4, 4, 2, true>(g, d->act, most, s) != MOE_OK) return api_fail(MOE_EHIP, "the product kernel's LDS size was refused");
+    } else {
+      narrow<kTiles>(g, src, d->act, L.max_tiles, s);
+    }
   }
   if (topk_w)
     launch_kernel(k_mx_combine, dim3(static_cast<uint32_t>((d->n + 255) / 256) * T), dim3(256), 0, s, reinterpret_cast<const float*>(ws + L.rows),
