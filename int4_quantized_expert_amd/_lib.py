@@ -368,44 +368,70 @@ MX_ACT_NONE, MX_ACT_SWIGLU = 0, 1
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 
+_torch = None
+_raw_stream = None
+
+
+def _load_torch():
+    """torch, imported at the first call that needs it, and the cheapest way to the current stream's handle: building a
+    torch.cuda.Stream takes 2.7 us of a call that otherwise takes about 5."""
+    global _torch, _raw_stream
+    import torch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _torch = torch
+    return torch
+
+
 def _bad(msg: str):
     raise MoeError(-1, msg)
 
 
 def _torch_dtype(code: int):
-    import torch
+    torch = _torch or _load_torch()
     return torch.float32 if code == MOE_F32 else torch.bfloat16
 
 
 def _check_tensor(name: str, t, dtype, need: int) -> None:
     """A contiguous device tensor of at least `need` elements of `dtype` (None and addresses pass)."""
-    if t is None or isinstance(t, int):
+    if t is None or type(t) is int:
         return
-    if t.dtype != dtype:
-        _bad(f"{name} is {t.dtype}, {dtype} expected")
-    if not t.is_contiguous():
-        _bad(f"{name} is not contiguous")
-    if t.numel() < need:
+    if t.dtype != dtype or t.numel() < need or not t.is_contiguous():
+        if t.dtype != dtype:
+            _bad(f"{name} is {t.dtype}, {dtype} expected")
+        if not t.is_contiguous():
+            _bad(f"{name} is not contiguous")
         _bad(f"{name} has {t.numel()} elements, {need} needed")
 
 
 def _call_on(tensors, stream, fn, *args) -> None:
-    """fn(*args, stream) on the device that the tensors share."""
-    import torch
+    """fn(*args, stream) on the device that the tensors share; stream None: torch's current one there."""
+    torch = _torch or _load_torch()
     dev = None
     for t in tensors:
-        if t is not None and not isinstance(t, int):
-            if t.device.type != "cuda":
-                _bad(f"a tensor is on {t.device}, not on a GPU")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                _bad(f"tensors on {dev} and {t.device}")
-    if dev is None or dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
+        if t is None or type(t) is int:
+            continue
+        i = t.get_device()
+        if i < 0:
+            _bad(f"a tensor is on {t.device}, not on a GPU")
+        if dev is None:
+            dev = i
+        elif i != dev:
+            _bad(f"tensors on device {dev} and device {i}")
+    here = torch.cuda.current_device()
+    if dev is None:
+        dev = here
+    if stream is None:
+        stream = _raw_stream(dev)
+    elif type(stream) is not int:
+        stream = stream.cuda_stream
+    if dev == here:
+        rc = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)))
+            rc = fn(*args, stream)
+    if rc != 0:
+        raise MoeError(rc, last_error())
 
 
 def route_desc(n_experts, top_k, score="softmax", n_groups=1, top_groups=1, group_top=1, renormalize=True, scale=1.0,
@@ -419,9 +445,9 @@ def route_desc(n_experts, top_k, score="softmax", n_groups=1, top_groups=1, grou
 def route(r: RouteDesc, T: int, logits, bias, topk_ids, topk_w, logits_stride=None, stream=None) -> None:
     """Routing of T tokens from their logits (moe_route_forward).  logits: [T, n_experts], rows may be strided;
     logits_stride (elements) defaults to the tensor's, for an address to n_experts."""
-    import torch
+    torch = _torch or _load_torch()
     E, k = r.n_experts, r.top_k
-    if not isinstance(logits, int):
+    if type(logits) is not int:
         if logits.dim() != 2 or logits.shape[0] < T or logits.shape[1] < E or (E > 1 and logits.stride(1) != 1):
             _bad(f"logits of shape {tuple(logits.shape)}, strides {logits.stride()}: rows of {E} adjacent values expected")
         if logits.dtype != _torch_dtype(r.logit_dtype):
@@ -441,7 +467,7 @@ def route(r: RouteDesc, T: int, logits, bias, topk_ids, topk_w, logits_stride=No
 
 def router_route(d: MoeDesc, r: RouteDesc, T: int, x, router_w, bias, topk_ids, topk_w, ws, stream=None) -> None:
     """router_topk with routing from scores: logits R x, then route (moe_router_route)."""
-    import torch
+    torch = _torch or _load_torch()
     _check_tensor("bias", bias, torch.float32, r.n_experts)
     _check_tensor("topk_ids", topk_ids, torch.int32, T * r.top_k)
     _check_tensor("topk_w", topk_w, torch.float32, T * r.top_k)
@@ -452,7 +478,7 @@ def router_route(d: MoeDesc, r: RouteDesc, T: int, x, router_w, bias, topk_ids, 
 
 def mx_shapes(rows: int, cols: int) -> tuple[tuple[int, int], tuple[int, int]]:
     """Shapes of the uint8 codes and scales tensors of an MX matrix [rows, cols]."""
-    if lib().mx_codes_bytes(rows, cols) < 0:
+    if not (0 <= rows < 1 << 31 and 0 <= cols <= 1 << 20):
         _bad(f"an MX matrix of {rows} x {cols} is negative or too large")
     padded = -(-cols // 256) * 256
     return (rows, padded // 2), (rows, padded // 32)
@@ -460,17 +486,17 @@ def mx_shapes(rows: int, cols: int) -> tuple[tuple[int, int], tuple[int, int]]:
 
 def _mx_rows(name: str, t):
     """(dtype code, rows, cols, row stride) of a 2-d tensor whose rows are adjacent values."""
-    import torch
+    torch = _torch or _load_torch()
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         _bad(f"{name} of shape {tuple(t.shape)}, strides {t.stride()}: a matrix with adjacent values in its rows expected")
-    code = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}.get(t.dtype)
-    if code is None:
+    code = MOE_F32 if t.dtype == torch.float32 else MOE_BF16
+    if code == MOE_BF16 and t.dtype != torch.bfloat16:
         _bad(f"{name} is {t.dtype}, float32 or bfloat16 expected")
     return code, t.shape[0], t.shape[1], t.stride(0)
 
 
 def _check_mx(name: str, codes, scales, rows: int, cols: int) -> None:
-    import torch
+    torch = _torch or _load_torch()
     (_, c), (_, s) = mx_shapes(rows, cols)
     _check_tensor(f"{name} codes", codes, torch.uint8, rows * c)
     _check_tensor(f"{name} scales", scales, torch.uint8, rows * s)
@@ -526,13 +552,13 @@ def mx_linear(d: MxProductDesc, M: int, a, a_scales, w_codes, w_scales, out, ws,
 
 def mx_experts(d: MxProductDesc, T: int, a, a_scales, topk_ids, topk_w, slot_table, pool, out, ws, stream=None) -> None:
     """Product by routed expert (mx_experts_forward); topk_w None: one output row per pair, else the weighted sums."""
-    import torch
+    torch = _torch or _load_torch()
     pairs = T * d.top_k
     _check_a(d, a, a_scales, pairs if d.pair_rows else T)
     _check_tensor("topk_ids", topk_ids, torch.int32, pairs)
     _check_tensor("topk_w", topk_w, torch.float32, pairs)
     _check_tensor("slot_table", slot_table, torch.int64, d.n_experts)
-    if not isinstance(pool, int) and _nbytes(pool) < d.pool_bytes:
+    if type(pool) is not int and _nbytes(pool) < d.pool_bytes:
         _bad(f"pool has {_nbytes(pool)} bytes, pool_bytes is {d.pool_bytes}")
     _check_tensor("out", out, _torch_dtype(d.out_dtype), (pairs if topk_w is None else T) * d.n)
     _call_on((a, a_scales, topk_ids, topk_w, slot_table, pool, out, ws), stream, lib().mx_experts_forward,
