@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "device_common.h"
+#include "topk_wave.h"
 
 namespace moe {
 
@@ -81,6 +82,37 @@ __device__ __forceinline__ uint32_t mx_mag8(const float (&v)[8]) {
     m = b > m ? b : m;
   }
   return m;
+}
+
+// Piece p (eight values) of the padded matrix -> its row and column.
+struct Piece {
+  int64_t row;
+  int64_t col;
+};
+
+__device__ __forceinline__ Piece piece_at(int64_t p, uint32_t per_row) {
+  const int64_t r = (p >> 31) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(p) / per_row) : p / per_row;
+  return {r, (p - r * per_row) * 8};
+}
+
+// One piece of a row-major matrix quantised; the four lanes of a block call it
+// together.
+template <int DT>
+__device__ __forceinline__ void mx_quantize_piece(const void* x, int64_t stride, int64_t cols, uint32_t per_row, int64_t p,
+                                                  int64_t pieces, uint32_t* codes, uint8_t* scales) {
+  if (p >= pieces) return;   // pieces of a block are whole: per_row is a multiple of 32
+  const int lane = threadIdx.x & (kWave - 1);
+  const Piece at = piece_at(p, per_row);
+  float v[8];
+  mx_load8<DT>(x, at.row * stride, at.col, cols, v);
+  uint32_t m = mx_mag8(v);
+  uint32_t o = lane_xor<1>(m, lane);
+  m = o > m ? o : m;
+  o = lane_xor<2>(m, lane);
+  m = o > m ? o : m;
+  const uint32_t byte = mx_scale_byte(m);
+  codes[p] = mx_codes8(v, byte);
+  if ((lane & 3) == 0) scales[p >> 2] = static_cast<uint8_t>(byte);
 }
 
 }  // namespace moe

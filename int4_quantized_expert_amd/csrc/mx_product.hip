@@ -256,31 +256,42 @@ __global__ __launch_bounds__(kNarrowWaves* kWave) void k_mx_narrow(MxArgs a) {
 
 // Many rows of A: a block forms BM rows of A x BN rows of W.  Both operands'
 // codes (128 bytes of a row per chunk) and scales (8 bytes) go to LDS with
-// direct loads, two chunks deep: while a chunk is multiplied the next one
-// arrives.  A row's eight 16-byte pieces are placed by piece ^ (row mod 8), so
-// that sixteen lanes reading one piece of sixteen rows hit different banks.
-//   rows of W past N and rows of A past M read as zeros (the buffer descriptors
-//   end there; a row's offset is in the lane's part of the address, which the
-//   bounds check compares with what the scalar part leaves) and are not stored; with SWIGLU the first half of a block's W
-//   rows are gate rows and the second half the up rows of the same outputs.
-template <int WM, int WN, int TM, int TN>
+// direct loads, through S stages: while a chunk is multiplied the next S - 1
+// are on their way.  A row's eight 16-byte pieces are placed by piece ^ (row
+// mod 8), so that sixteen lanes reading one piece of sixteen rows hit
+// different banks.
+//   Rows of W past N and rows of A past M read as zeros (the buffer
+//   descriptors end there; a row's offset is in the lane's part of the
+//   address, which the bounds check compares with what the scalar part leaves)
+//   and are not stored; with SWIGLU the first half of a block's W rows are gate
+//   rows and the second half the up rows of the same outputs.
+//   Every wave issues the same number of loads per chunk (a wave without a
+//   share repeats the last one, the same bytes to the same place), so that
+//   waiting for all but the newest (S - 2) kLoads means the oldest chunk.
+template <int WM, int WN, int TM, int TN, int S>
 struct TileCfg {
-  static constexpr int kWaves = WM * WN, kBM = WM * TM * 16, kBN = WN * TN * 16;
-  static constexpr int kCodes = (kBM + kBN) * 128, kScales = (kBM + kBN) * 8;
-  static constexpr int kStage = kCodes + kScales;
-  static constexpr size_t kLds = 2 * static_cast<size_t>(kStage);
+  static constexpr int kWaves = WM * WN, kBM = WM * TM * 16, kBN = WN * TN * 16, kRows = kBM + kBN;
+  static constexpr int kStage = kRows * 136;                // codes, then scales
+  static constexpr int kCodeGroups = kRows / 8, kScaleGroups = kRows / 32;   // rows of a direct load: 8, 32
+  static constexpr int kPC = (kCodeGroups + kWaves - 1) / kWaves, kPS = (kScaleGroups + kWaves - 1) / kWaves;
+  static constexpr int kLoads = kPC + kPS;
+  static constexpr size_t kLds = S * static_cast<size_t>(kStage);
+  static_assert(kRows % 32 == 0 && kBM % 16 == 0, "whole groups");
+  static_assert((S - 2) * kLoads < 64, "the wait counter has six bits");
 };
 
 __device__ __forceinline__ int64_t clamp32(int64_t n) { return n < 0xfffffff0ll ? n : 0xfffffff0ll; }
 
-template <int WM, int WN, int TM, int TN, int ACT, bool EXPERTS>
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+template <int WM, int WN, int TM, int TN, int S, int ACT, bool EXPERTS>
 __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
-  using C = TileCfg<WM, WN, TM, TN>;
+  using C = TileCfg<WM, WN, TM, TN, S>;
   constexpr int NM = ACT == MX_ACT_SWIGLU ? 2 : 1;
   constexpr int kCols = C::kBN / NM;                       // outputs of a block
-  constexpr int AI = C::kBM / 8, WI = C::kBN / 8;          // direct loads of codes per chunk: eight rows each
-  constexpr int AS = C::kBM / 32, WS = C::kBN / 32;        // of scales: 32 rows each
-  constexpr int PA = (AI + C::kWaves - 1) / C::kWaves, PW = (WI + C::kWaves - 1) / C::kWaves;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r = lane & 15, q = lane >> 4;
@@ -338,60 +349,67 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
                              : raw_rsrc(ab + m0 * pitch, clamp32(static_cast<int64_t>(count) * pitch));
     const u32x4 ras = EXPERTS ? raw_rsrc(a.as, clamp32(static_cast<int64_t>(a.arows) * spitch))
                               : raw_rsrc(a.as + m0 * spitch, clamp32(static_cast<int64_t>(count) * spitch));
-    // a lane's place in a direct load: row lane / 8 of eight, piece lane mod 8;
-    // of scales: row lane / 2 of 32, word lane mod 2
-    const uint32_t piece = static_cast<uint32_t>(((lane & 7) ^ (lane >> 3)) << 4);
-    const uint32_t vw = static_cast<uint32_t>(lane >> 3) * pitch + piece;
-    const uint32_t vs = static_cast<uint32_t>(lane >> 1) * spitch + (lane & 1) * 4;
-    uint32_t va[PA], vas = vs;
-    if constexpr (EXPERTS) {
-      const auto row_at = [&](int i) {                     // source row of the tile's row i (clamped: zeros are not needed)
-        const int p = pairs[i < count ? i : count - 1];
-        return static_cast<uint32_t>(a.pair_rows ? p : p / a.k);
-      };
+    // a stage's row -> its row in its operand
+    const auto row_at = [&](int row) {
+      if (row < C::kBM) {
+        if constexpr (EXPERTS) {
+          const int p = pairs[row < count ? row : count - 1];
+          return static_cast<uint32_t>(a.pair_rows ? p : p / a.k);
+        }
+        return static_cast<uint32_t>(row);
+      }
+      row -= C::kBM;
+      return static_cast<uint32_t>(NM == 2 && row >= kCols ? row - kCols : row);
+    };
+    // this wave's loads: a lane takes piece lane mod 8 of row lane / 8 of its
+    // group; of scales word lane mod 2 of row lane / 2
+    uint32_t vc[C::kPC], vs[C::kPS];
 #pragma unroll
-      for (int i = 0; i < PA; ++i) va[i] = row_at((wave + i * C::kWaves) * 8 + (lane >> 3)) * pitch + piece;
-      vas = row_at(wave * 32 + (lane >> 1)) * spitch + (lane & 1) * 4;
+    for (int i = 0; i < C::kPC; ++i) {
+      int g = wave + i * C::kWaves;
+      g = g < C::kCodeGroups ? g : C::kCodeGroups - 1;
+      vc[i] = row_at(g * 8 + (lane >> 3)) * pitch + static_cast<uint32_t>(((lane & 7) ^ (lane >> 3)) << 4);
     }
-
+#pragma unroll
+    for (int i = 0; i < C::kPS; ++i) {
+      int g = wave + i * C::kWaves;
+      g = g < C::kScaleGroups ? g : C::kScaleGroups - 1;
+      vs[i] = row_at(g * 32 + (lane >> 1)) * spitch + static_cast<uint32_t>((lane & 1) * 4);
+    }
     const auto fetch = [&](int chunk, int buf) {
       uint8_t* st = smem + buf * C::kStage;
 #pragma unroll
-      for (int i = 0; i < PA; ++i) {
-        const int g = wave + i * C::kWaves;
-        if (AI % C::kWaves == 0 || g < AI) {
-          if constexpr (EXPERTS) lds_load<16>(ra, st + g * 1024, va[i], chunk * 128);
-          else lds_load<16>(ra, st + g * 1024, vw + g * 8 * pitch, chunk * 128);
-        }
+      for (int i = 0; i < C::kPC; ++i) {
+        int g = wave + i * C::kWaves;
+        g = g < C::kCodeGroups ? g : C::kCodeGroups - 1;
+        const int row = g * 8;
+        const u32x4 rs = row < C::kBM ? ra : (NM == 2 && row >= C::kBM + kCols ? rw[NM - 1] : rw[0]);
+        lds_load<16>(rs, st + g * 1024, vc[i], chunk * 128);
       }
 #pragma unroll
-      for (int i = 0; i < PW; ++i) {
-        const int g = wave + i * C::kWaves;
-        if (WI % C::kWaves == 0 || g < WI) {
-          const int m = NM == 2 && g >= WI / 2 ? 1 : 0;
-          lds_load<16>(m ? rw[NM - 1] : rw[0], st + (AI + g) * 1024, vw + (g - m * (WI / 2)) * 8 * pitch, chunk * 128);
-        }
-      }
-      uint8_t* ss = st + C::kCodes;
-      if (wave < AS) {
-        if constexpr (EXPERTS) lds_load<4>(ras, ss + wave * 256, vas, chunk * 8);
-        else lds_load<4>(ras, ss + wave * 256, vs + wave * 32 * spitch, chunk * 8);
-      }
-      for (int g = (wave + C::kWaves - AS % C::kWaves) % C::kWaves; g < WS; g += C::kWaves) {
-        const int m = NM == 2 && g >= WS / 2 ? 1 : 0;
-        lds_load<4>(m ? rws[NM - 1] : rws[0], ss + (AS + g) * 256, vs + (g - m * (WS / 2)) * 32 * spitch, chunk * 8);
+      for (int i = 0; i < C::kPS; ++i) {
+        int g = wave + i * C::kWaves;
+        g = g < C::kScaleGroups ? g : C::kScaleGroups - 1;
+        const int row = g * 32;
+        uint8_t* to = st + C::kRows * 128 + g * 256;
+        const u32x4 rs = row < C::kBM ? ras : (NM == 2 && row >= C::kBM + kCols ? rws[NM - 1] : rws[0]);
+        lds_load<4>(rs, to, vs[i], chunk * 8);
       }
     };
-    static_assert(AS <= C::kWaves, "a wave loads at most one group of A's scales");
+    static_assert(C::kBM % 32 == 0 && kCols % 32 == 0, "a group of scales is of one operand");
 
-    fetch(0, 0);
+#pragma unroll
+    for (int c = 0; c < S - 1; ++c)
+      if (c < a.chunks) fetch(c, c);
+    int buf = 0;
     for (int chunk = 0; chunk < a.chunks; ++chunk) {
-      const int buf = chunk & 1;
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();   // the chunk has arrived everywhere, and the other stage is read to its end
-      if (chunk + 1 < a.chunks) fetch(chunk + 1, buf ^ 1);
+      if (chunk + S - 2 < a.chunks) wait_loads<(S - 2) * C::kLoads>();
+      else wait_loads<0>();
+      __syncthreads();   // the chunk has arrived everywhere, and the stage before it is read to its end
+      if (chunk + S - 1 < a.chunks) fetch(chunk + S - 1, buf == 0 ? S - 1 : buf - 1);
       const uint8_t* st = smem + buf * C::kStage;
-      const uint8_t* ss = st + C::kCodes;
+      const uint8_t* ss = st + C::kRows * 128;
+      buf = buf + 1 == S ? 0 : buf + 1;
       int sa[TM], sw[TN];
 #pragma unroll
       for (int i = 0; i < TM; ++i)
@@ -449,28 +467,71 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
   }
 }
 
-// Pairs grouped by expert: one block counts, scans and places.  The order of
-// an expert's pairs does not change any result (every pair has its own column
-// of the product), so LDS atomics may hand out the places.
-constexpr int kGroupThr = 1024;
+// Before the tiles: block 0 groups the pairs by expert, the others quantise A.
+//
+// Grouping is one block's work: count (LDS atomics, which hand out each pair's
+// place within its expert), scan, place.  The order of an expert's pairs does
+// not change any result, since every pair has its own column of the product.
+// Up to kPrepThr * 4 * NI pairs stay in registers between the passes (four
+// consecutive ids a load, all requested at once); more are read again (NI = 0).
+constexpr int kPrepThr = 1024;
 
-__global__ __launch_bounds__(kGroupThr) void k_mx_group(MxArgs a, int P, int kTileRows, int32_t* place, int32_t* plist, MxTile* tiles,
-                                                        int32_t* ntiles) {
+struct PrepArgs {
+  MxArgs g;
+  int P, rows;            // pairs; pairs per tile
+  int32_t* place;
+  int32_t* plist;
+  MxTile* tiles;
+  int32_t* ntiles;
+  const void* x;          // A, fp32 or bf16, to quantise; NULL: nothing
+  int64_t pieces, cols;
+  uint32_t per_row;
+  uint32_t* codes;
+  uint8_t* scales;
+};
+
+template <int NI>
+__device__ __forceinline__ void group_pairs(const PrepArgs& p) {
   __shared__ int32_t cnt[kMaxExperts + 1];       // the last: pairs whose id is unusable
-  __shared__ int32_t sum_p[kGroupThr / kWave], sum_t[kGroupThr / kWave];
+  __shared__ int32_t sum_p[kPrepThr / kWave], sum_t[kPrepThr / kWave];
   __shared__ int32_t start[kMaxExperts + 1];
+  const MxArgs& a = p.g;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  for (int e = tid; e <= a.E; e += kGroupThr) cnt[e] = 0;
+  const int P = p.P, E = a.E;
+  const auto bucket = [&](int id) { return id >= 0 && id < E ? id : E; };
+  // bucket (11 bits) and place of each pair
+  uint32_t kept[NI > 0 ? NI : 1][4];
+  if constexpr (NI > 0) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int at = (i * kPrepThr + tid) * 4;
+      if (at + 4 <= P) __builtin_memcpy(kept[i], a.ids + at, 16);
+      else
+#pragma unroll
+        for (int x = 0; x < 4; ++x) kept[i][x] = at + x < P ? static_cast<uint32_t>(a.ids[at + x]) : 0u;
+    }
+  }
+  // the slots of this thread's expert, requested before they are needed
+  const int64_t off = tid < E ? blob_of(a.slots, tid, E, a.need, a.pool_bytes) : -1;
+  for (int e = tid; e <= E; e += kPrepThr) cnt[e] = 0;
   __syncthreads();
-  for (int p = tid; p < P; p += kGroupThr) {
-    const int id = a.ids[p];
-    place[p] = atomicAdd(&cnt[(id >= 0 && id < a.E) ? id : a.E], 1);
+  if constexpr (NI > 0) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if ((i * kPrepThr + tid) * 4 + x < P) {
+          const uint32_t b = static_cast<uint32_t>(bucket(static_cast<int>(kept[i][x])));
+          kept[i][x] = b | (static_cast<uint32_t>(atomicAdd(&cnt[b], 1)) << 11);
+        }
+  } else {
+    for (int i = tid; i < P; i += kPrepThr) p.place[i] = atomicAdd(&cnt[bucket(a.ids[i])], 1);
   }
   __syncthreads();
   // exclusive scans of the pair and tile counts; the bucket of unusable ids
   // (index E <= 1024, one past the threads at most) comes last
-  const int c = tid < a.E ? cnt[tid] : 0;
-  const int nt = (c + kTileRows - 1) / kTileRows;
+  const int c = tid < E ? cnt[tid] : 0;
+  const int nt = (c + p.rows - 1) / p.rows;
   int ip = c, it = nt;
   for (int s = 1; s < kWave; s <<= 1) {
     const int op = __shfl_up(ip, s), ot = __shfl_up(it, s);
@@ -479,35 +540,54 @@ __global__ __launch_bounds__(kGroupThr) void k_mx_group(MxArgs a, int P, int kTi
   if (lane == kWave - 1) { sum_p[wave] = ip; sum_t[wave] = it; }
   __syncthreads();
   int bp = 0, bt = 0, tp = 0, tt = 0;
-  for (int w = 0; w < kGroupThr / kWave; ++w) {
+#pragma unroll
+  for (int w = 0; w < kPrepThr / kWave; ++w) {
     if (w < wave) { bp += sum_p[w]; bt += sum_t[w]; }
     tp += sum_p[w];
     tt += sum_t[w];
   }
   const int sp = bp + ip - c, st = bt + it - nt;
-  if (tid < a.E) start[tid] = sp;
-  if (c > 0) {
-    const int64_t off = blob_of(a.slots, tid, a.E, a.need, a.pool_bytes);
-    if (off < 0) atomicOr(a.flags, 1u);
-    for (int i = 0; i < nt; ++i) {
-      const int left = c - i * kTileRows;
-      tiles[st + i] = MxTile{off, sp + i * kTileRows, left < kTileRows ? left : kTileRows};
-    }
-  }
-  const int lost = cnt[a.E], lost_t = (lost + kTileRows - 1) / kTileRows;
-  for (int i = tid; i < lost_t; i += kGroupThr) {
-    const int left = lost - i * kTileRows;
-    tiles[tt + i] = MxTile{-1, tp + i * kTileRows, left < kTileRows ? left : kTileRows};
-  }
+  if (tid < E) start[tid] = sp;
+  const int lost = cnt[E], lost_t = (lost + p.rows - 1) / p.rows;
   if (tid == 0) {
-    *ntiles = tt + lost_t;
-    start[a.E] = tp;
+    *p.ntiles = tt + lost_t;
+    start[E] = tp;
     if (lost) atomicOr(a.flags, 1u);
   }
   __syncthreads();
-  for (int p = tid; p < P; p += kGroupThr) {
-    const int id = a.ids[p];
-    plist[start[(id >= 0 && id < a.E) ? id : a.E] + place[p]] = p;
+  if constexpr (NI > 0) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int at = (i * kPrepThr + tid) * 4 + x;
+        if (at < P) p.plist[start[kept[i][x] & 2047u] + (kept[i][x] >> 11)] = at;
+      }
+  } else {
+    for (int i = tid; i < P; i += kPrepThr) p.plist[start[bucket(a.ids[i])] + p.place[i]] = i;
+  }
+  if (c > 0) {
+    if (off < 0) atomicOr(a.flags, 1u);
+    for (int i = 0; i < nt; ++i) {
+      const int left = c - i * p.rows;
+      p.tiles[st + i] = MxTile{off, sp + i * p.rows, left < p.rows ? left : p.rows};
+    }
+  }
+  for (int i = tid; i < lost_t; i += kPrepThr) {
+    const int left = lost - i * p.rows;
+    p.tiles[tt + i] = MxTile{-1, tp + i * p.rows, left < p.rows ? left : p.rows};
+  }
+}
+
+template <int SRC, int NI>
+__global__ __launch_bounds__(kPrepThr) void k_mx_prep(PrepArgs p) {
+  if (blockIdx.x == 0) {
+    group_pairs<NI>(p);
+    return;
+  }
+  if constexpr (SRC != kMxF4) {
+    mx_quantize_piece<SRC>(p.x, p.cols, p.cols, p.per_row, static_cast<int64_t>(blockIdx.x - 1) * kPrepThr + threadIdx.x,
+                           p.pieces, p.codes, p.scales);
   }
 }
 
@@ -651,14 +731,14 @@ void narrow(MxArgs a, int src, int act, int ny, hipStream_t s) {
   else narrow_act<kMxF4, MODE>(a, act, grid, s);
 }
 
-template <int WM, int WN, int TM, int TN, bool EXPERTS>
+template <int WM, int WN, int TM, int TN, int S, bool EXPERTS>
 int tile(MxArgs a, int act, int64_t tiles, hipStream_t s) {
-  using C = TileCfg<WM, WN, TM, TN>;
+  using C = TileCfg<WM, WN, TM, TN, S>;
   const int cols = act == MX_ACT_SWIGLU ? C::kBN / 2 : C::kBN;
   a.nblk = (a.N + cols - 1) / cols;
   const dim3 grid(static_cast<uint32_t>((tiles * a.nblk + 7) / 8 * 8)), block(C::kWaves * kWave);
-  const auto kernel = act == MX_ACT_SWIGLU ? &k_mx_tile<WM, WN, TM, TN, MX_ACT_SWIGLU, EXPERTS>
-                                           : &k_mx_tile<WM, WN, TM, TN, MX_ACT_NONE, EXPERTS>;
+  const auto kernel = act == MX_ACT_SWIGLU ? &k_mx_tile<WM, WN, TM, TN, S, MX_ACT_SWIGLU, EXPERTS>
+                                           : &k_mx_tile<WM, WN, TM, TN, S, MX_ACT_NONE, EXPERTS>;
   if (C::kLds > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(C::kLds));
@@ -666,6 +746,15 @@ int tile(MxArgs a, int act, int64_t tiles, hipStream_t s) {
   }
   launch_kernel(kernel, grid, block, static_cast<uint32_t>(C::kLds), s, a);
   return MOE_OK;
+}
+
+template <int SRC>
+void prep_src(const PrepArgs& p, uint32_t blocks, hipStream_t s) {
+  const dim3 grid(blocks), block(kPrepThr);
+  if (p.P <= 4 * kPrepThr) launch_kernel(k_mx_prep<SRC, 1>, grid, block, 0, s, p);
+  else if (p.P <= 8 * kPrepThr) launch_kernel(k_mx_prep<SRC, 2>, grid, block, 0, s, p);
+  else if (p.P <= 24 * kPrepThr) launch_kernel(k_mx_prep<SRC, 6>, grid, block, 0, s, p);
+  else launch_kernel(k_mx_prep<SRC, 0>, grid, block, 0, s, p);
 }
 
 MxArgs common_args(const mx_product_desc& d, const void* a, const void* as, void* out, void* ws) {
@@ -728,9 +817,9 @@ int mx_linear_forward(const mx_product_desc* d, int32_t M, const void* a, const 
   const auto tiles = [&](int bm, int bn) {
     return static_cast<int64_t>((M + bm - 1) / bm) * ((wrows + bn - 1) / bn);
   };
-  if (tiles(256, 256) >= 192) rc = tile<2, 4, 8, 4, false>(g, d->act, (M + 255) / 256, s);
-  else if (tiles(128, 128) >= 192) rc = tile<2, 2, 4, 4, false>(g, d->act, (M + 127) / 128, s);
-  else rc = tile<1, 4, 4, 2, false>(g, d->act, (M + 63) / 64, s);
+  if (tiles(256, 256) >= 192) rc = tile<2, 4, 8, 4, 2, false>(g, d->act, (M + 255) / 256, s);
+  else if (tiles(128, 128) >= 192) rc = tile<2, 2, 4, 4, 2, false>(g, d->act, (M + 127) / 128, s);
+  else rc = tile<1, 4, 4, 2, 3, false>(g, d->act, (M + 63) / 64, s);
   return rc == MOE_OK ? launched() : api_fail(MOE_EHIP, "the product kernel's LDS size was refused");
 }
 
@@ -787,30 +876,44 @@ int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const
   if (P <= kDirectPairs) {
     narrow<kDirect>(g, d->a_dtype, d->act, P, s);
   } else {
-    int32_t* place = reinterpret_cast<int32_t*>(ws + L.place);
-    int32_t* plist = reinterpret_cast<int32_t*>(ws + L.plist);
-    MxTile* tiles = reinterpret_cast<MxTile*>(ws + L.tiles);
-    int32_t* ntiles = reinterpret_cast<int32_t*>(ws + L.ntiles);
     g.arows = static_cast<int>(rows);
-    // tiles of 64 pairs; 16 where the experts have few each or A passes 4 GiB
-    const bool wide = P >= 8 * d->n_experts && rows * (mx_padded(d->k) / 2) < (int64_t(1) << 32) - 65536;
-    launch_kernel(k_mx_group, dim3(1), dim3(kGroupThr), 0, s, g, P, wide ? 64 : 16, place, plist, tiles, ntiles);
-    g.plist = plist;
-    g.tiles = tiles;
-    g.ntiles = ntiles;
-    int src = d->a_dtype;
-    if (src != MX_FP4) {
-      launch_mx_quantize(src, rows, d->k, a, d->k, ws + L.codes, ws + L.scales, s);
-      g.a = ws + L.codes;
-      g.as = ws + L.scales;
-      src = MX_FP4;
-    }
-    if (wide) {
-      const int64_t most = (P < d->n_experts + 1 ? P : d->n_experts + 1) + static_cast<int64_t>(P) / 64;
-      if (tile<1, 4, 4, 2, true>(g, d->act, most, s) != MOE_OK) return api_fail(MOE_EHIP, "the product kernel's LDS size was refused");
+    // rows per tile by the pairs that an expert has on average; A's offsets
+    // have 32 bits in the tiles
+    const int each = P / d->n_experts;
+    const bool far = rows * (mx_padded(d->k) / 2) >= (int64_t(1) << 32) - 65536;
+    const int bm = far ? 16 : each >= 96 ? 128 : each >= 24 ? 64 : 32;
+    PrepArgs p{};
+    p.g = g;
+    p.P = P;
+    p.rows = bm;
+    p.place = reinterpret_cast<int32_t*>(ws + L.place);
+    p.plist = reinterpret_cast<int32_t*>(ws + L.plist);
+    p.tiles = reinterpret_cast<MxTile*>(ws + L.tiles);
+    p.ntiles = reinterpret_cast<int32_t*>(ws + L.ntiles);
+    if (d->a_dtype == MX_FP4) {
+      prep_src<kMxF4>(p, 1, s);
     } else {
-      narrow<kTiles>(g, src, d->act, L.max_tiles, s);
+      p.x = a;
+      p.cols = d->k;
+      p.per_row = static_cast<uint32_t>(mx_padded(d->k) / 8);
+      p.pieces = rows * p.per_row;
+      p.codes = reinterpret_cast<uint32_t*>(ws + L.codes);
+      p.scales = ws + L.scales;
+      const uint32_t blocks = static_cast<uint32_t>(1 + (p.pieces + kPrepThr - 1) / kPrepThr);
+      if (d->a_dtype == MOE_F32) prep_src<kF32>(p, blocks, s);
+      else prep_src<kBF16>(p, blocks, s);
+      g.a = p.codes;
+      g.as = p.scales;
     }
+    g.plist = p.plist;
+    g.tiles = p.tiles;
+    g.ntiles = p.ntiles;
+    const int64_t most = (P < d->n_experts + 1 ? P : d->n_experts + 1) + static_cast<int64_t>(P) / bm;
+    if (bm == 16) narrow<kTiles>(g, MX_FP4, d->act, static_cast<int>(most), s);
+    else if (bm == 32) rc = tile<1, 4, 2, 2, 3, true>(g, d->act, most, s);
+    else if (bm == 64) rc = tile<1, 4, 4, 2, 3, true>(g, d->act, most, s);
+    else rc = tile<2, 2, 4, 4, 2, true>(g, d->act, most, s);
+    if (rc != MOE_OK) return api_fail(MOE_EHIP, "the product kernel's LDS size was refused");
   }
   if (topk_w)
     launch_kernel(k_mx_combine, dim3(static_cast<uint32_t>((d->n + 255) / 256) * T), dim3(256), 0, s, reinterpret_cast<const float*>(ws + L.rows),

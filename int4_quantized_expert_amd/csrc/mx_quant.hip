@@ -20,17 +20,6 @@ namespace {
 constexpr int kQThr = 256;
 constexpr int kIter = 4;
 
-// Piece p (eight values) of the padded matrix -> its row and column.
-struct Piece {
-  int64_t row;
-  int64_t col;
-};
-
-__device__ __forceinline__ Piece piece_at(int64_t p, uint32_t per_row) {
-  const int64_t r = (p >> 31) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(p) / per_row) : p / per_row;
-  return {r, (p - r * per_row) * 8};
-}
-
 template <int DT>
 __global__ __launch_bounds__(kQThr) void k_mx_quantize(const void* x, int64_t stride, int64_t cols, uint32_t per_row,
                                                        int64_t pieces, uint32_t* codes, uint8_t* scales) {

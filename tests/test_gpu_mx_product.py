@@ -464,10 +464,12 @@ def test_experts_stream_through_the_slot_cache():
     small = torch.zeros(4 * stride, dtype=torch.uint8, device=DEV)
     cache = M.ExpertCache(4, stride, small, host, 1, E)
     copy = torch.cuda.Stream()
+    events = []                              # the cache waits for a slot's last reader later on: they live as long as it
     for step in range(4):
         ids = np.stack([rng.choice(E, 2, replace=False)] * 3).astype(np.int32)
         table = np.full(E, -1, dtype=np.int64)
         ready, done = torch.cuda.Event(), torch.cuda.Event()
+        events += [ready, done]
         cache.acquire(0, ids, table, copy, ready)
         torch.cuda.current_stream().wait_event(ready)
         x.slots, x.pool = dev(table), small
