@@ -255,9 +255,11 @@ __global__ __launch_bounds__(kNarrowWaves* kWave) void k_mx_narrow(MxArgs a) {
 }
 
 // Many rows of A: a block forms BM rows of A x BN rows of W.  Both operands'
-// codes (128 bytes of a row per chunk) and scales (8 bytes) go to LDS with
-// direct loads, through S stages: while a chunk is multiplied the next S - 1
-// are on their way.  A row's eight 16-byte pieces are placed by piece ^ (row
+// codes (128 bytes of a row per chunk) go to LDS with direct loads, through S
+// stages: while a chunk is multiplied the next S - 1 are on their way.  Their
+// scales go with every second chunk, 16 bytes of a row for two chunks (4-byte
+// loads with every chunk touched as many lines as the codes: 8192^3 took 308
+// instead of 282 us).  A row's eight 16-byte pieces are placed by piece ^ (row
 // mod 8), so that sixteen lanes reading one piece of sixteen rows hit
 // different banks.
 //   Rows of W past N and rows of A past M read as zeros (the buffer
@@ -265,19 +267,20 @@ __global__ __launch_bounds__(kNarrowWaves* kWave) void k_mx_narrow(MxArgs a) {
 //   address, which the bounds check compares with what the scalar part leaves)
 //   and are not stored; with SWIGLU the first half of a block's W rows are gate
 //   rows and the second half the up rows of the same outputs.
-//   Every wave issues the same number of loads per chunk (a wave without a
-//   share repeats the last one, the same bytes to the same place), so that
-//   waiting for all but the newest (S - 2) kLoads means the oldest chunk.
+//   Every wave issues the same number of loads for a chunk (a wave without a
+//   share repeats the last one, the same bytes to the same place), so that all
+//   but the newest chunk's have landed once no more than that number is left.
 template <int WM, int WN, int TM, int TN, int S>
 struct TileCfg {
   static constexpr int kWaves = WM * WN, kBM = WM * TM * 16, kBN = WN * TN * 16, kRows = kBM + kBN;
-  static constexpr int kStage = kRows * 136;                // codes, then scales
-  static constexpr int kCodeGroups = kRows / 8, kScaleGroups = kRows / 32;   // rows of a direct load: 8, 32
+  static constexpr int kStage = kRows * 128;                // the codes of a chunk
+  // rows of a direct load: 8 of codes, 64 of scales, each of one operand
+  static constexpr int kCodeGroups = kRows / 8, kAScales = (kBM + 63) / 64, kScaleGroups = kAScales + kBN / 64;
+  static constexpr int kScales = kScaleGroups * 1024;       // the scales of two chunks
   static constexpr int kPC = (kCodeGroups + kWaves - 1) / kWaves, kPS = (kScaleGroups + kWaves - 1) / kWaves;
-  static constexpr int kLoads = kPC + kPS;
-  static constexpr size_t kLds = S * static_cast<size_t>(kStage);
-  static_assert(kRows % 32 == 0 && kBM % 16 == 0, "whole groups");
-  static_assert((S - 2) * kLoads < 64, "the wait counter has six bits");
+  static constexpr size_t kLds = S * static_cast<size_t>(kStage) + 2 * kScales;
+  static_assert(S == 2 || S == 3, "two buffers of scales serve up to three stages of codes");
+  static_assert(kBM % 8 == 0 && kBN % 64 == 0, "whole groups");
 };
 
 __device__ __forceinline__ int64_t clamp32(int64_t n) { return n < 0xfffffff0ll ? n : 0xfffffff0ll; }
@@ -292,6 +295,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
   using C = TileCfg<WM, WN, TM, TN, S>;
   constexpr int NM = ACT == MX_ACT_SWIGLU ? 2 : 1;
   constexpr int kCols = C::kBN / NM;                       // outputs of a block
+  static_assert(kCols % 64 == 0, "a group of scales is of one matrix");
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r = lane & 15, q = lane >> 4;
@@ -362,7 +366,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
       return static_cast<uint32_t>(NM == 2 && row >= kCols ? row - kCols : row);
     };
     // this wave's loads: a lane takes piece lane mod 8 of row lane / 8 of its
-    // group; of scales word lane mod 2 of row lane / 2
+    // group; of scales 16 bytes of row lane (with an odd number of chunks the
+    // last 8 of them lie past the row's end and are not used)
     uint32_t vc[C::kPC], vs[C::kPS];
 #pragma unroll
     for (int i = 0; i < C::kPC; ++i) {
@@ -374,7 +379,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
     for (int i = 0; i < C::kPS; ++i) {
       int g = wave + i * C::kWaves;
       g = g < C::kScaleGroups ? g : C::kScaleGroups - 1;
-      vs[i] = row_at(g * 32 + (lane >> 1)) * spitch + static_cast<uint32_t>((lane & 1) * 4);
+      const int row = g * 64 + lane;
+      vs[i] = row_at(g >= C::kAScales ? row - C::kAScales * 64 + C::kBM : row < C::kBM ? row : C::kBM - 1) * spitch;
     }
     const auto fetch = [&](int chunk, int buf) {
       uint8_t* st = smem + buf * C::kStage;
@@ -386,40 +392,43 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
         const u32x4 rs = row < C::kBM ? ra : (NM == 2 && row >= C::kBM + kCols ? rw[NM - 1] : rw[0]);
         lds_load<16>(rs, st + g * 1024, vc[i], chunk * 128);
       }
+      if (chunk & 1) return;
+      uint8_t* ss = smem + S * C::kStage + (chunk >> 1 & 1) * C::kScales;
 #pragma unroll
       for (int i = 0; i < C::kPS; ++i) {
         int g = wave + i * C::kWaves;
         g = g < C::kScaleGroups ? g : C::kScaleGroups - 1;
-        const int row = g * 32;
-        uint8_t* to = st + C::kRows * 128 + g * 256;
-        const u32x4 rs = row < C::kBM ? ras : (NM == 2 && row >= C::kBM + kCols ? rws[NM - 1] : rws[0]);
-        lds_load<4>(rs, to, vs[i], chunk * 8);
+        const int row = (g - C::kAScales) * 64;   // of W
+        const u32x4 rs = g < C::kAScales ? ras : (NM == 2 && row >= kCols ? rws[NM - 1] : rws[0]);
+        lds_load<16>(rs, ss + g * 1024, vs[i], chunk * 8);
       }
     };
-    static_assert(C::kBM % 32 == 0 && kCols % 32 == 0, "a group of scales is of one operand");
 
 #pragma unroll
     for (int c = 0; c < S - 1; ++c)
       if (c < a.chunks) fetch(c, c);
     int buf = 0;
     for (int chunk = 0; chunk < a.chunks; ++chunk) {
-      if (chunk + S - 2 < a.chunks) wait_loads<(S - 2) * C::kLoads>();
-      else wait_loads<0>();
+      // S = 3: the next chunk's loads, with scales if it is even, may be on
+      // their way still
+      if (S == 2 || chunk + 1 >= a.chunks) wait_loads<0>();
+      else if (chunk & 1) wait_loads<C::kPC + C::kPS>();
+      else wait_loads<C::kPC>();
       __syncthreads();   // the chunk has arrived everywhere, and the stage before it is read to its end
       if (chunk + S - 1 < a.chunks) fetch(chunk + S - 1, buf == 0 ? S - 1 : buf - 1);
       const uint8_t* st = smem + buf * C::kStage;
-      const uint8_t* ss = st + C::kRows * 128;
+      const uint8_t* ss = smem + S * C::kStage + (chunk >> 1 & 1) * C::kScales + (chunk & 1) * 8;
       buf = buf + 1 == S ? 0 : buf + 1;
       int sa[TM], sw[TN];
 #pragma unroll
       for (int i = 0; i < TM; ++i)
-        sa[i] = *reinterpret_cast<const uint16_t*>(ss + ((wm * TM + i) * 16 + r) * 8 + q * 2);
+        sa[i] = *reinterpret_cast<const uint16_t*>(ss + ((wm * TM + i) * 16 + r) * 16 + q * 2);
       const auto wrow = [&](int j) {   // W rows of this wave's tile j: with SWIGLU gate and up tiles in turn
         return NM == 1 ? (wn * TN + j) * 16 : (j & 1) * kCols + (wn * (TN / 2) + j / 2) * 16;
       };
 #pragma unroll
       for (int j = 0; j < TN; ++j)
-        sw[j] = *reinterpret_cast<const uint16_t*>(ss + (C::kBM + wrow(j) + r) * 8 + q * 2);
+        sw[j] = *reinterpret_cast<const uint16_t*>(ss + (C::kAScales * 64 + wrow(j) + r) * 16 + q * 2);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int at = ((2 * q + s) ^ (r & 7)) << 4;
