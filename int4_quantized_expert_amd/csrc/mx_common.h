@@ -28,60 +28,74 @@ __device__ __forceinline__ float mx_scale_f32(uint32_t byte) {
   return __uint_as_float(byte == 0u ? 0x00400000u : (byte == 255u ? 0x7fc00000u : byte << 23));
 }
 
-// Eight values over the block's power of two as eight codes, the first in the
-// lowest four bits.  The conversion divides by the power exactly, rounds to
-// nearest with ties to even and saturates at 6 (checked against the formula
-// over all exponents); a block of scale byte 255 gets zero codes.
-__device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], uint32_t byte) {
-  const float s = mx_scale_f32(byte);
-  uint32_t c = 0;
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0], v[1], s, 0);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], s, 1);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], s, 2);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], s, 3);
-  return byte == 255u ? 0u : c;
-}
+// Eight values of a row as they are stored: fp32, or pairs of bf16.
+template <int DT>
+struct Eight {
+  uint32_t w[DT == kF32 ? 8 : 4];
+};
 
 // Eight values from element c of a row of `cols`; zeros past its end.  The
 // row's start is aligned to the element only.
 template <int DT>
-__device__ __forceinline__ void mx_load8(const void* base, int64_t row, int64_t c, int64_t cols, float (&v)[8]) {
+__device__ __forceinline__ void mx_load8(const void* base, int64_t row, int64_t c, int64_t cols, Eight<DT>& v) {
+  constexpr int kWords = DT == kF32 ? 8 : 4;
   if constexpr (DT == kF32) {
     const float* p = static_cast<const float*>(base) + row;
-    if (c + 8 <= cols) {
-      uint32_t w[8];
-      __builtin_memcpy(w, p + c, 32);
+    if (c + 8 <= cols) __builtin_memcpy(v.w, p + c, 32);
+    else
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? p[c + i] : 0.f;
-    }
+      for (int i = 0; i < 8; ++i) v.w[i] = c + i < cols ? __float_as_uint(p[c + i]) : 0u;
   } else {
     const uint16_t* p = static_cast<const uint16_t*>(base) + row;
-    if (c + 8 <= cols) {
-      uint32_t w[4];
-      __builtin_memcpy(w, p + c, 16);
+    if (c + 8 <= cols) __builtin_memcpy(v.w, p + c, 16);
+    else
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? bf16_to_f32(p[c + i]) : 0.f;
-    }
+      for (int i = 0; i < kWords; ++i)
+        v.w[i] = (c + 2 * i < cols ? p[c + 2 * i] : 0u) | ((c + 2 * i + 1 < cols ? p[c + 2 * i + 1] : 0u) << 16);
   }
 }
 
-__device__ __forceinline__ uint32_t mx_mag8(const float (&v)[8]) {
-  uint32_t m = 0;
+// The largest magnitude's fp32 bits (as whole numbers NaN > inf > any number).
+template <int DT>
+__device__ __forceinline__ uint32_t mx_mag8(const Eight<DT>& v) {
+  if constexpr (DT == kF32) {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = __float_as_uint(v[i]) & 0x7fffffffu;   // as whole numbers NaN > inf > any number
-    m = b > m ? b : m;
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t b = v.w[i] & 0x7fffffffu;
+      m = b > m ? b : m;
+    }
+    return m;
+  } else {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v.w[i] & 0x7fff7fffu));
+    return static_cast<uint32_t>(m[0] > m[1] ? m[0] : m[1]) << 16;
   }
-  return m;
+}
+
+// Eight values over the block's power of two as eight codes, the first in the
+// lowest four bits.  The conversions divide by the power exactly, round to
+// nearest with ties to even and saturate at 6 (checked against the formula
+// over all exponents); a block of scale byte 255 gets zero codes.
+template <int DT>
+__device__ __forceinline__ uint32_t mx_codes8(const Eight<DT>& v, uint32_t byte) {
+  const float s = mx_scale_f32(byte);
+  uint32_t c = 0;
+  if constexpr (DT == kF32) {
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(v.w[0]), __uint_as_float(v.w[1]), s, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(v.w[2]), __uint_as_float(v.w[3]), s, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(v.w[4]), __uint_as_float(v.w[5]), s, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, __uint_as_float(v.w[6]), __uint_as_float(v.w[7]), s, 3);
+  } else {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, v.w[0]), s, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, v.w[1]), s, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, v.w[2]), s, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, v.w[3]), s, 3);
+  }
+  return byte == 255u ? 0u : c;
 }
 
 // Piece p (eight values) of the padded matrix -> its row and column.
@@ -103,7 +117,7 @@ __device__ __forceinline__ void mx_quantize_piece(const void* x, int64_t stride,
   if (p >= pieces) return;   // pieces of a block are whole: per_row is a multiple of 32
   const int lane = threadIdx.x & (kWave - 1);
   const Piece at = piece_at(p, per_row);
-  float v[8];
+  Eight<DT> v;
   mx_load8<DT>(x, at.row * stride, at.col, cols, v);
   uint32_t m = mx_mag8(v);
   uint32_t o = lane_xor<1>(m, lane);

@@ -26,7 +26,6 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr int kMxF4 = 2;                 // a_dtype code MX_FP4
 constexpr int kChunk = kMxPad;           // k values per step
-constexpr int kNarrowWaves = 8;
 constexpr int kDirectPairs = 128;        // pairs that the kernels group by themselves
 
 enum Mode { kDense, kDirect, kTiles, kSum };
@@ -81,78 +80,143 @@ struct Part {
 };
 
 template <int SRC>
-__device__ __forceinline__ void load_part(const void* a, const uint8_t* as, int64_t row, bool on, int chunk, int q, int K,
-                                          int chunks, Part& p) {
-  if (!on) {
-    p.c[0] = p.c[1] = v4i{0, 0, 0, 0};
-    p.sc = 0;
-    return;
-  }
-  if constexpr (SRC == kMxF4) {
-    const v4i* c = reinterpret_cast<const v4i*>(static_cast<const uint8_t*>(a) + (row * chunks + chunk) * 128 + q * 32);
+struct Stored {
+  typedef uint32_t T;
+};
+template <>
+struct Stored<kBF16> {
+  typedef uint16_t T;
+};
+
+// The same as it is stored: an MX matrix's codes, or values still to quantise.
+template <int SRC>
+struct RawPart {
+  Eight<SRC> v[2][4];
+};
+template <>
+struct RawPart<kMxF4> {
+  Part p;
+};
+
+// A part from a wave-uniform base and a lane's offset (scalar base, 32-bit
+// offset loads; the address arithmetic of cold kernels counts).  Codes: bytes
+// from the chunk's first; values: elements from the row's chunk, `left` of them
+// to the row's end.
+__device__ __forceinline__ void load_codes(const uint8_t* codes, const uint8_t* scales, uint32_t co, uint32_t so, bool on,
+                                           Part& p) {
+  if (on) {
+    const v4i* c = reinterpret_cast<const v4i*>(codes + co);
     p.c[0] = c[0];
     p.c[1] = c[1];
-    p.sc = *reinterpret_cast<const uint16_t*>(as + (row * chunks + chunk) * 8 + q * 2);
+    p.sc = *reinterpret_cast<const uint16_t*>(scales + so);
   } else {
-    int sc = 0;
+    p.c[0] = p.c[1] = v4i{0, 0, 0, 0};
+    p.sc = 0;
+  }
+}
+
+template <int SRC>
+__device__ __forceinline__ void load_values(const void* base, int64_t at, int left, bool on, RawPart<SRC>& p) {
+  // one test for the lane's 64 values, so that the usual path is short and in
+  // one piece (a cold kernel waits for its instructions)
+  const auto* src = static_cast<const typename Stored<SRC>::T*>(base) + at;
+  if (on && left >= 64) {
+    __builtin_memcpy(p.v, src, sizeof(p.v));
+  } else {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (on) mx_load8<SRC>(src, 0, b * 32 + i * 8, left, p.v[b][i]);
+        else p.v[b][i] = Eight<SRC>{};
+      }
+  }
+}
+
+template <int SRC>
+__device__ __forceinline__ Part finish_part(const RawPart<SRC>& p) {
+  if constexpr (SRC == kMxF4) {
+    return p.p;
+  } else {
+    Part o;
+    o.sc = 0;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      float v[4][8];
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        mx_load8<SRC>(a, row * K, static_cast<int64_t>(chunk) * kChunk + q * 64 + b * 32 + i * 8, K, v[i]);
-        const uint32_t o = mx_mag8(v[i]);
-        m = o > m ? o : m;
+        const uint32_t x = mx_mag8(p.v[b][i]);
+        m = x > m ? x : m;
       }
       const uint32_t byte = mx_scale_byte(m);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p.c[b][i] = static_cast<int>(mx_codes8(v[i], byte));
-      sc |= static_cast<int>(byte) << (8 * b);
+      for (int i = 0; i < 4; ++i) o.c[b][i] = static_cast<int>(mx_codes8(p.v[b][i], byte));
+      o.sc |= static_cast<int>(byte) << (8 * b);
     }
-    p.sc = sc;
+    return o;
   }
+}
+
+__device__ __forceinline__ int64_t readlane64(int64_t v, int l) {
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(v & 0xffffffff), l);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(v >> 32), l);
+  return static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+__device__ __forceinline__ float readlane_f(float v, int l) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
 }
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
+// Round to nearest even in one instruction.
+__device__ __forceinline__ uint16_t to_bf16(float y) { return __builtin_bit_cast(uint16_t, static_cast<__bf16>(y)); }
+
 __device__ __forceinline__ void store_out(void* out, int64_t i, float y, int bf16) {
-  if (bf16) static_cast<uint16_t*>(out)[i] = f32_to_bf16(y);
+  if (bf16) static_cast<uint16_t*>(out)[i] = to_bf16(y);
   else static_cast<float*>(out)[i] = y;
 }
 
-// Few rows of A: a block forms 16 outputs of up to 16 rows (kSum: of one
+// Few rows of A: a block forms 16 outputs of up to 16 MT rows (kSum: of one
 // token), its waves take the chunks of k in turn and their sums are joined in
-// LDS.  Bound by the reads of W; A is read (and quantised) by every block.
-//   kDense   rows 16 y .. of A
-//   kDirect  y is a pair; the block of the first pair of an expert
-//            takes all of that expert's pairs, the others end
+// LDS.  Bound by the reads of W and the chain of dependent loads before them
+// (ids, slots); A is read, and quantised, by every block, while W is on its way.
+//   kDense   rows 16 MT y .. of A
+//   kDirect  y is a pair; the block of the first pair of an expert takes all
+//            of that expert's pairs, the others end
 //   kTiles   y is a tile of the grouped list
 //   kSum     y is a token; its experts' products are summed with their weights
-template <int SRC, int ACT, int MODE>
-__global__ __launch_bounds__(kNarrowWaves* kWave) void k_mx_narrow(MxArgs a) {
+template <int SRC, int ACT, int MODE, int MT, int NW>
+__global__ __launch_bounds__(NW* kWave) void k_mx_narrow(MxArgs a) {
   constexpr int NM = ACT == MX_ACT_SWIGLU ? 2 : 1;
-  __shared__ __align__(16) float red[NM][kNarrowWaves][16][20];   // 20: four-float stores, fewer bank conflicts
+  static_assert(MT == 1 || (MODE == kDense && SRC == kMxF4), "more row tiles are for the dense product of codes");
+  __shared__ __align__(16) float red[NM][NW][16][20];   // 20: four-float stores, fewer bank conflicts
   __shared__ int32_t list[kDirectPairs];
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r = lane & 15, q = lane >> 4;
   const int y = blockIdx.x / a.nblk, bx = blockIdx.x % a.nblk;
   const int n0 = bx * 16;
-  const int wrow = n0 + r < a.N ? n0 + r : a.N - 1;   // a row past the end is read again and not stored
+  const uint32_t pitch = a.chunks * 128u, spitch = a.chunks * 8u;
+  const uint32_t wr = n0 + r < a.N ? r : a.N - 1 - n0;   // a row past the end is read again and not stored
+  const uint32_t wco = wr * pitch + q * 32, wso = wr * spitch + q * 2;
+  const int64_t wc0 = n0 * static_cast<int64_t>(pitch), ws0 = n0 * static_cast<int64_t>(spitch);
 
   // where the rows come from, and where they go
   int count = 0;
   int64_t off = 0;
   const int32_t* pairs = nullptr;
+  int64_t offs = 0;    // kSum: lane i has expert i's blob and weight
+  float wts = 0.f;
   if constexpr (MODE == kDense) {
-    count = a.M - y * 16;
-    count = count < 16 ? count : 16;
+    count = a.M - y * 16 * MT;
+    count = count < 16 * MT ? count : 16 * MT;
   } else if constexpr (MODE == kDirect) {
-    const int p = y, e = a.ids[p];
-    const uint64_t b0 = __ballot(lane < a.M && a.ids[lane < a.M ? lane : 0] == e);
-    const uint64_t b1 = __ballot(lane + kWave < a.M && a.ids[lane + kWave < a.M ? lane + kWave : 0] == e);
+    const int i0 = a.ids[lane < a.M ? lane : 0], i1 = a.ids[lane + kWave < a.M ? lane + kWave : 0];
+    const int e = __builtin_amdgcn_readlane(y < kWave ? i0 : i1, y & (kWave - 1));
+    const uint64_t b0 = __ballot(lane < a.M && i0 == e), b1 = __ballot(lane + kWave < a.M && i1 == e);
     const int first = b0 ? __ffsll(static_cast<unsigned long long>(b0)) - 1 : kWave + __ffsll(static_cast<unsigned long long>(b1)) - 1;
-    if (first != p) return;
+    if (first != y) return;
+    off = blob_of(a.slots, e, a.E, a.need, a.pool_bytes);
     count = __popcll(b0) + __popcll(b1);
     if (wave == 0) {
       if ((b0 >> lane) & 1ull) list[__popcll(b0 & lane_mask_lt(lane))] = lane;
@@ -160,7 +224,6 @@ __global__ __launch_bounds__(kNarrowWaves* kWave) void k_mx_narrow(MxArgs a) {
     }
     __syncthreads();
     pairs = list;
-    off = blob_of(a.slots, e, a.E, a.need, a.pool_bytes);
     if (off < 0 && tid == 0 && bx == 0) atomicOr(a.flags, 1u);
   } else if constexpr (MODE == kTiles) {
     if (y >= *a.ntiles) return;
@@ -170,84 +233,129 @@ __global__ __launch_bounds__(kNarrowWaves* kWave) void k_mx_narrow(MxArgs a) {
     pairs = a.plist + t.first;
   } else {
     count = 1;
+    if (lane < a.k) {
+      const int e = a.ids[y * a.k + lane];
+      wts = a.wts[y * a.k + lane];
+      offs = blob_of(a.slots, e, a.E, a.need, a.pool_bytes);
+      if (offs < 0 && wave == 0 && bx == 0) atomicOr(a.flags, 1u);
+    }
   }
 
   for (int g0 = 0; g0 < (MODE == kDirect ? count : 1); g0 += 16) {
     const int here = MODE == kDirect ? (count - g0 < 16 ? count - g0 : 16) : count;
-    const bool on = r < here;
-    int64_t row = 0, dst = 0;
-    if constexpr (MODE == kDense) {
-      row = dst = static_cast<int64_t>(y) * 16 + r;
-    } else if constexpr (MODE == kDirect || MODE == kTiles) {
-      const int p = on ? pairs[g0 + r] : 0;
-      row = a.pair_rows ? p : p / a.k;
-      dst = p;
-    }
-    v4f acc[NM];
+    // A's rows: kDense and kSum from a uniform base, the others by the list
+    int64_t row0 = 0;
+    int64_t row[MT];
 #pragma unroll
-    for (int m = 0; m < NM; ++m) acc[m] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < MT; ++t) row[t] = t * 16 + r;
+    if constexpr (MODE == kDense) row0 = static_cast<int64_t>(y) * 16 * MT;
+    if constexpr (MODE == kDirect || MODE == kTiles) {
+      const int p = r < here ? pairs[g0 + r] : 0;
+      row[0] = a.pair_rows ? p : p / a.k;
+    }
+    v4f acc[MT][NM];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int m = 0; m < NM; ++m) acc[t][m] = v4f{0.f, 0.f, 0.f, 0.f};
     const int tasks = MODE == kSum ? a.k * a.chunks : a.chunks;
-    if (off >= 0) {
-      for (int task = wave; task < tasks; task += kNarrowWaves) {
-        int chunk = task;
-        const uint8_t *wc = a.wc, *wsc = a.wsc;
-        float w = 1.f;
-        if constexpr (MODE == kSum) {
-          const int i = task / a.chunks;
-          chunk = task - i * a.chunks;
-          const int t = y;
-          const int e = a.ids[t * a.k + i];
-          const int64_t o = blob_of(a.slots, e, a.E, a.need, a.pool_bytes);
-          if (o < 0) {
-            if (lane == 0 && bx == 0) atomicOr(a.flags, 1u);
-            continue;
-          }
-          w = a.wts[t * a.k + i];
-          row = a.pair_rows ? t * a.k + i : t;
-          wc = a.pool + o + a.codes_off;
-          wsc = a.pool + o + a.scales_off;
-        } else if constexpr (MODE != kDense) {
-          wc = a.pool + off + a.codes_off;
-          wsc = a.pool + off + a.scales_off;
-        }
-        Part A, W[NM];
-#pragma unroll
-        for (int m = 0; m < NM; ++m)
-          load_part<kMxF4>(wc, wsc, wrow + m * static_cast<int64_t>(a.N), true, chunk, q, a.K, a.chunks, W[m]);
-        load_part<SRC>(a.a, a.as, row, on, chunk, q, a.K, a.chunks, A);
-        v4f d[NM];
-#pragma unroll
-        for (int m = 0; m < NM; ++m) {
-          d[m] = MODE == kSum ? v4f{0.f, 0.f, 0.f, 0.f} : acc[m];
-          d[m] = mfma4(W[m].c[0], A.c[0], d[m], W[m].sc, A.sc, 0);
-          d[m] = mfma4(W[m].c[1], A.c[1], d[m], W[m].sc, A.sc, 1);
-          if constexpr (MODE == kSum) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[m][i] = fmaf(w, d[m][i], acc[m][i]);
-          } else {
-            acc[m] = d[m];
-          }
-        }
+
+    // one task: a chunk of k (kSum: of one expert)
+    RawPart<SRC> A[MT];
+    RawPart<kMxF4> W[NM];
+    float w = 1.f;
+    const auto load = [&](int task) {
+      int chunk = task;
+      const uint8_t *wc = a.wc, *wsc = a.wsc;
+      bool usable = true;
+      int64_t o = off;
+      if constexpr (MODE == kSum) {
+        const int i = task / a.chunks;
+        chunk = task - i * a.chunks;
+        row0 = a.pair_rows ? static_cast<int64_t>(y) * a.k + i : y;
+        o = readlane64(offs, i);
+        w = readlane_f(wts, i);
       }
+      if constexpr (SRC == kMxF4) {
+        const uint8_t* ac = static_cast<const uint8_t*>(a.a) + row0 * pitch + chunk * 128;
+        const uint8_t* as = a.as + row0 * spitch + chunk * 8;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          if constexpr (MODE == kTiles) load_codes(ac + row[t] * pitch, as + row[t] * spitch, q * 32, q * 2, r < here, A[t].p);
+          else load_codes(ac, as, static_cast<uint32_t>(row[t]) * pitch + q * 32, static_cast<uint32_t>(row[t]) * spitch + q * 2,
+                          t * 16 + r < here, A[t].p);
+        }
+      } else {
+        const int c0 = chunk * kChunk + q * 64;
+        const auto* av = static_cast<const typename Stored<SRC>::T*>(a.a) + row0 * a.K;
+        load_values<SRC>(av, row[0] * a.K + c0, a.K - c0, r < here, A[0]);
+      }
+      if constexpr (MODE != kDense) {
+        usable = o >= 0;
+        wc = a.pool + o + a.codes_off;
+        wsc = a.pool + o + a.scales_off;
+      }
+      wc += wc0 + chunk * 128;
+      wsc += ws0 + chunk * 8;
+#pragma unroll
+      for (int m = 0; m < NM; ++m)
+        load_codes(wc + m * a.N * static_cast<int64_t>(pitch), wsc + m * a.N * static_cast<int64_t>(spitch), wco, wso, usable,
+                   W[m].p);
+    };
+    // the next task's loads are requested before this one is multiplied
+    bool have = false;
+    for (int task = wave;; task += NW) {
+      Part pa[MT], pw[NM];
+      const float w0 = w;
+      if (have) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) pa[t] = finish_part<SRC>(A[t]);
+#pragma unroll
+        for (int m = 0; m < NM; ++m) pw[m] = W[m].p;
+      }
+      const bool more = task < tasks;
+      if (more) load(task);
+      if (have) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int m = 0; m < NM; ++m) {
+            v4f d = MODE == kSum ? v4f{0.f, 0.f, 0.f, 0.f} : acc[t][m];
+            d = mfma4(pw[m].c[0], pa[t].c[0], d, pw[m].sc, pa[t].sc, 0);
+            d = mfma4(pw[m].c[1], pa[t].c[1], d, pw[m].sc, pa[t].sc, 1);
+            if constexpr (MODE == kSum) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[t][m][i] = fmaf(w0, d[i], acc[t][m][i]);
+            } else {
+              acc[t][m] = d;
+            }
+          }
+      }
+      if (!more) break;
+      have = true;
     }
 #pragma unroll
-    for (int m = 0; m < NM; ++m) *reinterpret_cast<v4f*>(&red[m][wave][r][4 * q]) = acc[m];
-    __syncthreads();
-    if (tid < 256) {
-      const int tr = tid >> 4, n = tid & 15;
-      if (tr < here && n0 + n < a.N) {
-        float v[NM];
+    for (int t = 0; t < MT; ++t) {
+      if (t > 0) __syncthreads();
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
-          v[m] = 0.f;
+      for (int m = 0; m < NM; ++m) *reinterpret_cast<v4f*>(&red[m][wave][r][4 * q]) = acc[t][m];
+      __syncthreads();
+      if (tid < 256) {
+        const int tr = tid >> 4, n = tid & 15;
+        if (t * 16 + tr < here && n0 + n < a.N) {
+          float v[NM];
 #pragma unroll
-          for (int w = 0; w < kNarrowWaves; ++w) v[m] += red[m][w][tr][n];
+          for (int m = 0; m < NM; ++m) {
+            v[m] = 0.f;
+#pragma unroll
+            for (int x = 0; x < NW; ++x) v[m] += red[m][x][tr][n];
+          }
+          int64_t to;
+          if constexpr (MODE == kDense) to = static_cast<int64_t>(y) * 16 * MT + t * 16 + tr;
+          else if constexpr (MODE == kSum) to = y;
+          else to = pairs[g0 + tr];
+          store_out(a.out, to * a.N + n0 + n, NM == 2 ? silu(v[0]) * v[NM - 1] : v[0], a.out_bf16);
         }
-        int64_t to;
-        if constexpr (MODE == kDense) to = static_cast<int64_t>(y) * 16 + tr;
-        else if constexpr (MODE == kSum) to = y;
-        else to = pairs[g0 + tr];
-        store_out(a.out, to * a.N + n0 + n, NM == 2 ? silu(v[0]) * v[NM - 1] : v[0], a.out_bf16);
       }
     }
     if (MODE == kDirect) __syncthreads();
@@ -461,8 +569,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
       if (whole && n + 4 <= a.N) {
         if (a.out_bf16) {
           uint2 w;
-          w.x = f32_to_bf16(y[0]) | (static_cast<uint32_t>(f32_to_bf16(y[1])) << 16);
-          w.y = f32_to_bf16(y[2]) | (static_cast<uint32_t>(f32_to_bf16(y[3])) << 16);
+          w.x = to_bf16(y[0]) | (static_cast<uint32_t>(to_bf16(y[1])) << 16);
+          w.y = to_bf16(y[2]) | (static_cast<uint32_t>(to_bf16(y[3])) << 16);
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to + n) = w;
         } else {
           *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to + n) = float4{y[0], y[1], y[2], y[3]};
@@ -724,20 +832,31 @@ int launched() {
   return api_fail(MOE_EHIP, buf);
 }
 
-template <int SRC, int MODE>
-void narrow_act(const MxArgs& a, int act, dim3 grid, hipStream_t s) {
-  const dim3 block(kNarrowWaves * kWave);
-  if (act == MX_ACT_SWIGLU) launch_kernel(k_mx_narrow<SRC, MX_ACT_SWIGLU, MODE>, grid, block, 0, s, a);
-  else launch_kernel(k_mx_narrow<SRC, MX_ACT_NONE, MODE>, grid, block, 0, s, a);
+template <int SRC, int MODE, int MT, int NW>
+void narrow_act(const MxArgs& a, int act, uint32_t blocks, hipStream_t s) {
+  const dim3 grid(blocks), block(NW * kWave);
+  if (act == MX_ACT_SWIGLU) launch_kernel(k_mx_narrow<SRC, MX_ACT_SWIGLU, MODE, MT, NW>, grid, block, 0, s, a);
+  else launch_kernel(k_mx_narrow<SRC, MX_ACT_NONE, MODE, MT, NW>, grid, block, 0, s, a);
 }
 
-template <int MODE>
+template <int MODE, int MT, int NW>
+void narrow_src(const MxArgs& a, int src, int act, uint32_t blocks, hipStream_t s) {
+  // more row tiles than one take codes: their values do not fit the registers
+  if (MT > 1 || src == kMxF4) narrow_act<kMxF4, MODE, MT, NW>(a, act, blocks, s);
+  else if (src == kF32) narrow_act<kF32, MODE, 1, NW>(a, act, blocks, s);
+  else narrow_act<kBF16, MODE, 1, NW>(a, act, blocks, s);
+}
+
+template <int MODE, int MT = 1>
 void narrow(MxArgs a, int src, int act, int ny, hipStream_t s) {
   a.nblk = (a.N + 15) / 16;
-  const dim3 grid(static_cast<uint32_t>(a.nblk) * ny);
-  if (src == kF32) narrow_act<kF32, MODE>(a, act, grid, s);
-  else if (src == kBF16) narrow_act<kBF16, MODE>(a, act, grid, s);
-  else narrow_act<kMxF4, MODE>(a, act, grid, s);
+  const uint32_t blocks = static_cast<uint32_t>(a.nblk) * ny;
+  const int tasks = a.chunks * (MODE == kSum ? a.k : 1);
+  // a wave's instructions cost more than its loads: four waves with two tasks
+  // each take 8.1 us where eight with one take 10.2 (ten experts' gate and up
+  // rows, 512 outputs, k = 2048); longer rows need eight to hide their loads
+  if (tasks <= 8) narrow_src<MODE, MT, 4>(a, src, act, blocks, s);
+  else narrow_src<MODE, MT, 8>(a, src, act, blocks, s);
 }
 
 template <int WM, int WN, int TM, int TN, int S, bool EXPERTS>
@@ -822,6 +941,11 @@ int mx_linear_forward(const mx_product_desc* d, int32_t M, const void* a, const 
     launch_mx_quantize(d->a_dtype, M, d->k, a, d->k, ws + L.codes, ws + L.scales, s);
     g.a = ws + L.codes;
     g.as = ws + L.scales;
+  }
+  if (M <= 64) {
+    if (M <= 32) narrow<kDense, 2>(g, MX_FP4, d->act, 1, s);
+    else narrow<kDense, 4>(g, MX_FP4, d->act, 1, s);
+    return launched();
   }
   const auto tiles = [&](int bm, int bn) {
     return static_cast<int64_t>((M + bm - 1) / bm) * ((wrows + bn - 1) / bn);

@@ -25,15 +25,13 @@ __global__ __launch_bounds__(kQThr) void k_mx_quantize(const void* x, int64_t st
                                                        int64_t pieces, uint32_t* codes, uint8_t* scales) {
   const int lane = threadIdx.x & (kWave - 1);
   const int64_t p0 = static_cast<int64_t>(blockIdx.x) * (kQThr * kIter) + threadIdx.x;
-  float v[kIter][8];
+  Eight<DT> v[kIter];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
     const int64_t p = p0 + i * kQThr;
     const Piece at = piece_at(p < pieces ? p : 0, per_row);
     if (p < pieces) mx_load8<DT>(x, at.row * stride, at.col, cols, v[i]);
-    else
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    else v[i] = Eight<DT>{};
   }
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
