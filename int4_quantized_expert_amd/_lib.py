@@ -370,13 +370,16 @@ MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 
 _torch = None
 _raw_stream = None
+_current_device = None
 
 
 def _load_torch():
-    """torch, imported at the first call that needs it, and the cheapest way to the current stream's handle: building a
-    torch.cuda.Stream takes 2.7 us of a call that otherwise takes about 5."""
-    global _torch, _raw_stream
+    """torch, imported at the first call that needs it, and the cheapest ways to the current device and its stream's
+    handle: building a torch.cuda.Stream takes 2.7 us of a call that otherwise takes about 5."""
+    global _torch, _raw_stream, _current_device
     import torch
+    torch.cuda.is_available() and torch.cuda.init()
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda i: torch.cuda.current_stream(i).cuda_stream)
     _torch = torch
@@ -392,34 +395,40 @@ def _torch_dtype(code: int):
     return torch.float32 if code == MOE_F32 else torch.bfloat16
 
 
+def _fits(t, dtype, need: int) -> bool:
+    """Whether t is a contiguous tensor of at least `need` elements of `dtype` (None and addresses pass)."""
+    return t is None or type(t) is int or (t.dtype is dtype and t.numel() >= need and t.is_contiguous())
+
+
+def _misfit(name: str, t, dtype, need: int):
+    if t.dtype is not dtype:
+        _bad(f"{name} is {t.dtype}, {dtype} expected")
+    if not t.is_contiguous():
+        _bad(f"{name} is not contiguous")
+    _bad(f"{name} has {t.numel()} elements, {need} needed")
+
+
 def _check_tensor(name: str, t, dtype, need: int) -> None:
-    """A contiguous device tensor of at least `need` elements of `dtype` (None and addresses pass)."""
-    if t is None or type(t) is int:
-        return
-    if t.dtype != dtype or t.numel() < need or not t.is_contiguous():
-        if t.dtype != dtype:
-            _bad(f"{name} is {t.dtype}, {dtype} expected")
-        if not t.is_contiguous():
-            _bad(f"{name} is not contiguous")
-        _bad(f"{name} has {t.numel()} elements, {need} needed")
+    if not _fits(t, dtype, need):
+        _misfit(name, t, dtype, need)
 
 
 def _call_on(tensors, stream, fn, *args) -> None:
     """fn(*args, stream) on the device that the tensors share; stream None: torch's current one there."""
-    torch = _torch or _load_torch()
-    dev = None
+    if _torch is None:
+        _load_torch()
+    dev = -2
     for t in tensors:
-        if t is None or type(t) is int:
-            continue
-        i = t.get_device()
-        if i < 0:
-            _bad(f"a tensor is on {t.device}, not on a GPU")
-        if dev is None:
-            dev = i
-        elif i != dev:
-            _bad(f"tensors on device {dev} and device {i}")
-    here = torch.cuda.current_device()
-    if dev is None:
+        if t is not None and type(t) is not int:
+            i = t.get_device()
+            if i != dev:
+                if i < 0:
+                    _bad(f"a tensor is on {t.device}, not on a GPU")
+                if dev >= 0:
+                    _bad(f"tensors on device {dev} and device {i}")
+                dev = i
+    here = _current_device()
+    if dev < 0:
         dev = here
     if stream is None:
         stream = _raw_stream(dev)
@@ -428,7 +437,7 @@ def _call_on(tensors, stream, fn, *args) -> None:
     if dev == here:
         rc = fn(*args, stream)
     else:
-        with torch.cuda.device(dev):
+        with _torch.cuda.device(dev):
             rc = fn(*args, stream)
     if rc != 0:
         raise MoeError(rc, last_error())
@@ -448,13 +457,14 @@ def route(r: RouteDesc, T: int, logits, bias, topk_ids, topk_w, logits_stride=No
     torch = _torch or _load_torch()
     E, k = r.n_experts, r.top_k
     if type(logits) is not int:
-        if logits.dim() != 2 or logits.shape[0] < T or logits.shape[1] < E or (E > 1 and logits.stride(1) != 1):
+        shape, strides = logits.shape, logits.stride()
+        if len(shape) != 2 or shape[0] < T or shape[1] < E or (E > 1 and strides[1] != 1):
             _bad(f"logits of shape {tuple(logits.shape)}, strides {logits.stride()}: rows of {E} adjacent values expected")
         if logits.dtype != _torch_dtype(r.logit_dtype):
             _bad(f"logits is {logits.dtype}, {_torch_dtype(r.logit_dtype)} expected")
         if logits_stride is None:
-            logits_stride = logits.stride(0)
-        elif T > 1 and logits_stride != logits.stride(0):
+            logits_stride = strides[0]
+        elif T > 1 and logits_stride != strides[0]:
             _bad(f"logits_stride={logits_stride} differs from the tensor's {logits.stride(0)}")
     elif logits_stride is None:
         logits_stride = E
@@ -478,35 +488,43 @@ def router_route(d: MoeDesc, r: RouteDesc, T: int, x, router_w, bias, topk_ids, 
 
 def mx_shapes(rows: int, cols: int) -> tuple[tuple[int, int], tuple[int, int]]:
     """Shapes of the uint8 codes and scales tensors of an MX matrix [rows, cols]."""
+    padded = _mx_padded(rows, cols)
+    return (rows, padded // 2), (rows, padded // 32)
+
+
+def _mx_padded(rows: int, cols: int) -> int:
     if not (0 <= rows < 1 << 31 and 0 <= cols <= 1 << 20):
         _bad(f"an MX matrix of {rows} x {cols} is negative or too large")
-    padded = -(-cols // 256) * 256
-    return (rows, padded // 2), (rows, padded // 32)
+    return (cols + 255) & -256
 
 
 def _mx_rows(name: str, t):
     """(dtype code, rows, cols, row stride) of a 2-d tensor whose rows are adjacent values."""
     torch = _torch or _load_torch()
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        _bad(f"{name} of shape {tuple(t.shape)}, strides {t.stride()}: a matrix with adjacent values in its rows expected")
-    code = MOE_F32 if t.dtype == torch.float32 else MOE_BF16
-    if code == MOE_BF16 and t.dtype != torch.bfloat16:
-        _bad(f"{name} is {t.dtype}, float32 or bfloat16 expected")
-    return code, t.shape[0], t.shape[1], t.stride(0)
+    shape = t.shape
+    if len(shape) != 2 or (shape[1] > 1 and t.stride(1) != 1):
+        _bad(f"{name} of shape {tuple(shape)}, strides {t.stride()}: a matrix with adjacent values in its rows expected")
+    dtype = t.dtype
+    code = MOE_F32 if dtype is torch.float32 else MOE_BF16
+    if code == MOE_BF16 and dtype is not torch.bfloat16:
+        _bad(f"{name} is {dtype}, float32 or bfloat16 expected")
+    return code, shape[0], shape[1], t.stride(0)
 
 
 def _check_mx(name: str, codes, scales, rows: int, cols: int) -> None:
-    torch = _torch or _load_torch()
-    (_, c), (_, s) = mx_shapes(rows, cols)
-    _check_tensor(f"{name} codes", codes, torch.uint8, rows * c)
-    _check_tensor(f"{name} scales", scales, torch.uint8, rows * s)
+    n = rows * _mx_padded(rows, cols)
+    u8 = (_torch or _load_torch()).uint8
+    if not _fits(codes, u8, n >> 1):
+        _misfit(f"{name} codes", codes, u8, n >> 1)
+    if not _fits(scales, u8, n >> 5):
+        _misfit(f"{name} scales", scales, u8, n >> 5)
 
 
 def mx_quantize(x, codes, scales, stream=None) -> None:
     """The rows of x (float32 or bfloat16 [rows, cols], rows may be strided) into an MX matrix."""
     dtype, rows, cols, stride = _mx_rows("x", x)
     _check_mx("the", codes, scales, rows, cols)
-    _call_on((x, codes, scales), stream, lib().mx_quantize, dtype, rows, cols, _ptr(x), stride, _ptr(codes),
+    _call_on((x, codes, scales), stream, lib().mx_quantize, dtype, rows, cols, x.data_ptr(), stride, _ptr(codes),
              _ptr(scales))
 
 
@@ -515,7 +533,7 @@ def mx_dequantize(codes, scales, out, stream=None) -> None:
     dtype, rows, cols, stride = _mx_rows("out", out)
     _check_mx("the", codes, scales, rows, cols)
     _call_on((codes, scales, out), stream, lib().mx_dequantize, dtype, rows, cols, _ptr(codes), _ptr(scales),
-             _ptr(out), stride)
+             out.data_ptr(), stride)
 
 
 def mx_product_desc(n, k, a="bf16", out="bf16", act="none", n_experts=0, top_k=0, pair_rows=False, codes_off=0,
