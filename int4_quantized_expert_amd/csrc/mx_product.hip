@@ -386,8 +386,12 @@ struct TileCfg {
   static constexpr int kCodeGroups = kRows / 8, kAScales = (kBM + 63) / 64, kScaleGroups = kAScales + kBN / 64;
   static constexpr int kScales = kScaleGroups * 1024;       // the scales of two chunks
   static constexpr int kPC = (kCodeGroups + kWaves - 1) / kWaves, kPS = (kScaleGroups + kWaves - 1) / kWaves;
-  static constexpr size_t kLds = S * static_cast<size_t>(kStage) + 2 * kScales;
-  static_assert(S == 2 || S == 3, "two buffers of scales serve up to three stages of codes");
+  static constexpr int kSBufs = S / 2 + 1;                  // chunk pairs that S chunks in a row can touch
+  static constexpr size_t kLds = S * static_cast<size_t>(kStage) + kSBufs * static_cast<size_t>(kScales);
+  // loads of the S - 2 chunks after an even and after an odd one: every even
+  // chunk brings scales
+  static constexpr int kNewEven = (S - 2) * kPC + (S - 2) / 2 * kPS, kNewOdd = (S - 2) * kPC + (S - 1) / 2 * kPS;
+  static_assert(S >= 2 && kNewOdd < 64, "the wait counter has six bits");
   static_assert(kBM % 8 == 0 && kBN % 64 == 0, "whole groups");
 };
 
@@ -490,6 +494,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
       const int row = g * 64 + lane;
       vs[i] = row_at(g >= C::kAScales ? row - C::kAScales * 64 + C::kBM : row < C::kBM ? row : C::kBM - 1) * spitch;
     }
+    int sput = 0, sget = 0;   // buffers of scales
     const auto fetch = [&](int chunk, int buf) {
       uint8_t* st = smem + buf * C::kStage;
 #pragma unroll
@@ -501,7 +506,8 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
         lds_load<16>(rs, st + g * 1024, vc[i], chunk * 128);
       }
       if (chunk & 1) return;
-      uint8_t* ss = smem + S * C::kStage + (chunk >> 1 & 1) * C::kScales;
+      uint8_t* ss = smem + S * C::kStage + sput * C::kScales;
+      sput = sput + 1 == C::kSBufs ? 0 : sput + 1;
 #pragma unroll
       for (int i = 0; i < C::kPS; ++i) {
         int g = wave + i * C::kWaves;
@@ -517,15 +523,15 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
       if (c < a.chunks) fetch(c, c);
     int buf = 0;
     for (int chunk = 0; chunk < a.chunks; ++chunk) {
-      // S = 3: the next chunk's loads, with scales if it is even, may be on
-      // their way still
-      if (S == 2 || chunk + 1 >= a.chunks) wait_loads<0>();
-      else if (chunk & 1) wait_loads<C::kPC + C::kPS>();
-      else wait_loads<C::kPC>();
+      // the loads of the next S - 2 chunks may be on their way still
+      if (chunk + S - 2 >= a.chunks) wait_loads<0>();
+      else if (chunk & 1) wait_loads<C::kNewOdd>();
+      else wait_loads<C::kNewEven>();
       __syncthreads();   // the chunk has arrived everywhere, and the stage before it is read to its end
       if (chunk + S - 1 < a.chunks) fetch(chunk + S - 1, buf == 0 ? S - 1 : buf - 1);
       const uint8_t* st = smem + buf * C::kStage;
-      const uint8_t* ss = smem + S * C::kStage + (chunk >> 1 & 1) * C::kScales + (chunk & 1) * 8;
+      const uint8_t* ss = smem + S * C::kStage + sget * C::kScales + (chunk & 1) * 8;
+      if (chunk & 1) sget = sget + 1 == C::kSBufs ? 0 : sget + 1;
       buf = buf + 1 == S ? 0 : buf + 1;
       int sa[TM], sw[TN];
 #pragma unroll
@@ -590,7 +596,10 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
 // place within its expert), scan, place.  The order of an expert's pairs does
 // not change any result, since every pair has its own column of the product.
 // Up to kPrepThr * 4 * NI pairs stay in registers between the passes (four
-// consecutive ids a load, all requested at once); more are read again (NI = 0).
+// consecutive ids a load, all requested at once) and are placed in LDS, from
+// where the list is written in order (scattered 4-byte stores to memory took
+// half of 18 us for 20480 pairs); more are read again and placed in memory
+// (NI = 0).
 constexpr int kPrepThr = 1024;
 
 struct PrepArgs {
@@ -612,6 +621,7 @@ __device__ __forceinline__ void group_pairs(const PrepArgs& p) {
   __shared__ int32_t cnt[kMaxExperts + 1];       // the last: pairs whose id is unusable
   __shared__ int32_t sum_p[kPrepThr / kWave], sum_t[kPrepThr / kWave];
   __shared__ int32_t start[kMaxExperts + 1];
+  __shared__ __align__(16) uint16_t listed[NI > 0 ? NI * 4 * kPrepThr : 1];
   const MxArgs& a = p.g;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int P = p.P, E = a.E;
@@ -678,8 +688,21 @@ __device__ __forceinline__ void group_pairs(const PrepArgs& p) {
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int at = (i * kPrepThr + tid) * 4 + x;
-        if (at < P) p.plist[start[kept[i][x] & 2047u] + (kept[i][x] >> 11)] = at;
+        if (at < P) listed[start[kept[i][x] & 2047u] + (kept[i][x] >> 11)] = static_cast<uint16_t>(at);
       }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int at = (i * kPrepThr + tid) * 4;
+      int32_t four[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) four[x] = listed[at + x];
+      if (at + 4 <= P) *reinterpret_cast<int4*>(p.plist + at) = int4{four[0], four[1], four[2], four[3]};
+      else
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (at + x < P) p.plist[at + x] = four[x];
+    }
   } else {
     for (int i = tid; i < P; i += kPrepThr) p.plist[start[bucket(a.ids[i])] + p.place[i]] = i;
   }
