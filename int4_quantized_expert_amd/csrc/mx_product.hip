@@ -378,21 +378,29 @@ __global__ __launch_bounds__(NW* kWave) void k_mx_narrow(MxArgs a) {
 //   Every wave issues the same number of loads for a chunk (a wave without a
 //   share repeats the last one, the same bytes to the same place), so that all
 //   but the newest chunk's have landed once no more than that number is left.
-template <int WM, int WN, int TM, int TN, int S>
+//   KS = 2: a stage is two chunks, and two groups of waves multiply one each,
+//   their sums joined at the end.  For long rows of tiles that do not fill the
+//   GPU: 512 x 2048 x 8192 takes 19.0 instead of 21.8 us, 256 x 4096 x 4096
+//   12.1 instead of 12.9; with five chunks joining costs more than it saves
+//   (333 x 2000 x 1111 11.4 instead of 10.9).
+template <int WM, int WN, int TM, int TN, int S, int KS>
 struct TileCfg {
-  static constexpr int kWaves = WM * WN, kBM = WM * TM * 16, kBN = WN * TN * 16, kRows = kBM + kBN;
-  static constexpr int kStage = kRows * 128;                // the codes of a chunk
+  static constexpr int kGroup = WM * WN, kWaves = KS * kGroup;
+  static constexpr int kBM = WM * TM * 16, kBN = WN * TN * 16, kRows = kBM + kBN;
+  static constexpr int kStage = KS * kRows * 128;           // the codes of a stage's chunks
   // rows of a direct load: 8 of codes, 64 of scales, each of one operand
   static constexpr int kCodeGroups = kRows / 8, kAScales = (kBM + 63) / 64, kScaleGroups = kAScales + kBN / 64;
   static constexpr int kScales = kScaleGroups * 1024;       // the scales of two chunks
-  static constexpr int kPC = (kCodeGroups + kWaves - 1) / kWaves, kPS = (kScaleGroups + kWaves - 1) / kWaves;
-  static constexpr int kSBufs = S / 2 + 1;                  // chunk pairs that S chunks in a row can touch
+  static constexpr int kPC = (KS * kCodeGroups + kWaves - 1) / kWaves, kPS = (kScaleGroups + kWaves - 1) / kWaves;
+  static constexpr int kSBufs = KS == 1 ? S / 2 + 1 : S;    // chunk pairs that S stages in a row can touch
   static constexpr size_t kLds = S * static_cast<size_t>(kStage) + kSBufs * static_cast<size_t>(kScales);
-  // loads of the S - 2 chunks after an even and after an odd one: every even
-  // chunk brings scales
-  static constexpr int kNewEven = (S - 2) * kPC + (S - 2) / 2 * kPS, kNewOdd = (S - 2) * kPC + (S - 1) / 2 * kPS;
+  // loads of the S - 2 stages after an even and after an odd one: every stage,
+  // with KS = 1 every even one, brings scales
+  static constexpr int kNewEven = (S - 2) * kPC + (KS == 1 ? (S - 2) / 2 : S - 2) * kPS;
+  static constexpr int kNewOdd = (S - 2) * kPC + (KS == 1 ? (S - 1) / 2 : S - 2) * kPS;
   static_assert(S >= 2 && kNewOdd < 64, "the wait counter has six bits");
-  static_assert(kBM % 8 == 0 && kBN % 64 == 0, "whole groups");
+  static_assert(kBM % 8 == 0 && kBN % 64 == 0 && (KS == 1 || KS == 2), "whole groups");
+  static_assert(KS == 1 || kGroup * TM * TN * 1024 <= S * kStage, "the joined sums fit the stages");
 };
 
 __device__ __forceinline__ int64_t clamp32(int64_t n) { return n < 0xfffffff0ll ? n : 0xfffffff0ll; }
@@ -402,16 +410,16 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-template <int WM, int WN, int TM, int TN, int S, int ACT, bool EXPERTS>
-__global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
-  using C = TileCfg<WM, WN, TM, TN, S>;
+template <int WM, int WN, int TM, int TN, int S, int KS, int ACT, bool EXPERTS>
+__global__ __launch_bounds__(KS* WM* WN* kWave) void k_mx_tile(MxArgs a) {
+  using C = TileCfg<WM, WN, TM, TN, S, KS>;
   constexpr int NM = ACT == MX_ACT_SWIGLU ? 2 : 1;
   constexpr int kCols = C::kBN / NM;                       // outputs of a block
   static_assert(kCols % 64 == 0, "a group of scales is of one matrix");
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int r = lane & 15, q = lane >> 4;
-  const int wm = wave / WN, wn = wave % WN;
+  const int kg = wave / C::kGroup, wm = wave % C::kGroup / WN, wn = wave % WN;
   const int pitch = a.chunks * 128, spitch = a.chunks * 8;
 
   // which tile: an XCD (blockIdx mod 8) runs a contiguous range of them, so
@@ -484,7 +492,7 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
 #pragma unroll
     for (int i = 0; i < C::kPC; ++i) {
       int g = wave + i * C::kWaves;
-      g = g < C::kCodeGroups ? g : C::kCodeGroups - 1;
+      g = (g < KS * C::kCodeGroups ? g : KS * C::kCodeGroups - 1) % C::kCodeGroups;
       vc[i] = row_at(g * 8 + (lane >> 3)) * pitch + static_cast<uint32_t>(((lane & 7) ^ (lane >> 3)) << 4);
     }
 #pragma unroll
@@ -495,17 +503,19 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
       vs[i] = row_at(g >= C::kAScales ? row - C::kAScales * 64 + C::kBM : row < C::kBM ? row : C::kBM - 1) * spitch;
     }
     int sput = 0, sget = 0;   // buffers of scales
-    const auto fetch = [&](int chunk, int buf) {
+    const auto fetch = [&](int stage, int buf) {
       uint8_t* st = smem + buf * C::kStage;
 #pragma unroll
       for (int i = 0; i < C::kPC; ++i) {
         int g = wave + i * C::kWaves;
-        g = g < C::kCodeGroups ? g : C::kCodeGroups - 1;
-        const int row = g * 8;
+        g = g < KS * C::kCodeGroups ? g : KS * C::kCodeGroups - 1;
+        const int row = g % C::kCodeGroups * 8;
+        int chunk = stage * KS + g / C::kCodeGroups;
+        if (KS == 2 && chunk >= a.chunks) chunk = a.chunks - 1;   // not multiplied
         const u32x4 rs = row < C::kBM ? ra : (NM == 2 && row >= C::kBM + kCols ? rw[NM - 1] : rw[0]);
         lds_load<16>(rs, st + g * 1024, vc[i], chunk * 128);
       }
-      if (chunk & 1) return;
+      if (KS == 1 && (stage & 1)) return;
       uint8_t* ss = smem + S * C::kStage + sput * C::kScales;
       sput = sput + 1 == C::kSBufs ? 0 : sput + 1;
 #pragma unroll
@@ -514,25 +524,27 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
         g = g < C::kScaleGroups ? g : C::kScaleGroups - 1;
         const int row = (g - C::kAScales) * 64;   // of W
         const u32x4 rs = g < C::kAScales ? ras : (NM == 2 && row >= kCols ? rws[NM - 1] : rws[0]);
-        lds_load<16>(rs, ss + g * 1024, vs[i], chunk * 8);
+        lds_load<16>(rs, ss + g * 1024, vs[i], stage * KS * 8);
       }
     };
 
+    const int stages = (a.chunks + KS - 1) / KS;
 #pragma unroll
     for (int c = 0; c < S - 1; ++c)
-      if (c < a.chunks) fetch(c, c);
+      if (c < stages) fetch(c, c);
     int buf = 0;
-    for (int chunk = 0; chunk < a.chunks; ++chunk) {
-      // the loads of the next S - 2 chunks may be on their way still
-      if (chunk + S - 2 >= a.chunks) wait_loads<0>();
-      else if (chunk & 1) wait_loads<C::kNewOdd>();
+    for (int stage = 0; stage < stages; ++stage) {
+      // the loads of the next S - 2 stages may be on their way still
+      if (stage + S - 2 >= stages) wait_loads<0>();
+      else if (stage & 1) wait_loads<C::kNewOdd>();
       else wait_loads<C::kNewEven>();
-      __syncthreads();   // the chunk has arrived everywhere, and the stage before it is read to its end
-      if (chunk + S - 1 < a.chunks) fetch(chunk + S - 1, buf == 0 ? S - 1 : buf - 1);
-      const uint8_t* st = smem + buf * C::kStage;
-      const uint8_t* ss = smem + S * C::kStage + sget * C::kScales + (chunk & 1) * 8;
-      if (chunk & 1) sget = sget + 1 == C::kSBufs ? 0 : sget + 1;
+      __syncthreads();   // the stage has arrived everywhere, and the one before it is read to its end
+      if (stage + S - 1 < stages) fetch(stage + S - 1, buf == 0 ? S - 1 : buf - 1);
+      const uint8_t* st = smem + buf * C::kStage + kg * C::kRows * 128;
+      const uint8_t* ss = smem + S * C::kStage + sget * C::kScales + (KS == 1 ? stage & 1 : kg) * 8;
+      if (KS == 2 || (stage & 1)) sget = sget + 1 == C::kSBufs ? 0 : sget + 1;
       buf = buf + 1 == S ? 0 : buf + 1;
+      if (KS == 2 && stage * KS + kg >= a.chunks) continue;
       int sa[TM], sw[TN];
 #pragma unroll
       for (int i = 0; i < TM; ++i)
@@ -557,6 +569,18 @@ __global__ __launch_bounds__(WM* WN* kWave) void k_mx_tile(MxArgs a) {
           for (int j = 0; j < TN; ++j) acc[i][j] = mfma4(fw[j], fa[i], acc[i][j], sw[j], sa[i], s);
       }
     }
+  }
+
+  if constexpr (KS == 2) {
+    __syncthreads();   // every stage is read to its end (or there was none)
+    v4f* part = reinterpret_cast<v4f*>(smem) + (wave % C::kGroup) * TM * TN * kWave + lane;
+    if (kg == 1)
+#pragma unroll
+      for (int i = 0; i < TM * TN; ++i) part[i * kWave] = acc[i / TN][i % TN];
+    __syncthreads();
+    if (kg == 1) return;
+#pragma unroll
+    for (int i = 0; i < TM * TN; ++i) acc[i / TN][i % TN] += part[i * kWave];
   }
 
   // a lane holds four consecutive outputs of one row
@@ -882,14 +906,14 @@ void narrow(MxArgs a, int src, int act, int ny, hipStream_t s) {
   else narrow_src<MODE, MT, 8>(a, src, act, blocks, s);
 }
 
-template <int WM, int WN, int TM, int TN, int S, bool EXPERTS>
+template <int WM, int WN, int TM, int TN, int S, int KS, bool EXPERTS>
 int tile(MxArgs a, int act, int64_t tiles, hipStream_t s) {
-  using C = TileCfg<WM, WN, TM, TN, S>;
+  using C = TileCfg<WM, WN, TM, TN, S, KS>;
   const int cols = act == MX_ACT_SWIGLU ? C::kBN / 2 : C::kBN;
   a.nblk = (a.N + cols - 1) / cols;
   const dim3 grid(static_cast<uint32_t>((tiles * a.nblk + 7) / 8 * 8)), block(C::kWaves * kWave);
-  const auto kernel = act == MX_ACT_SWIGLU ? &k_mx_tile<WM, WN, TM, TN, S, MX_ACT_SWIGLU, EXPERTS>
-                                           : &k_mx_tile<WM, WN, TM, TN, S, MX_ACT_NONE, EXPERTS>;
+  const auto kernel = act == MX_ACT_SWIGLU ? &k_mx_tile<WM, WN, TM, TN, S, KS, MX_ACT_SWIGLU, EXPERTS>
+                                           : &k_mx_tile<WM, WN, TM, TN, S, KS, MX_ACT_NONE, EXPERTS>;
   if (C::kLds > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(C::kLds));
@@ -973,9 +997,13 @@ int mx_linear_forward(const mx_product_desc* d, int32_t M, const void* a, const 
   const auto tiles = [&](int bm, int bn) {
     return static_cast<int64_t>((M + bm - 1) / bm) * ((wrows + bn - 1) / bn);
   };
-  if (tiles(256, 256) >= 192) rc = tile<2, 4, 8, 4, 2, false>(g, d->act, (M + 255) / 256, s);
-  else if (tiles(128, 128) >= 192) rc = tile<2, 2, 4, 4, 2, false>(g, d->act, (M + 127) / 128, s);
-  else rc = tile<1, 4, 4, 2, 3, false>(g, d->act, (M + 63) / 64, s);
+  // the largest tile that still gives most of the 256 CUs one (a 256 x 256 tile
+  // reads half as much per product as a 128 x 128 one: 8192^3 takes 309 against
+  // 454 us; 2048^3, with 64 and 256 tiles, is left to the smaller)
+  if (tiles(256, 256) >= 192) rc = tile<2, 4, 8, 4, 2, 1, false>(g, d->act, (M + 255) / 256, s);
+  else if (tiles(128, 128) >= 192) rc = tile<2, 2, 4, 4, 2, 1, false>(g, d->act, (M + 127) / 128, s);
+  else if (tiles(64, 128) > 256 || g.chunks < 16) rc = tile<1, 4, 4, 2, 3, 1, false>(g, d->act, (M + 63) / 64, s);
+  else rc = tile<1, 4, 4, 2, 3, 2, false>(g, d->act, (M + 63) / 64, s);
   return rc == MOE_OK ? launched() : api_fail(MOE_EHIP, "the product kernel's LDS size was refused");
 }
 
@@ -1066,9 +1094,9 @@ int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const
     g.ntiles = p.ntiles;
     const int64_t most = (P < d->n_experts + 1 ? P : d->n_experts + 1) + static_cast<int64_t>(P) / bm;
     if (bm == 16) narrow<kTiles>(g, MX_FP4, d->act, static_cast<int>(most), s);
-    else if (bm == 32) rc = tile<1, 4, 2, 2, 3, true>(g, d->act, most, s);
-    else if (bm == 64) rc = tile<1, 4, 4, 2, 3, true>(g, d->act, most, s);
-    else rc = tile<2, 2, 4, 4, 2, true>(g, d->act, most, s);
+    else if (bm == 32) rc = tile<1, 4, 2, 2, 3, 1, true>(g, d->act, most, s);
+    else if (bm == 64) rc = tile<1, 4, 4, 2, 3, 1, true>(g, d->act, most, s);
+    else rc = tile<2, 2, 4, 4, 2, 1, true>(g, d->act, most, s);
     if (rc != MOE_OK) return api_fail(MOE_EHIP, "the product kernel's LDS size was refused");
   }
   if (topk_w)

@@ -74,6 +74,11 @@ def test_linear_long_and_wide():
     linear(70, 24, 9000, seed=8, act="swiglu")
     linear(2, 5000, 256, seed=9)
     linear(600, 1100, 512, seed=10, out="bf16")
+    linear(100, 150, 5000, seed=11, act="swiglu", out="bf16")      # two groups of chunks, the last pair half empty
+    linear(150, 300, 4100, seed=12)
+    linear(65, 130, 4096 + 256, seed=13, a="mx")
+    linear(3500, 3600, 300, seed=14, out="bf16")                   # the largest tiles, ragged in every direction
+    linear(2000, 1000, 700, seed=15, act="swiglu")
 
 
 def test_linear_nan_blocks_stay_in_their_rows():
