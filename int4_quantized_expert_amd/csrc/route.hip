@@ -86,9 +86,19 @@ __device__ __forceinline__ uint64_t order_key64(double d) {
 }
 
 struct WaveLds {
-  uint64_t key[kCandMax];
+  uint64_t key[2 * kCandMax];   // candidates; behind them a place per lane for what is none
   int32_t id[kCandMax];
 };
+
+// A wave's experts: slot j of a lane.  VEC: four neighbours a load (E = 64 NJ).
+template <bool VEC>
+__device__ __forceinline__ int expert_of(int lane, int j) {
+  return VEC ? 4 * lane + 256 * (j >> 2) + (j & 3) : lane + j * kWave;
+}
+template <bool VEC>
+__device__ __forceinline__ int lane_of(int e) { return VEC ? (e >> 2) & (kWave - 1) : e & (kWave - 1); }
+template <bool VEC>
+__device__ __forceinline__ int slot_of(int e) { return VEC ? (e >> 8) * 4 + (e & 3) : e / kWave; }
 
 __device__ __forceinline__ int mbcnt(uint64_t m) {
   return static_cast<int>(__builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(m >> 32),
@@ -113,20 +123,22 @@ __device__ __forceinline__ uint32_t kth_bound(const uint32_t (&key)[NJ], int k) 
   return theta;
 }
 
-// Candidates: entries with key >= theta (key 0: no entry), ranked by (key,
+// Candidates: entries with key >= theta >= 1 (key 0: no entry), ranked by (key,
 // -id).  Returns their number; if at most 64, lane r < number holds the id and
 // key of rank r.
-template <int NJ>
+template <int NJ, bool VEC>
 __device__ __forceinline__ int rank32(const uint32_t (&key)[NJ], uint32_t theta, int lane, WaveLds* lds, int* id_out,
                                       uint32_t* key_out) {
   lds->key[lane] = 0;   // padding; a wave's LDS accesses land in order
   int cnt = 0;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const bool in = key[j] != 0u && key[j] >= theta;
+    const bool in = key[j] >= theta;
     const uint64_t m = __ballot(in);
     const int pos = cnt + mbcnt(m);
-    if (in && pos < kCandMax) lds->key[pos] = (static_cast<uint64_t>(key[j]) << 32) | static_cast<uint32_t>(~(lane + j * kWave));
+    // no branch: a lane without a candidate, and one past the 64th, writes to its own place behind them
+    lds->key[in && pos < kCandMax ? pos : kCandMax + lane] =
+        (static_cast<uint64_t>(key[j]) << 32) | static_cast<uint32_t>(~expert_of<VEC>(lane, j));
     cnt += __popcll(m);
   }
   if (cnt > kCandMax) return cnt;
@@ -151,7 +163,7 @@ __device__ __forceinline__ int rank32(const uint32_t (&key)[NJ], uint32_t theta,
 // The same on 64-bit keys, bounded by their 32-bit images: lane r < k returns
 // the id of rank r.  More than 64 candidates (many equal keys) take k rounds
 // of a wave arg-max.
-template <int NJ>
+template <int NJ, bool VEC>
 __device__ __forceinline__ int topk64(const uint32_t (&key32)[NJ], const uint64_t (&key64)[NJ], int k, int lane,
                                       WaveLds* lds) {
   const uint32_t theta = kth_bound<NJ>(key32, k);
@@ -163,7 +175,7 @@ __device__ __forceinline__ int topk64(const uint32_t (&key32)[NJ], const uint64_
     const int pos = cnt + mbcnt(m);
     if (in && pos < kCandMax) {
       lds->key[pos] = key64[j];
-      lds->id[pos] = lane + j * kWave;
+      lds->id[pos] = expert_of<VEC>(lane, j);
     }
     cnt += __popcll(m);
   }
@@ -187,9 +199,9 @@ __device__ __forceinline__ int topk64(const uint32_t (&key32)[NJ], const uint64_
     int bid = 0x7fffffff;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      if (!((taken >> j) & 1u) && key32[j] != 0u && key64[j] > best) {
+      if (!((taken >> j) & 1u) && key32[j] != 0u && key64[j] > best) {   // equal keys: the lower slot is the lower id
         best = key64[j];
-        bid = lane + j * kWave;
+        bid = expert_of<VEC>(lane, j);
       }
     }
 #define ARGMAX(S)                                                                                            \
@@ -204,10 +216,32 @@ __device__ __forceinline__ int topk64(const uint32_t (&key32)[NJ], const uint64_
   }
     ARGMAX(1) ARGMAX(2) ARGMAX(4) ARGMAX(8) ARGMAX(16) ARGMAX(32)
 #undef ARGMAX
-    if ((bid & (kWave - 1)) == lane) taken |= 1u << (bid / kWave);
+    if (lane_of<VEC>(bid) == lane) taken |= 1u << slot_of<VEC>(bid);
     if (lane == i) myid = bid;
   }
   return myid;
+}
+
+__device__ __forceinline__ float second_of(float hi, float lo, float v) { return __builtin_amdgcn_fmed3f(hi, lo, v); }
+__device__ __forceinline__ double second_of(double hi, double lo, double v) { return v > hi ? hi : (v > lo ? v : lo); }
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return a > b ? a : b; }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return a < b ? a : b; }
+
+template <int S>
+__device__ __forceinline__ float lane_xor_f(float v, int lane) {
+  return __uint_as_float(lane_xor<S>(__float_as_uint(v), lane));
+}
+template <int S>
+__device__ __forceinline__ double lane_xor_f(double v, int lane) { return lane_xor_d<S>(v, lane); }
+
+// The two largest of two lanes' two largest (lo <= hi).
+template <int S, typename F>
+__device__ __forceinline__ void merge_two(F& hi, F& lo, int lane) {
+  const F oh = lane_xor_f<S>(hi, lane), ol = lane_xor_f<S>(lo, lane);
+  lo = larger(smaller(hi, oh), larger(lo, ol));
+  hi = larger(hi, oh);
 }
 
 // Scores of the groups from the experts' values in LDS (-inf: not counted).
@@ -215,22 +249,32 @@ __device__ __forceinline__ int topk64(const uint32_t (&key32)[NJ], const uint64_
 // return its score, lanes of no group -inf.
 template <typename F>
 __device__ __forceinline__ F group_score(const F* val, const RouteArgs& a, int L, int lane) {
+  typedef F F4 __attribute__((ext_vector_type(4)));
   const int g = lane / L;
   F hi = -INFINITY, lo = -INFINITY;
-  if (g < a.G) {
+  const F* v = val + g * a.gsize;
+  if (a.gsize % (4 * L) == 0) {
+    if (g < a.G) {
+      for (int x = 4 * (lane & (L - 1)); x < a.gsize; x += 4 * L) {
+        const F4 w = *reinterpret_cast<const F4*>(v + x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lo = second_of(hi, lo, w[i]);
+          hi = larger(hi, w[i]);
+        }
+      }
+    }
+  } else if (g < a.G) {
     for (int x = lane & (L - 1); x < a.gsize; x += L) {
-      const F v = val[g * a.gsize + x];
-      lo = v > hi ? hi : (v > lo ? v : lo);
-      hi = v > hi ? v : hi;
+      lo = second_of(hi, lo, v[x]);
+      hi = larger(hi, v[x]);
     }
   }
-  for (int st = 1; st < L; st <<= 1) {
-    const F oh = __shfl_xor(hi, st), ol = __shfl_xor(lo, st);
-    const F mid = oh > hi ? hi : oh;       // the smaller of the two largest
-    const F second = oh > hi ? ol : lo;    // the second of the side with the larger first
-    hi = oh > hi ? oh : hi;
-    lo = mid > second ? mid : second;
-  }
+  if (L > 1) merge_two<1>(hi, lo, lane);
+  if (L > 2) merge_two<2>(hi, lo, lane);
+  if (L > 4) merge_two<4>(hi, lo, lane);
+  if (L > 8) merge_two<8>(hi, lo, lane);
+  if (L > 16) merge_two<16>(hi, lo, lane);
   return a.gt == 2 && hi != -INFINITY && lo != -INFINITY ? hi + lo : hi;
 }
 
@@ -244,35 +288,29 @@ __device__ __forceinline__ double readlane_f(double v, int l) {
              static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(b & 0xffffffffu), l)));
 }
 
-// Rank of this lane's group among all, ties to the lower group.
-template <typename F>
-__device__ __forceinline__ int group_rank(F sc, const RouteArgs& a, int L, int lane) {
-  const int g = lane / L;
-  int rank = 0;
-  for (int o = 0; o < a.G; ++o) {
-    const F v = readlane_f(sc, o * L);
-    rank += (v > sc || (v == sc && o < g)) ? 1 : 0;
-  }
-  return rank;
-}
-
 // 1 for the experts of the groups in `keep` (bit g L: group g), else 0.
-template <int NJ>
+template <int NJ, bool VEC>
 __device__ __forceinline__ void mark_groups(uint64_t keep, const RouteArgs& a, int L, int lane, uint32_t (&mark)[NJ]) {
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const uint32_t e = static_cast<uint32_t>(lane + j * kWave), n = static_cast<uint32_t>(a.E);
+    const uint32_t e = static_cast<uint32_t>(expert_of<VEC>(lane, j)), n = static_cast<uint32_t>(a.E);
     const uint32_t g = e < n ? (e * a.ginv) >> 20 : 0u;
     mark[j] = e < n && ((keep >> (g * L)) & 1ull) ? 1u : 0u;
   }
 }
 
-// The choice by double-precision scores.  Lane r < k returns the id of rank r;
-// *denom_out: the softmax denominator.
-template <int NJ, bool SIGMOID>
-__device__ __forceinline__ int choose_exact(const RouteArgs& a, const float (&l)[NJ], const float (&bias)[NJ], float mx,
-                                         int lane, WaveLds* lds, double* val, double* denom_out) {
-  double s[NJ], sum = 0.0, denom = 1.0;
+struct Chosen {
+  int id;         // lane r < k: the id of rank r
+  double denom;   // the softmax denominator
+};
+
+// The choice by double-precision scores.
+template <int NJ, bool SIGMOID, bool VEC>
+__device__ __forceinline__ Chosen choose_exact(const RouteArgs& a, const float (&l)[NJ], const float (&bias)[NJ], float mx,
+                                               int L, int lane, WaveLds* lds, double* val) {
+  Chosen c;
+  double s[NJ], sum = 0.0;
+  c.denom = 1.0;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     const double x = static_cast<double>(l[j]);
@@ -281,31 +319,34 @@ __device__ __forceinline__ int choose_exact(const RouteArgs& a, const float (&l)
     sum += s[j];
   }
   if (!SIGMOID) {
-    denom = wave_sum_d(sum, lane);
-    if (denom == 0.0) denom = 1.0;   // a row whose mask leaves nothing
+    c.denom = wave_sum_d(sum, lane);
+    if (c.denom == 0.0) c.denom = 1.0;   // a row whose mask leaves nothing
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) s[j] /= denom;
+    for (int j = 0; j < NJ; ++j) s[j] /= c.denom;
   }
-  *denom_out = denom;
   uint32_t key32[NJ];
   uint64_t key64[NJ];
   if (a.G > 1) {
     wave_sync_lds();
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const int e = lane + j * kWave;
+      const int e = expert_of<VEC>(lane, j);
       const double v = s[j] + static_cast<double>(bias[j]);
       if (e < a.E) val[e] = (l[j] == -INFINITY || v != v) ? -INFINITY : v;
     }
     wave_sync_lds();
-    int L = kWave;
-    while (L * a.G > kWave) L >>= 1;
     const double sc = group_score<double>(val, a, L, lane);
-    const int rank = group_rank<double>(sc, a, L, lane);
-    mark_groups<NJ>(__ballot(lane / L < a.G && rank < a.tg && (lane & (L - 1)) == 0), a, L, lane, key32);
+    const int g = lane / L;
+    int rank = 0;   // among all groups, ties to the lower group
+    for (int o = 0; o < a.G; ++o) {
+      const double v = readlane_f(sc, o * L);
+      rank += (v > sc || (v == sc && o < g)) ? 1 : 0;
+    }
+    mark_groups<NJ, VEC>(__ballot(g < a.G && rank < a.tg && (lane & (L - 1)) == 0), a, L, lane, key32);
+    wave_sync_lds();
   } else {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) key32[j] = lane + j * kWave < a.E ? 1u : 0u;
+    for (int j = 0; j < NJ; ++j) key32[j] = expert_of<VEC>(lane, j) < a.E ? 1u : 0u;
   }
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
@@ -314,27 +355,29 @@ __device__ __forceinline__ int choose_exact(const RouteArgs& a, const float (&l)
     key64[j] = order_key64(key);
     key32[j] = key32[j] ? order_key(static_cast<float>(key)) : 0u;   // order_key is never 0 for a number
   }
-  return topk64<NJ>(key32, key64, a.k, lane, lds);
+  c.id = topk64<NJ, VEC>(key32, key64, a.k, lane, lds);
+  return c;
 }
 
 // The same choice from fp32 scores, where it is certain.  With u = 2^-24:
 //   sigmoid   exp2 of a rounded product, a sum and a reciprocal of 1 ulp each
-//             leave |error of s| <= (0.23 + 1 + 1 + 2) u < 8 u
+//             leave |error of s| <= (0.45 + 0.5 + 1 + 2) u < 8 u
 //   softmax   a term exp(d) <= 1 is off by exp(d) (2 |d| + 2) u <= 3 u; the
 //             denominator, whose terms are off by 2 |d| + 2 u and whose mean
 //             |d| is at most the entropy, 6.94, by (14 + 2 + 16 + 6) u of
 //             itself; |error of s| < 64 u
 // and a bias adds a rounding of u |v|; `eps` is that bound.  A group's score is
-// off by 2 eps + u |sum| at most.  Groups: the worst that stays has to lead the
-// best that goes by more than twice the bound.  Experts: every entry within
-// 2 eps of the bound on the k-th largest is a candidate, and neighbours among
-// the first k + 1 have to differ by more than 2 eps (a logit is exact).
+// off by 2 eps + u |sum| at most.  Groups: one that stays has fewer than
+// top_groups others that may lie above it, one that goes at least that many
+// that do, by more than twice the bound.  Experts: every entry within 2 eps of
+// the bound on the k-th largest is a candidate, and neighbours among the first
+// k + 1 have to differ by more than 2 eps (a logit is exact).
 // Returns false where it is not certain (equal keys, empty groups).
-template <int NJ, bool SIGMOID>
+template <int NJ, bool SIGMOID, bool VEC>
 __device__ __forceinline__ bool choose_fast(const RouteArgs& a, const float (&l)[NJ], const float (&bias)[NJ], float mx,
-                                            int lane, WaveLds* lds, float* val, int* id) {
+                                            int L, int lane, WaveLds* lds, float* val, int* id) {
   constexpr float kLog2e = 1.4426950408889634f, u = 5.9604644775390625e-8f;
-  float v[NJ], big = 0.f;
+  float v[NJ];
   if (SIGMOID) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) v[j] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-l[j] * kLog2e));
@@ -345,48 +388,64 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs& a, const float (&l)
       v[j] = l[j] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((l[j] - mx) * kLog2e);
       sum += v[j];
     }
-#define STEP(S) sum += __uint_as_float(lane_xor<S>(__float_as_uint(sum), lane))
+#define STEP(S) sum += lane_xor_f<S>(sum, lane)
     STEP(1); STEP(2); STEP(4); STEP(8); STEP(16); STEP(32);
 #undef STEP
     const float r = __builtin_amdgcn_rcpf(sum);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) v[j] *= r;
   }
+  // the largest magnitude as whole numbers: infinities and NaN come out on top
+  uint32_t top = 0;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    v[j] = l[j] == -INFINITY ? -INFINITY : v[j] + bias[j];
-    if (v[j] != v[j]) big = INFINITY;
-    else if (v[j] != -INFINITY) big = fmaxf(big, fabsf(v[j]));
+    const bool out = l[j] == -INFINITY;
+    const float x = v[j] + bias[j];
+    const uint32_t m = out ? 0u : __float_as_uint(x) & 0x7fffffffu;
+    top = m > top ? m : top;
+    v[j] = out ? -INFINITY : x;
   }
-  big = wave_max_f(big, lane);
-  if (!(big < 1e30f)) return false;
+  // scores are at most 1: with biases below 3 no exchange is needed
+  float big = 4.f;
+  if (__ballot(top >= 0x40800000u)) {
+    big = wave_max_f(__uint_as_float(top), lane);   // passes NaN over, which is not below itself
+    if (__ballot(!(__uint_as_float(top) < 1e30f))) return false;
+  }
   const float eps = (SIGMOID ? 8.f : 64.f) * u + 2.f * u * big;
   uint32_t key[NJ];
   if (a.G > 1) {
+    if (VEC) {
+      typedef float f32x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int e = lane + j * kWave;
-      if (e < a.E) val[e] = v[j];
+      for (int j = 0; j < NJ; j += 4) *reinterpret_cast<f32x4*>(val + expert_of<VEC>(lane, j)) = f32x4{v[j], v[j + 1], v[j + 2], v[j + 3]};
+    } else {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if (expert_of<VEC>(lane, j) < a.E) val[expert_of<VEC>(lane, j)] = v[j];
     }
     wave_sync_lds();
-    int L = kWave;
-    while (L * a.G > kWave) L >>= 1;
     const float sc = group_score<float>(val, a, L, lane);
-    const int rank = group_rank<float>(sc, a, L, lane);
+    const float margin = 4.f * eps + 8.f * u * big, low = sc - margin, high = sc + margin;
+    int maybe = -1, surely = 0;   // the group itself lies above low
+    for (int o = 0; o < a.G; ++o) {
+      const float x = readlane_f(sc, o * L);
+      maybe += x > low ? 1 : 0;
+      surely += x > high ? 1 : 0;
+    }
+    if (sc == -INFINITY) maybe = 64;
     const bool real = lane / L < a.G;
-    const float lead = -wave_max_f(real && rank < a.tg ? -sc : -INFINITY, lane);
-    const float next = wave_max_f(real && rank >= a.tg ? sc : -INFINITY, lane);
-    if (!(lead - next > 4.f * eps + 8.f * u * big)) return false;
-    mark_groups<NJ>(__ballot(real && rank < a.tg && (lane & (L - 1)) == 0), a, L, lane, key);
+    if (__ballot(real && maybe >= a.tg && surely < a.tg)) return false;
+    mark_groups<NJ, VEC>(__ballot(real && maybe < a.tg && (lane & (L - 1)) == 0), a, L, lane, key);
   } else {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) key[j] = lane + j * kWave < a.E ? 1u : 0u;
+    for (int j = 0; j < NJ; ++j) key[j] = VEC || expert_of<VEC>(lane, j) < a.E ? 1u : 0u;
   }
   const bool by_score = a.bias != nullptr;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const float x = by_score || l[j] != l[j] ? v[j] : l[j];
-    key[j] = key[j] ? order_key(x) : 0u;
+    const float x = (by_score || l[j] != l[j] ? v[j] : l[j]) + 0.f;   // one key for both zeros
+    const uint32_t b = __float_as_uint(x);
+    key[j] = key[j] ? b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u) : 0u;
   }
   const uint32_t theta = kth_bound<NJ>(key, a.k);
   uint32_t from = theta > 1u ? theta : 1u;
@@ -395,7 +454,7 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs& a, const float (&l)
     else from = order_key(key_float(theta) - 2.5f * eps);
   }
   uint32_t mykey = 0;
-  const int cnt = rank32<NJ>(key, from, lane, lds, id, &mykey);
+  const int cnt = rank32<NJ, VEC>(key, from, lane, lds, id, &mykey);
   if (cnt > kCandMax) return false;
   if (!by_score) return true;
   const float mine = key_float(mykey), below = __shfl_down(mine, 1);
@@ -403,63 +462,102 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs& a, const float (&l)
   return __ballot(!sure) == 0;
 }
 
+// One token's logits on the wave.
+template <int NJ, int DT, bool VEC>
+__device__ __forceinline__ void load_row(const RouteArgs& a, int64_t t, int lane, float (&l)[NJ]) {
+  const int64_t row = t * a.stride;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int j = 0; j < NJ; j += 4) {
+      const int64_t at = row + expert_of<VEC>(lane, j);
+      if constexpr (DT == kF32) {
+        const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + at);
+        l[j] = w.x; l[j + 1] = w.y; l[j + 2] = w.z; l[j + 3] = w.w;
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + at);
+        l[j] = __uint_as_float(w.x << 16);
+        l[j + 1] = __uint_as_float(w.x & 0xffff0000u);
+        l[j + 2] = __uint_as_float(w.y << 16);
+        l[j + 3] = __uint_as_float(w.y & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int e = lane + j * kWave;
+      l[j] = e < a.E ? load_scalar<DT>(a.logits, static_cast<size_t>(row + e)) : -INFINITY;
+    }
+  }
+}
+
+template <int NJ>
+__device__ __forceinline__ float row_max(const float (&l)[NJ], int lane) {
+  float m = l[0];   // fmaxf passes NaN over
+#pragma unroll
+  for (int j = 1; j < NJ; ++j) m = fmaxf(m, l[j]);
+  return wave_max_f(m, lane);
+}
+
 // NJ: logits per lane (E <= 64 NJ).  WIDE: experts or groups are compared by
-// scores (a bias or groups).
-template <int NJ, int DT, bool SIGMOID, bool WIDE>
+// scores (a bias or groups).  VEC: E = 64 NJ and aligned rows.
+// Bound by the instructions of a token's wave (about 1000 with groups): 32768
+// tokens of 512 bf16 logits in 8 groups take 5x the time of reading them.
+// Several tokens per wave, sharing the bias and the evaluation of the weights,
+// were slower (four 62, eight 65, sixteen 87 us against one's 59): fewer waves
+// hide less of each other's exchanges.
+template <int NJ, int DT, bool SIGMOID, bool WIDE, bool VEC>
 __global__ __launch_bounds__(kRtWaves* kWave) void k_route(RouteArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ WaveLds wave_lds[kRtWaves];
   const int lane = threadIdx.x & (kWave - 1);
-  const int wave = threadIdx.x / kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRtWaves + wave;
   if (t >= a.T) return;   // no barrier below: waves are independent
-  WaveLds* lds = reinterpret_cast<WaveLds*>(smem) + wave;
-  double* val = reinterpret_cast<double*>(smem + kRtWaves * sizeof(WaveLds)) + static_cast<size_t>(wave) * (WIDE ? a.E : 0);
+  WaveLds* lds = &wave_lds[wave];
 
-  const int64_t row = t * a.stride;
   float l[NJ];
-  float bias[NJ];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int e = lane + j * kWave;
-    l[j] = e < a.E ? load_scalar<DT>(a.logits, static_cast<size_t>(row + e)) : -INFINITY;
-    bias[j] = (WIDE && a.bias && e < a.E) ? a.bias[e] : 0.f;
-  }
-  float mx = l[0];   // fmaxf passes NaN over
-#pragma unroll
-  for (int j = 1; j < NJ; ++j) mx = fmaxf(mx, l[j]);
-  mx = wave_max_f(mx, lane);
-
-  int id = 0;
-  double denom = 1.0;   // of a softmax that is not divided out again
+  load_row<NJ, DT, VEC>(a, t, lane, l);
+  const float mx = SIGMOID ? 0.f : row_max<NJ>(l, lane);
+  Chosen c{0, 1.0};
   if constexpr (WIDE) {
-    const bool sum_too = !SIGMOID && !a.renorm;
-    if (sum_too || !choose_fast<NJ, SIGMOID>(a, l, bias, mx, lane, lds, reinterpret_cast<float*>(val), &id))
-      id = choose_exact<NJ, SIGMOID>(a, l, bias, mx, lane, lds, val, &denom);
+    double* val = reinterpret_cast<double*>(smem) + static_cast<size_t>(wave) * a.E;
+    float bias[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int e = expert_of<VEC>(lane, j);
+      bias[j] = a.bias && (VEC || e < a.E) ? a.bias[e] : 0.f;
+    }
+    int L = kWave;   // lanes per group
+    while (L * a.G > kWave) L >>= 1;
+    // a softmax that is not divided out again needs the exact denominator anyway
+    if ((!SIGMOID && !a.renorm) ||
+        !choose_fast<NJ, SIGMOID, VEC>(a, l, bias, mx, L, lane, lds, reinterpret_cast<float*>(val), &c.id))
+      c = choose_exact<NJ, SIGMOID, VEC>(a, l, bias, mx, L, lane, lds, val);
   } else {
     if (!SIGMOID && !a.renorm) {
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) sum += l[j] == -INFINITY ? 0.f : expf(l[j] - mx);
-      denom = wave_sum_d(static_cast<double>(sum), lane);
-      if (denom == 0.0) denom = 1.0;
+      c.denom = wave_sum_d(static_cast<double>(sum), lane);
+      if (c.denom == 0.0) c.denom = 1.0;
     }
     uint32_t key[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
-      key[j] = lane + j * kWave < a.E ? order_key(l[j] != l[j] ? -INFINITY : l[j]) : 0u;
+      key[j] = VEC || lane + j * kWave < a.E ? order_key(l[j] != l[j] ? -INFINITY : l[j]) : 0u;
     const uint32_t theta = kth_bound<NJ>(key, a.k);
     uint32_t mykey = 0;
-    if (rank32<NJ>(key, theta, lane, lds, &id, &mykey) > kCandMax) {
+    if (rank32<NJ, VEC>(key, theta > 1u ? theta : 1u, lane, lds, &c.id, &mykey) > kCandMax) {
       uint64_t key64[NJ];
 #pragma unroll
       for (int j = 0; j < NJ; ++j) key64[j] = key[j];
-      id = topk64<NJ>(key, key64, a.k, lane, lds);
+      c.id = topk64<NJ, VEC>(key, key64, a.k, lane, lds);
     }
   }
 
   // weights of the chosen, in double precision (one exp per lane)
   const bool on = lane < a.k;
-  const float lc = on ? load_scalar<DT>(a.logits, static_cast<size_t>(row + id)) : -INFINITY;
+  const float lc = on ? load_scalar<DT>(a.logits, static_cast<size_t>(t * a.stride + c.id)) : -INFINITY;
   double sc = 0.0;
   if (on && lc != -INFINITY) {
     if (SIGMOID) sc = 1.0 / (1.0 + exp(-static_cast<double>(lc)));
@@ -469,32 +567,42 @@ __global__ __launch_bounds__(kRtWaves* kWave) void k_route(RouteArgs a) {
     const double sum = wave_sum_d(sc, lane);
     sc = sum == 0.0 ? 0.0 : sc / sum;
   } else if (!SIGMOID) {
-    sc /= denom;
+    sc /= c.denom;
   }
   if (on) {
-    a.ids[t * a.k + lane] = id;
+    a.ids[t * a.k + lane] = c.id;
     a.w[t * a.k + lane] = static_cast<float>(sc * static_cast<double>(a.scale));
   }
 }
 
-template <int NJ, int DT, bool SIGMOID>
-void launch_route_wide(const RouteArgs& a, bool wide, dim3 grid, dim3 block, hipStream_t s) {
-  const uint32_t lds = kRtWaves * (sizeof(WaveLds) + (wide && a.G > 1 ? static_cast<uint32_t>(a.E) * 8u : 0u));
-  if (wide) launch_kernel(k_route<NJ, DT, SIGMOID, true>, grid, block, lds, s, a);
-  else launch_kernel(k_route<NJ, DT, SIGMOID, false>, grid, block, lds, s, a);
+template <int NJ, int DT, bool SIGMOID, bool WIDE, bool VEC>
+void launch_route(const RouteArgs& a, hipStream_t s) {
+  const uint32_t lds = WIDE && a.G > 1 ? kRtWaves * static_cast<uint32_t>(a.E) * 8u : 0u;
+  const dim3 grid(static_cast<uint32_t>((a.T + kRtWaves - 1) / kRtWaves)), block(kRtWaves * kWave);
+  launch_kernel(k_route<NJ, DT, SIGMOID, WIDE, VEC>, grid, block, lds, s, a);
 }
 
-template <int NJ, int DT>
-void launch_route_score(const RouteArgs& a, bool sigmoid, bool wide, dim3 grid, dim3 block, hipStream_t s) {
-  if (sigmoid) launch_route_wide<NJ, DT, true>(a, wide, grid, block, s);
-  else launch_route_wide<NJ, DT, false>(a, wide, grid, block, s);
+template <int NJ, int DT, bool SIGMOID>
+void launch_route_wide(const RouteArgs& a, bool wide, hipStream_t s) {
+  constexpr uintptr_t kAlign = DT == kF32 ? 16 : 8;
+  const bool vec = a.E == 64 * NJ && a.stride % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & (kAlign - 1)) == 0;
+  if (wide && vec) launch_route<NJ, DT, SIGMOID, true, true>(a, s);
+  else if (wide) launch_route<NJ, DT, SIGMOID, true, false>(a, s);
+  else if (vec) launch_route<NJ, DT, SIGMOID, false, true>(a, s);
+  else launch_route<NJ, DT, SIGMOID, false, false>(a, s);
+}
+
+template <int DT, bool SIGMOID>
+void launch_route_size(const RouteArgs& a, bool wide, hipStream_t s) {
+  if (a.E <= 4 * kWave) launch_route_wide<4, DT, SIGMOID>(a, wide, s);
+  else if (a.E <= 8 * kWave) launch_route_wide<8, DT, SIGMOID>(a, wide, s);
+  else launch_route_wide<16, DT, SIGMOID>(a, wide, s);
 }
 
 template <int DT>
-void launch_route_dt(const RouteArgs& a, bool sigmoid, bool wide, dim3 grid, dim3 block, hipStream_t s) {
-  if (a.E <= 4 * kWave) launch_route_score<4, DT>(a, sigmoid, wide, grid, block, s);
-  else if (a.E <= 8 * kWave) launch_route_score<8, DT>(a, sigmoid, wide, grid, block, s);
-  else launch_route_score<16, DT>(a, sigmoid, wide, grid, block, s);
+void launch_route_dt(const RouteArgs& a, bool sigmoid, bool wide, hipStream_t s) {
+  if (sigmoid) launch_route_size<DT, true>(a, wide, s);
+  else launch_route_size<DT, false>(a, wide, s);
 }
 
 int bad(const char* fmt, long long x = 0, long long y = 0) {
@@ -552,9 +660,8 @@ int route_forward(const moe_route_desc* r, int32_t T, const void* logits, int64_
   // all groups staying is no choice of groups
   if (a.tg == a.G) a.G = 1;
   const bool sigmoid = r->score == MOE_SCORE_SIGMOID, wide = bias != nullptr || a.G > 1;
-  const dim3 grid(static_cast<uint32_t>((T + kRtWaves - 1) / kRtWaves)), block(kRtWaves * kWave);
-  if (r->logit_dtype == MOE_F32) launch_route_dt<kF32>(a, sigmoid, wide, grid, block, s);
-  else launch_route_dt<kBF16>(a, sigmoid, wide, grid, block, s);
+  if (r->logit_dtype == MOE_F32) launch_route_dt<kF32>(a, sigmoid, wide, s);
+  else launch_route_dt<kBF16>(a, sigmoid, wide, s);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) {
     char buf[256];
