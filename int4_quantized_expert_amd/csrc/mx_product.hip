@@ -26,7 +26,13 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr int kMxF4 = 2;                 // a_dtype code MX_FP4
 constexpr int kChunk = kMxPad;           // k values per step
-constexpr int kDirectPairs = 128;        // pairs that the kernels group by themselves
+// Pairs up to which the blocks find their expert's pairs by themselves instead
+// of a grouping launch: gate and up rows of top-10 experts (512 outputs, k =
+// 2048) take 10.2 us against 12.3 for 20 pairs, 15.1 against 13.0 for 40.
+constexpr int kDirectPairs = 32;
+// Pairs up to which a token's weighted sum is one block's work: down rows (2048
+// outputs, k = 512) 16.4 us against 17.2 for 80 pairs, 22.7 against 19.2 for 120.
+constexpr int kSumPairs = 80;
 
 enum Mode { kDense, kDirect, kTiles, kSum };
 
@@ -211,17 +217,13 @@ __global__ __launch_bounds__(NW* kWave) void k_mx_narrow(MxArgs a) {
     count = a.M - y * 16 * MT;
     count = count < 16 * MT ? count : 16 * MT;
   } else if constexpr (MODE == kDirect) {
-    const int i0 = a.ids[lane < a.M ? lane : 0], i1 = a.ids[lane + kWave < a.M ? lane + kWave : 0];
-    const int e = __builtin_amdgcn_readlane(y < kWave ? i0 : i1, y & (kWave - 1));
-    const uint64_t b0 = __ballot(lane < a.M && i0 == e), b1 = __ballot(lane + kWave < a.M && i1 == e);
-    const int first = b0 ? __ffsll(static_cast<unsigned long long>(b0)) - 1 : kWave + __ffsll(static_cast<unsigned long long>(b1)) - 1;
-    if (first != y) return;
+    const int id = a.ids[lane < a.M ? lane : 0];
+    const int e = __builtin_amdgcn_readlane(id, y);
+    const uint64_t same = __ballot(lane < a.M && id == e);
+    if (__ffsll(static_cast<unsigned long long>(same)) - 1 != y) return;
     off = blob_of(a.slots, e, a.E, a.need, a.pool_bytes);
-    count = __popcll(b0) + __popcll(b1);
-    if (wave == 0) {
-      if ((b0 >> lane) & 1ull) list[__popcll(b0 & lane_mask_lt(lane))] = lane;
-      if ((b1 >> lane) & 1ull) list[__popcll(b0) + __popcll(b1 & lane_mask_lt(lane))] = lane + kWave;
-    }
+    count = __popcll(same);
+    if (wave == 0 && ((same >> lane) & 1ull)) list[__popcll(same & lane_mask_lt(lane))] = lane;
     __syncthreads();
     pairs = list;
     if (off < 0 && tid == 0 && bx == 0) atomicOr(a.flags, 1u);
@@ -241,6 +243,7 @@ __global__ __launch_bounds__(NW* kWave) void k_mx_narrow(MxArgs a) {
     }
   }
 
+  static_assert(kDirectPairs <= kWave, "one id per lane");
   for (int g0 = 0; g0 < (MODE == kDirect ? count : 1); g0 += 16) {
     const int here = MODE == kDirect ? (count - g0 < 16 ? count - g0 : 16) : count;
     // A's rows: kDense and kSum from a uniform base, the others by the list
@@ -1049,7 +1052,7 @@ int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const
   g.pool_bytes = d->pool_bytes;
   // a gated product is not linear in its sums, so the weighted sum of a token
   // in one block is for the plain one
-  if (topk_w && T <= 8 && d->act == MX_ACT_NONE) {
+  if (topk_w && P <= kSumPairs && d->act == MX_ACT_NONE) {
     narrow<kSum>(g, d->a_dtype, d->act, T, s);
     return launched();
   }

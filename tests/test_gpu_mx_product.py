@@ -79,6 +79,7 @@ def test_linear_long_and_wide():
     linear(65, 130, 4096 + 256, seed=13, a="mx")
     linear(3500, 3600, 300, seed=14, out="bf16")                   # the largest tiles, ragged in every direction
     linear(2000, 1000, 700, seed=15, act="swiglu")
+    linear(3500, 1800, 260, seed=16, act="swiglu", out="bf16")
 
 
 def test_linear_nan_blocks_stay_in_their_rows():
@@ -188,7 +189,7 @@ def run_experts(x: Experts, T, k, a="bf16", out="f32", pair_rows=False, combine=
     return ws, o[:n_out]
 
 
-@pytest.mark.parametrize("T,k", [(1, 1), (1, 10), (2, 4), (8, 8), (9, 3), (13, 10), (33, 4), (64, 10), (200, 6)])
+@pytest.mark.parametrize("T,k", [(1, 1), (1, 10), (2, 4), (8, 4), (8, 8), (8, 10), (9, 3), (11, 3), (13, 10), (27, 3), (33, 4), (64, 10), (200, 6)])
 @pytest.mark.parametrize("pair_rows", [False, True])
 def test_experts_shapes(T, k, pair_rows):
     x = Experts(np.random.default_rng(1), 12, 70, 300)
