@@ -223,6 +223,48 @@ def test_experts_many():
     run_experts(x, 1, 64, combine=True, pair_rows=True)
 
 
+@pytest.mark.parametrize("T,k", [(900, 7), (2500, 9), (3100, 9)])
+def test_experts_more_pairs_than_a_grouping_step_holds(T, k):
+    """Every way of grouping: 4096 pairs a step in registers, two, six, and more pairs than those; some ids unusable."""
+    x = Experts(np.random.default_rng(14), 40, 20, 40)
+    ids, _ = routing(np.random.default_rng(T), T, 40, k)
+    ids[::17, 0] = -1
+    ids[5, :] = 40
+    ws, _ = run_experts(x, T, k, ids=ids)
+    with pytest.raises(M.MoeError):
+        M.status_check(ws)
+    run_experts(x, T, k, combine=True, pair_rows=True)
+
+
+def test_rows_of_a_beyond_four_gib():
+    """65536 rows of 131072 codes: whole numbers, so that every order of summing gives the same bits."""
+    K, rows_, N = 131072, 65536, 16
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    pick = torch.tensor([0x22, 0xA2, 0x2A, 0xAA], dtype=torch.uint8, device=DEV)      # pairs of +-1
+    codes = torch.empty(rows_, K // 2, dtype=torch.uint8, device=DEV)
+    for i in range(0, rows_, 4096):
+        codes[i:i + 4096] = pick[torch.randint(0, 4, (4096, K // 2), generator=gen, device=DEV, dtype=torch.int32)]
+    scales = torch.full((rows_, K // 32), 127, dtype=torch.uint8, device=DEV)
+    w = pick[torch.randint(0, 4, (N, K // 2), generator=gen, device=DEV, dtype=torch.int32)]
+    ws_ = scales[:N].contiguous()
+
+    def signs(c):
+        return torch.stack((1 - 2 * ((c >> 3) & 1).double(), 1 - 2 * (c >> 7).double()), -1).flatten(1)
+    at = [0, 1, 40000, 65534, 65535]
+    want = (signs(codes[at]) @ signs(w).T).float()
+    d = M.mx_product_desc(N, K, a="mx", out="f32")
+    out = torch.empty(rows_, N, device=DEV)
+    M.mx_linear(d, rows_, codes, scales, w, ws_, out, workspace(d, rows_))
+    assert torch.equal(out[at], want)
+    nc = N * K // 2
+    pool = torch.cat((w.flatten(), ws_.flatten()))
+    d = M.mx_product_desc(N, K, a="mx", out="f32", n_experts=1, top_k=1, pair_rows=True, scales_off=nc, pool_bytes=pool.numel())
+    out.zero_()
+    M.mx_experts(d, rows_, codes, scales, torch.zeros(rows_, 1, dtype=torch.int32, device=DEV), None,
+                 torch.zeros(1, dtype=torch.int64, device=DEV), pool, out, workspace(d, rows_))
+    assert torch.equal(out[at], want)
+
+
 @pytest.mark.parametrize("T", [2, 5, 40, 90])
 @pytest.mark.parametrize("combine", [False, True])
 def test_experts_unusable_ids_and_slots(T, combine):
