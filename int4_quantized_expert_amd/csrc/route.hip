@@ -521,11 +521,15 @@ __global__ __launch_bounds__(kRtWaves* kWave) void k_route(RouteArgs a) {
   Chosen c{0, 1.0};
   if constexpr (WIDE) {
     double* val = reinterpret_cast<double*>(smem) + static_cast<size_t>(wave) * a.E;
-    float bias[NJ];
+    float bias[NJ] = {};
+    if (a.bias) {
+      if constexpr (VEC) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int e = expert_of<VEC>(lane, j);
-      bias[j] = a.bias && (VEC || e < a.E) ? a.bias[e] : 0.f;
+        for (int j = 0; j < NJ; j += 4) __builtin_memcpy(bias + j, a.bias + expert_of<VEC>(lane, j), 16);
+      } else {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) bias[j] = lane + j * kWave < a.E ? a.bias[lane + j * kWave] : 0.f;
+      }
     }
     int L = kWave;   // lanes per group
     while (L * a.G > kWave) L >>= 1;
