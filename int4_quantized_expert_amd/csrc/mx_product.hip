@@ -371,9 +371,11 @@ __global__ __launch_bounds__(NW* kWave) void k_mx_narrow(MxArgs a) {
 // stages: while a chunk is multiplied the next S - 1 are on their way.  Their
 // scales go with every second chunk, 16 bytes of a row for two chunks (4-byte
 // loads with every chunk touched as many lines as the codes: 8192^3 took 308
-// instead of 282 us).  A row's eight 16-byte pieces are placed by piece ^ (row
-// mod 8), so that sixteen lanes reading one piece of sixteen rows hit
-// different banks.
+// instead of 282 us).  Of a row's eight 16-byte pieces, piece c lies at c ^ (row
+// mod 8) ^ (row / 8 mod 2), so that sixteen lanes reading one piece of sixteen
+// rows use all 64 banks once (without the last term half of them twice: five
+// times the bank conflicts, 301 against 299 us for 8192^3, 11.8 against 11.2
+// for 256 x 4096 x 4096).
 //   Rows of W past N and rows of A past M read as zeros (the buffer
 //   descriptors end there; a row's offset is in the lane's part of the
 //   address, which the bounds check compares with what the scalar part leaves)
@@ -382,6 +384,9 @@ __global__ __launch_bounds__(NW* kWave) void k_mx_narrow(MxArgs a) {
 //   Every wave issues the same number of loads for a chunk (a wave without a
 //   share repeats the last one, the same bytes to the same place), so that all
 //   but the newest chunk's have landed once no more than that number is left.
+//   Bound: 8192^3 by the clock that its power leaves (2.0 GHz, the matrix units
+// busy 40% of the time; the same instructions on registers alone, with random
+// codes, reach 7.1 PFLOP/s), 3.9 PFLOP/s; experts by the reads of W, 4.4 TB/s.
 //   KS = 2: a stage is two chunks, and two groups of waves multiply one each,
 //   their sums joined at the end.  For long rows of tiles that do not fill the
 //   GPU: 512 x 2048 x 8192 takes 19.0 instead of 21.8 us, 256 x 4096 x 4096
@@ -497,7 +502,7 @@ __global__ __launch_bounds__(KS* WM* WN* kWave) void k_mx_tile(MxArgs a) {
     for (int i = 0; i < C::kPC; ++i) {
       int g = wave + i * C::kWaves;
       g = (g < KS * C::kCodeGroups ? g : KS * C::kCodeGroups - 1) % C::kCodeGroups;
-      vc[i] = row_at(g * 8 + (lane >> 3)) * pitch + static_cast<uint32_t>(((lane & 7) ^ (lane >> 3)) << 4);
+      vc[i] = row_at(g * 8 + (lane >> 3)) * pitch + static_cast<uint32_t>(((lane & 7) ^ (lane >> 3) ^ (g & 1)) << 4);
     }
 #pragma unroll
     for (int i = 0; i < C::kPS; ++i) {
@@ -561,16 +566,17 @@ __global__ __launch_bounds__(KS* WM* WN* kWave) void k_mx_tile(MxArgs a) {
         sw[j] = *reinterpret_cast<const uint16_t*>(ss + (C::kAScales * 64 + wrow(j) + r) * 16 + q * 2);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const int at = ((2 * q + s) ^ (r & 7)) << 4;
+        const int at = ((2 * q + s) ^ (r & 7) ^ (r >> 3)) << 4;
         v4i fa[TM], fw[TN];
 #pragma unroll
         for (int j = 0; j < TN; ++j) fw[j] = *reinterpret_cast<const v4i*>(st + (C::kBM + wrow(j) + r) * 128 + at);
 #pragma unroll
         for (int i = 0; i < TM; ++i) fa[i] = *reinterpret_cast<const v4i*>(st + ((wm * TM + i) * 16 + r) * 128 + at);
+        // one W tile with all of A's: 281 against 287 us for 8192^3 the other way round
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+        for (int j = 0; j < TN; ++j)
 #pragma unroll
-          for (int j = 0; j < TN; ++j) acc[i][j] = mfma4(fw[j], fa[i], acc[i][j], sw[j], sa[i], s);
+          for (int i = 0; i < TM; ++i) acc[i][j] = mfma4(fw[j], fa[i], acc[i][j], sw[j], sa[i], s);
       }
     }
   }
