@@ -37,7 +37,7 @@ constexpr int kSumPairs = 80;
 
 enum Mode { kDense, kDirect, kTiles, kSum };
 
-// A tile of the grouped path: up to `tile` pairs of one expert.
+// A tile of the grouped path: up to PrepArgs::rows pairs of one expert.
 struct MxTile {
   int64_t off;    // the expert's blob in the pool; -1: unusable, the rows are zero
   int32_t first;  // place of its first pair in the list
@@ -268,10 +268,10 @@ __global__ __launch_bounds__(NW* kWave) void k_mx_narrow(MxArgs a) {
     RawPart<SRC> A[MT];
     RawPart<kMxF4> W[NM];
     float w = 1.f;
+    bool usable = true;
     const auto load = [&](int task) {
       int chunk = task;
       const uint8_t *wc = a.wc, *wsc = a.wsc;
-      bool usable = true;
       int64_t o = off;
       if constexpr (MODE == kSum) {
         const int i = task / a.chunks;
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(NW* kWave) void k_mx_narrow(MxArgs a) {
         load_values<SRC>(av, row[0] * a.K + c0, a.K - c0, r < here, A[0]);
       }
       if constexpr (MODE != kDense) {
-        usable = o >= 0;
+        usable = o >= 0;   // an unusable expert's product is zero, whatever A holds
         wc = a.pool + o + a.codes_off;
         wsc = a.pool + o + a.scales_off;
       }
@@ -311,7 +311,8 @@ __global__ __launch_bounds__(NW* kWave) void k_mx_narrow(MxArgs a) {
     for (int task = wave;; task += NW) {
       Part pa[MT], pw[NM];
       const float w0 = w;
-      if (have) {
+      const bool product = have && usable;
+      if (product) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) pa[t] = finish_part<SRC>(A[t]);
 #pragma unroll
@@ -319,7 +320,7 @@ __global__ __launch_bounds__(NW* kWave) void k_mx_narrow(MxArgs a) {
       }
       const bool more = task < tasks;
       if (more) load(task);
-      if (have) {
+      if (product) {
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -638,7 +639,7 @@ constexpr int kPrepThr = 1024;
 
 struct PrepArgs {
   MxArgs g;
-  int P, rows;            // pairs; pairs per tile
+  int P, rows;            // pairs; most pairs of a tile
   int32_t* place;
   int32_t* plist;
   MxTile* tiles;

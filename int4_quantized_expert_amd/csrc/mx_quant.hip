@@ -4,8 +4,10 @@
 // handful of instructions each.  Four lanes share a block of 32 values, eight
 // values a lane, so that a wave's 16-byte loads and 4-byte stores are
 // contiguous; the block's largest magnitude takes two lane exchanges.  A
-// thread handles kIter such pieces, kThreads * 8 values apart, all requested
-// before any is used.
+// thread handles kIter such pieces, kQThr pieces apart, all requested before
+// any is used.  131072 x 2048 bf16 values take 149 us to quantise (4.6 TB/s; a
+// large copy reaches 4.75) and 103 us back (6.6 TB/s, part of it into the
+// last-level cache); 8 x 2048 take 2.7 and 2.5 us, an empty kernel's time.
 #include <hip/hip_runtime.h>
 
 #include <cstdio>

@@ -151,6 +151,18 @@ class Experts:
             y[t, i], b[t, i] = expected(av[t * k + i] if pair_rows else av[t], self.values[e], self.act, self.K)
         return y, b
 
+    def expect_sum(self, av, ids, w, pair_rows, lost=()):
+        """The weighted sums and their bound: the products' own, and the sum's additions over the terms' magnitudes."""
+        T, k = ids.shape
+        y, b = self.expect(av, ids, pair_rows, lost)
+        mag = np.zeros_like(y)
+        for e in np.unique(ids):
+            if 0 <= e < self.E and e not in lost:
+                t, i = np.nonzero(ids == e)
+                r = av[t * k + i] if pair_rows else av[t]
+                mag[t, i] = np.abs(y[t, i]) if self.act == "swiglu" else np.abs(r) @ np.abs(self.values[e]).T
+        return (w[..., None] * y).sum(1), (w[..., None] * b).sum(1) + 2 * g(k + 32) * (w[..., None] * mag).sum(1)
+
 
 def routing(rng, T, E, k, hot=0.0):
     ids = np.stack([rng.choice(E, size=k, replace=False) for _ in range(T)]).astype(np.int32)
@@ -172,19 +184,10 @@ def run_experts(x: Experts, T, k, a="bf16", out="f32", pair_rows=False, combine=
     M.mx_experts(d, T, at, a_s, dev(ids), dev(w.astype(np.float32)) if combine else None, x.slots, x.pool, o[:n_out], ws)
     torch.cuda.synchronize()
     assert (o[n_out] == 9.0).all()
-    y, b = x.expect(av, ids, pair_rows, lost)
     if combine:
-        # the terms' magnitudes bound the sum's own roundings
-        mag = np.zeros_like(y)
-        for e in np.unique(ids):
-            if 0 <= e < x.E and e not in lost:
-                t, i = np.nonzero(ids == e)
-                r = av[t * k + i] if pair_rows else av[t]
-                mag[t, i] = np.abs(y[t, i]) if x.act == "swiglu" else np.abs(r) @ np.abs(x.values[e]).T
-        b = (w[..., None] * b).sum(1) + 2 * g(k + 32) * (w[..., None] * mag).sum(1)
-        y = (w[..., None] * y).sum(1)
+        y, b = x.expect_sum(av, ids, w, pair_rows, lost)
     else:
-        y, b = y.reshape(T * k, -1), b.reshape(T * k, -1)
+        y, b = (v.reshape(T * k, -1) for v in x.expect(av, ids, pair_rows, lost))
     close(o[:n_out], y, b, out, f"T={T} k={k} {a} {out} pair_rows={pair_rows} combine={combine}")
     return ws, o[:n_out]
 
@@ -283,6 +286,28 @@ def test_experts_unusable_ids_and_slots(T, combine):
     ws, _ = run_experts(x, T, 4, combine=combine, ids=np.full((T, 4), 2, dtype=np.int32), lost=(3, 5))
     M.status_check(ws)
     run_experts(x, T, 4, combine=combine, ids=np.full((T, 4), -3, dtype=np.int32), lost=(3, 5))
+
+
+@pytest.mark.parametrize("T", [2, 30, 60])
+@pytest.mark.parametrize("combine", [False, True])
+def test_an_unusable_pair_is_zero_whatever_its_row_holds(T, combine):
+    """A NaN in the input row of a pair without an expert reaches no output."""
+    rng = np.random.default_rng(15)
+    x = Experts(rng, 6, 40, 300)
+    ids, w = routing(rng, T, 6, 3)
+    ids[1, 2] = 6
+    av, at, _ = a_side(rng, T * 3, 300, "bf16")
+    at[1 * 3 + 2, 7] = float("nan")
+    d = x.desc(3, pair_rows=True)
+    o = torch.full((T if combine else T * 3, 40), float("nan"), device=DEV)
+    M.mx_experts(d, T, at, None, dev(ids), dev(w.astype(np.float32)) if combine else None, x.slots, x.pool, o, workspace(d, T))
+    torch.cuda.synchronize()
+    assert torch.isfinite(o).all()
+    if combine:
+        close(o, *x.expect_sum(av, ids, w, True), "f32")
+    else:
+        close(o, *(v.reshape(-1, 40) for v in x.expect(av, ids, True)), "f32")
+        assert not o[1 * 3 + 2].any()
 
 
 def test_experts_no_tokens():
