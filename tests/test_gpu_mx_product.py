@@ -411,6 +411,26 @@ def test_captured_and_replayed(T):
         M.status_check(a["ws"])
 
 
+def test_launch_timer_counts_the_kernels():
+    x = Experts(np.random.default_rng(16), 8, 40, 300)
+    ids, w = routing(np.random.default_rng(1), 60, 8, 3)
+    d = x.desc(3)
+    a, it, wt = torch.randn(60, 300, device=DEV).to(torch.bfloat16), dev(ids), dev(w.astype(np.float32))
+    out, ws = torch.zeros(60, 40, device=DEV), workspace(d, 60)
+    timer = M.LaunchTimer(8)
+    timer.arm()
+    M.mx_experts(d, 60, a, None, it, wt, x.slots, x.pool, out, ws)      # grouping, product, weighted sum
+    torch.cuda.synchronize()
+    assert timer.n_recorded == 6 and all(0 < t < 1e5 for t in timer.kernel_us())
+    M.mx_experts(d, 60, a, None, it, wt, x.slots, x.pool, out, ws)      # not armed again
+    assert timer.n_recorded == 6
+    timer.arm()
+    M.route(M.route_desc(8, 2), 60, torch.randn(60, 8, device=DEV), None, torch.zeros(60, 2, dtype=torch.int32, device=DEV),
+            torch.zeros(60, 2, device=DEV))
+    torch.cuda.synchronize()
+    assert timer.n_recorded == 2
+
+
 def test_two_streams_with_their_own_workspaces():
     rng = np.random.default_rng(11)
     x = Experts(rng, 8, 64, 512)
