@@ -413,6 +413,23 @@ struct TileCfg {
   static_assert(KS == 1 || kGroup * TM * TN * 1024 <= S * kStage, "the joined sums fit the stages");
 };
 
+// A direct load of 16 bytes a lane (lane l's land at lds + 16 l), as lds_load<16>
+// of device_common.h but with the five wait states that a vector memory
+// instruction needs behind a vector instruction that wrote one of its scalar
+// operands: the compiler does not look into the assembly, and the offset may
+// come from v_readfirstlane.
+__device__ __forceinline__ void lds_copy(u32x4 rs, uint8_t* lds, uint32_t voff, int soff) {
+  const uint32_t la = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_u8*)lds)));
+  const uint32_t so = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(soff));
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 4\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(la), "v"(voff), "s"(rs), "s"(so)
+      : "memory");
+}
+
 __device__ __forceinline__ int64_t clamp32(int64_t n) { return n < 0xfffffff0ll ? n : 0xfffffff0ll; }
 
 template <int N>
@@ -523,7 +540,7 @@ __global__ __launch_bounds__(KS* WM* WN* kWave) void k_mx_tile(MxArgs a) {
         int chunk = stage * KS + g / C::kCodeGroups;
         if (KS == 2 && chunk >= a.chunks) chunk = a.chunks - 1;   // not multiplied
         const u32x4 rs = row < C::kBM ? ra : (NM == 2 && row >= C::kBM + kCols ? rw[NM - 1] : rw[0]);
-        lds_load<16>(rs, st + g * 1024, vc[i], chunk * 128);
+        lds_copy(rs, st + g * 1024, vc[i], chunk * 128);
       }
       if (KS == 1 && (stage & 1)) return;
       uint8_t* ss = smem + S * C::kStage + sput * C::kScales;
@@ -534,7 +551,7 @@ __global__ __launch_bounds__(KS* WM* WN* kWave) void k_mx_tile(MxArgs a) {
         g = g < C::kScaleGroups ? g : C::kScaleGroups - 1;
         const int row = (g - C::kAScales) * 64;   // of W
         const u32x4 rs = g < C::kAScales ? ras : (NM == 2 && row >= kCols ? rws[NM - 1] : rws[0]);
-        lds_load<16>(rs, ss + g * 1024, vs[i], stage * KS * 8);
+        lds_copy(rs, ss + g * 1024, vs[i], stage * KS * 8);
       }
     };
 

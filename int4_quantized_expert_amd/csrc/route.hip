@@ -225,9 +225,11 @@ __device__ __forceinline__ int topk64(const uint32_t (&key32)[NJ], const uint64_
 
 __device__ __forceinline__ float second_of(float hi, float lo, float v) { return __builtin_amdgcn_fmed3f(hi, lo, v); }
 __device__ __forceinline__ double second_of(double hi, double lo, double v) { return v > hi ? hi : (v > lo ? v : lo); }
-__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+// Of two numbers (no NaN comes here) in one instruction each, as the middle of
+// three: fmaxf and fminf would first quiet both.
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
 __device__ __forceinline__ double larger(double a, double b) { return a > b ? a : b; }
-__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, -INFINITY); }
 __device__ __forceinline__ double smaller(double a, double b) { return a < b ? a : b; }
 
 template <int S>
@@ -292,11 +294,15 @@ __device__ __forceinline__ double readlane_f(double v, int l) {
 // 1 for the experts of the groups in `keep` (bit g L: group g), else 0.
 template <int NJ, bool VEC>
 __device__ __forceinline__ void mark_groups(uint64_t keep, const RouteArgs& a, int L, int lane, uint32_t (&mark)[NJ]) {
+  const uint32_t n = static_cast<uint32_t>(a.E);
+  const auto kept = [&](uint32_t e) { return e < n && ((keep >> (((e * a.ginv) >> 20) * L)) & 1ull) ? 1u : 0u; };
+  if (VEC && (a.gsize & 3) == 0) {   // four neighbours are of one group
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const uint32_t e = static_cast<uint32_t>(expert_of<VEC>(lane, j)), n = static_cast<uint32_t>(a.E);
-    const uint32_t g = e < n ? (e * a.ginv) >> 20 : 0u;
-    mark[j] = e < n && ((keep >> (g * L)) & 1ull) ? 1u : 0u;
+    for (int j = 0; j < NJ; j += 4)
+      mark[j] = mark[j + 1] = mark[j + 2] = mark[j + 3] = kept(static_cast<uint32_t>(expert_of<VEC>(lane, j)));
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) mark[j] = kept(static_cast<uint32_t>(expert_of<VEC>(lane, j)));
   }
 }
 
@@ -442,11 +448,17 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs& a, const float (&l)
     for (int j = 0; j < NJ; ++j) key[j] = VEC || expert_of<VEC>(lane, j) < a.E ? 1u : 0u;
   }
   const bool by_score = a.bias != nullptr;
+  const auto key_of = [](float x) {   // order_key of a number; + 0 gives both zeros one key
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+  };
+  // a NaN logit has not come this far: its magnitude was refused above
+  if (by_score) {
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const float x = (by_score || l[j] != l[j] ? v[j] : l[j]) + 0.f;   // one key for both zeros
-    const uint32_t b = __float_as_uint(x);
-    key[j] = key[j] ? b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u) : 0u;
+    for (int j = 0; j < NJ; ++j) key[j] = key[j] ? key_of(v[j]) : 0u;
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) key[j] = key[j] ? key_of(l[j]) : 0u;
   }
   const uint32_t theta = kth_bound<NJ>(key, a.k);
   uint32_t from = theta > 1u ? theta : 1u;
@@ -571,7 +583,15 @@ __global__ __launch_bounds__(kRtWaves* kWave) void k_route(RouteArgs a) {
     else sc = exp(static_cast<double>(lc) - static_cast<double>(mx));
   }
   if (a.renorm) {
-    const double sum = wave_sum_d(sc, lane);
+    double sum = sc;
+    sum += lane_xor_d<1>(sum, lane);
+    sum += lane_xor_d<2>(sum, lane);
+    sum += lane_xor_d<4>(sum, lane);
+    sum += lane_xor_d<8>(sum, lane);
+    if (a.k > 16) {
+      sum += lane_xor_d<16>(sum, lane);
+      sum += lane_xor_d<32>(sum, lane);
+    }
     sc = sum == 0.0 ? 0.0 : sc / sum;
   } else if (!SIGMOID) {
     sc /= c.denom;
