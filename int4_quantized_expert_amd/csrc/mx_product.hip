@@ -188,6 +188,8 @@ __device__ __forceinline__ void store_out(void* out, int64_t i, float y, int bf1
 // token), its waves take the chunks of k in turn and their sums are joined in
 // LDS.  Bound by the reads of W and the chain of dependent loads before them
 // (ids, slots); A is read, and quantised, by every block, while W is on its way.
+// One token by 4096 x 2048: 4.4 us; through ten experts' gate and up rows (512
+// outputs, k = 2048): 7.4 us, 1.5 TB/s.
 //   kDense   rows 16 MT y .. of A
 //   kDirect  y is a pair; the block of the first pair of an expert takes all
 //            of that expert's pairs, the others end
@@ -651,7 +653,8 @@ __global__ __launch_bounds__(KS* WM* WN* kWave) void k_mx_tile(MxArgs a) {
 // consecutive ids a load, all requested at once) and are placed in LDS, from
 // where the list is written in order (scattered 4-byte stores to memory took
 // half of 18 us for 20480 pairs); more are read again and placed in memory
-// (NI = 0).
+// (NI = 0).  20480 pairs and 2048 x 2048 bf16 values take 11 us, 512 pairs and
+// 512 x 512 values 3.9 us.
 constexpr int kPrepThr = 1024;
 
 struct PrepArgs {
@@ -783,7 +786,9 @@ __global__ __launch_bounds__(kPrepThr) void k_mx_prep(PrepArgs p) {
   }
 }
 
-// out[t] = sum_i w[t, i] rows[t k + i], i ascending.
+// out[t] = sum_i w[t, i] rows[t k + i], i ascending.  The rows are fp32: half
+// the bytes would round every product before the sum.  64 tokens' 8 rows of
+// 2048: 4.0 us, little over a launch.
 __global__ __launch_bounds__(256) void k_mx_combine(const float* rows, const float* wts, int k, int N, void* out,
                                                     int bf16) {
   const int nblk = (N + 255) / 256;

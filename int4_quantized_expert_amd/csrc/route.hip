@@ -513,10 +513,10 @@ __device__ __forceinline__ float row_max(const float (&l)[NJ], int lane) {
 
 // NJ: logits per lane (E <= 64 NJ).  WIDE: experts or groups are compared by
 // scores (a bias or groups).  VEC: E = 64 NJ and aligned rows.
-// Bound by the instructions of a token's wave (about 680 vector and 330 scalar
-// ones with groups): 32768 tokens of 512 bf16 logits in 8 groups take 49.5 us,
-// six times the time of reading them; one token of 256 takes 3.6 us, 2048 of
-// 512 without groups 4.4 us, both little over a launch.
+// Bound by the instructions of a token's wave (607 vector and 315 scalar ones
+// with groups): 32768 tokens of 512 bf16 logits in 8 groups take 46 us, six
+// times the time of reading them; one token of 256 takes 3.4 us, 2048 of 512
+// without groups 4.5 us, both little over a launch.
 // Several tokens per wave, sharing the bias and the evaluation of the weights,
 // were slower (four 62, eight 65, sixteen 87 us against one's 59): fewer waves
 // hide less of each other's exchanges.
