@@ -133,8 +133,11 @@ int mx_linear_forward(const mx_product_desc* d, int32_t M, const void* a, const 
  *                in fp32 in a fixed order and rounded once
  *   slot_table   [E] int64 byte offsets
  * A pair whose id is outside [0, E) or whose slot is unusable contributes
- * nothing (its row is zero) and raises MOE_ERANGE in moe_status_check(workspace).
- * An expert may occur twice in a token's ids.  Errors as above.
+ * nothing, whatever its row of A and its weight hold (its row of the output is
+ * zero), and raises MOE_ERANGE in moe_status_check(workspace).  An expert may
+ * occur twice in a token's ids.  MOE_EINVAL also where a launch would need 2^32
+ * threads or more (T n of 2^32 columns, 2^35 values of A to quantise).  Errors
+ * as above.
  */
 int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const void* a_scales,
                        const int32_t* topk_ids, const float* topk_w, const int64_t* slot_table, const void* pool_base,

@@ -786,18 +786,38 @@ __global__ __launch_bounds__(kPrepThr) void k_mx_prep(PrepArgs p) {
   }
 }
 
-// out[t] = sum_i w[t, i] rows[t k + i], i ascending.  The rows are fp32: half
-// the bytes would round every product before the sum.  64 tokens' 8 rows of
-// 2048: 4.0 us, little over a launch.
-__global__ __launch_bounds__(256) void k_mx_combine(const float* rows, const float* wts, int k, int N, void* out,
-                                                    int bf16) {
-  const int nblk = (N + 255) / 256;
-  const int64_t t = blockIdx.x / nblk;
-  const int n = (blockIdx.x % nblk) * 256 + threadIdx.x;
-  if (n >= N) return;
-  float y = 0.f;
-  for (int i = 0; i < k; ++i) y = fmaf(wts[t * k + i], rows[(t * k + i) * N + n], y);
-  store_out(out, t * N + n, y, bf16);
+// out[t] = sum_i w[t, i] rows[t k + i], i ascending, over the pairs that have an
+// expert (a weight of another pair may be anything).  The rows are fp32: half
+// the bytes would round every product before the sum.  Ids, rows and slots are
+// requested in this order, so that the rows come while the slots are looked up.
+// 64 tokens' 8 rows of 2048: 4.0 us, little over a launch.
+__global__ __launch_bounds__(256) void k_mx_combine(MxArgs a, const float* rows) {
+  constexpr int kStep = 8;
+  const int t = blockIdx.x / a.nblk, lane = threadIdx.x & (kWave - 1);
+  const int n = (blockIdx.x % a.nblk) * 256 + threadIdx.x;
+  const int64_t p0 = static_cast<int64_t>(t) * a.k;
+  const int at = lane < a.k ? lane : 0;   // k <= 64
+  const int id = a.ids[p0 + at];
+  const float w = a.wts[p0 + at];
+  const float* row = rows + p0 * a.N + (n < a.N ? n : a.N - 1);
+  float v[kStep], y = 0.f;
+  const auto load = [&](int i0) {
+#pragma unroll
+    for (int x = 0; x < kStep; ++x) v[x] = row[static_cast<int64_t>(i0 + x < a.k ? i0 + x : a.k - 1) * a.N];
+  };
+  load(0);
+  const uint64_t usable = __ballot(lane < a.k && blob_of(a.slots, id, a.E, a.need, a.pool_bytes) >= 0);
+  for (int i0 = 0;;) {
+#pragma unroll
+    for (int x = 0; x < kStep; ++x) {
+      const int i = i0 + x < kWave ? i0 + x : kWave - 1;
+      if (i0 + x < a.k && ((usable >> i) & 1ull)) y = fmaf(readlane_f(w, i), v[x], y);
+    }
+    i0 += kStep;
+    if (i0 >= a.k) break;
+    load(i0);
+  }
+  if (n < a.N) store_out(a.out, static_cast<int64_t>(t) * a.N + n, y, a.out_bf16);
 }
 
 // ---------------------------------------------------------------------------
@@ -836,11 +856,24 @@ int check_product(const mx_product_desc* d, bool experts) {
   return MOE_OK;
 }
 
+// The tiles' offsets into A have 32 bits.
+bool far_rows(int64_t rows, int k) { return rows * (mx_padded(k) / 2) >= (int64_t(1) << 32) - 65536; }
+
 int check_rows(const mx_product_desc& d, int32_t T, bool experts) {
   if (T < 0 || T > (experts ? 65536 : (1 << 20))) return bad("%lld rows are negative or too many", T);
   if (static_cast<int64_t>(T) * (experts ? d.top_k : 1) * ((d.n + 15) / 16) >= (int64_t(1) << 31))
     return bad("%lld rows of %lld columns are too many for one launch", static_cast<long long>(T) * (experts ? d.top_k : 1), d.n);
-  if (experts && static_cast<int64_t>(T) * d.top_k >= (1 << 22)) return bad("T * top_k = %lld must be below 2^22", static_cast<long long>(T) * d.top_k);
+  if (!experts) return MOE_OK;
+  const int64_t P = static_cast<int64_t>(T) * d.top_k;
+  if (P >= (1 << 22)) return bad("T * top_k = %lld must be below 2^22", P);
+  // a launch holds fewer than 2^32 threads: those of the sums over a token's
+  // experts, of the quantisation and of the few-row kernel over grouped rows
+  const int64_t rows = d.pair_rows ? P : T, row_codes = mx_padded(d.k) / 2, most = int64_t(1) << 32;
+  if (T * ((d.n + 255) / 256 * int64_t(256)) >= most) return bad("%lld rows of %lld columns are too many for one launch", T, d.n);
+  if (d.a_dtype != MX_FP4 && rows * row_codes / 4 >= most - 2048)
+    return bad("%lld rows of %lld values are too many to quantise in one launch", rows, d.k);
+  if (far_rows(rows, d.k) && (P / 16 + d.n_experts + 1) * ((d.n + 15) / 16) * 512 >= most)
+    return bad("%lld pairs of %lld columns are too many for one launch", P, d.n);
   return MOE_OK;
 }
 
@@ -1105,11 +1138,9 @@ int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const
     // rows per tile by the pairs that an expert has on average (gate and up
     // rows, 512 outputs, k = 2048; tiles of 32, 64 and 128 rows): 16 pairs 63,
     // 65, 76 us; 32 pairs 77, 72, 83; 64 pairs 102, 90, 92; 96 pairs 70, 61,
-    // 56; 256 pairs 76, 63, 58.  The tiles' offsets into A have 32 bits; an A
-    // beyond 4 GiB takes the kernel of few rows
+    // 56; 256 pairs 76, 63, 58.  An A beyond 4 GiB takes the kernel of few rows
     const int each = P / d->n_experts;
-    const bool far = rows * (mx_padded(d->k) / 2) >= (int64_t(1) << 32) - 65536;
-    const int bm = far ? 16 : each >= 96 ? 128 : each >= 24 ? 64 : 32;
+    const int bm = far_rows(rows, d->k) ? 16 : each >= 96 ? 128 : each >= 24 ? 64 : 32;
     PrepArgs p{};
     p.g = g;
     p.P = P;
@@ -1143,9 +1174,13 @@ int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const
     else rc = tile<2, 2, 4, 4, 2, 1, true>(g, d->act, most, s);
     if (rc != MOE_OK) return api_fail(MOE_EHIP, "the product kernel's LDS size was refused");
   }
-  if (topk_w)
-    launch_kernel(k_mx_combine, dim3(static_cast<uint32_t>((d->n + 255) / 256) * T), dim3(256), 0, s, reinterpret_cast<const float*>(ws + L.rows),
-                  topk_w, d->top_k, d->n, out, d->out_dtype == MOE_BF16);
+  if (topk_w) {
+    const float* sums = static_cast<const float*>(g.out);
+    g.out = out;
+    g.out_bf16 = d->out_dtype == MOE_BF16;
+    g.nblk = (d->n + 255) / 256;
+    launch_kernel(k_mx_combine, dim3(static_cast<uint32_t>(g.nblk) * T), dim3(256), 0, s, g, sums);
+  }
   return launched();
 }
 

@@ -178,7 +178,7 @@ int mx_quantize(int32_t dtype, int64_t rows, int64_t cols, const void* x, int64_
   MarkScope marks;
   if (const int rc = check_matrix(dtype, rows, cols, x, x_stride, codes, scales)) return rc;
   if (rows == 0 || cols == 0) return api_ok();
-  if ((rows * (mx_padded(cols) / 8) + 1023) / 1024 > 0x7fffffffLL) return bad("rows * cols is too large for one launch");
+  if (rows * (mx_padded(cols) / 8) / kIter >= (int64_t(1) << 32) - 2048) return bad("rows * cols is too large for one launch");
   launch_mx_quantize(dtype, rows, cols, x, rows > 1 ? x_stride : 0, codes, scales, static_cast<hipStream_t>(stream));
   return launched();
 }
@@ -191,7 +191,7 @@ int mx_dequantize(int32_t dtype, int64_t rows, int64_t cols, const void* codes, 
   if (rows == 0 || cols == 0) return api_ok();
   const uint32_t per_row = static_cast<uint32_t>(mx_padded(cols) / 8);
   const int64_t pieces = rows * per_row, blocks = (pieces + kQThr * kIter - 1) / (kQThr * kIter);
-  if (blocks > 0x7fffffffLL) return bad("rows * cols is too large for one launch");
+  if (blocks * kQThr >= int64_t(1) << 32) return bad("rows * cols is too large for one launch");
   const dim3 grid(static_cast<uint32_t>(blocks)), block(kQThr);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t st = rows > 1 ? out_stride : 0;

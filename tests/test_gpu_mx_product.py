@@ -310,6 +310,27 @@ def test_an_unusable_pair_is_zero_whatever_its_row_holds(T, combine):
         assert not o[1 * 3 + 2].any()
 
 
+@pytest.mark.parametrize("T", [2, 8, 30, 60])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+@pytest.mark.parametrize("weight", [float("nan"), float("inf"), -2.0])
+def test_the_weight_of_an_unusable_pair_may_be_anything(T, act, weight):
+    """A padded batch: the last token has ids of no expert, and one pair of another token is lost; their weights are
+    not numbers.  The padded token's sum is zero, everything else as without them.  More experts than a step of the sum."""
+    rng = np.random.default_rng(16)
+    x = Experts(rng, 16, 40, 300, act=act)
+    ids, w = routing(rng, T, 16, 10)
+    ids[T - 1], ids[0, 9] = -1, 16
+    given = w.astype(np.float32)
+    given[T - 1], given[0, 9] = weight, weight
+    av, at, _ = a_side(rng, T, 300, "bf16")
+    o = torch.full((T, 40), float("nan"), device=DEV)
+    d = x.desc(10)
+    M.mx_experts(d, T, at, None, dev(ids), dev(given), x.slots, x.pool, o, workspace(d, T))
+    torch.cuda.synchronize()
+    assert not o[T - 1].any()
+    close(o, *x.expect_sum(av, ids, w, False), "f32")
+
+
 def test_experts_no_tokens():
     x = Experts(np.random.default_rng(7), 4, 16, 32)
     d = x.desc(2)

@@ -104,6 +104,9 @@ def test_mx_quantize_refusals():
         assert call(fn, x=h.p + 2) == -1 and call(fn, codes=h.p + 65544) == -1 and call(fn, scales=h.p + 131080) == -1
         assert call(fn, codes=h.p + 512) == -1 and call(fn, scales=h.p + 65536 + 256) == -1
         assert call(fn, rows=0) == 0 and call(fn, cols=0) == 0
+    far = 1 << 46                               # 2^37 values: more threads than a launch holds
+    for fn in (L.mx_quantize, L.mx_dequantize):
+        assert call(fn, rows=1 << 17, cols=1 << 20, stride=1 << 20, codes=far, scales=far << 1) == -1
     with pytest.raises(M.MoeError):
         M.mx_quantize(torch.zeros(2, 64, dtype=torch.float16), h.p, h.p)
     with pytest.raises(M.MoeError):
@@ -174,6 +177,12 @@ def test_mx_experts_bad_arguments():
     assert call(w=h.p + 8193) == -1
     assert call(out=h.p + 65536 + 512) == -1 and call(out=h.p + 8192) == -1 and call(ws=h.p + 65536) == -1
     assert call(T=0) == 0
+    # launches of 2^32 threads: the sum over experts, the quantisation, pairs by few rows (A beyond 4 GiB)
+    for n, k, a_dtype, top_k, T in ((1 << 16, 64, "bf16", 1, 1 << 16), (64, 1 << 19, "bf16", 1, 1 << 16),
+                                    (1 << 17, 1 << 20, "mx", 1, 1 << 14)):
+        big = M.mx_product_desc(n, k, a=a_dtype, n_experts=4, top_k=top_k, scales_off=1 << 38, pool_bytes=1 << 39)
+        assert L.mx_workspace_bytes(ctypes.byref(big), T) == 0, (n, k)
+        assert L.mx_workspace_bytes(ctypes.byref(big), T // 8) > 0, (n, k)
     with pytest.raises(M.MoeError):
         M.mx_experts(d, 4, torch.zeros(4, 64, dtype=torch.bfloat16), None, torch.zeros(4, 2, dtype=torch.int64), None, h.p, h.p,
                      h.p, torch.zeros(need, dtype=torch.uint8))
