@@ -8,13 +8,15 @@
 // double precision for all E experts; without bias and groups every score
 // grows with its logit and the logits are compared instead.  Most tokens need
 // neither: fp32 scores with a proven bound on their error decide wherever the
-// keys that matter lie further apart than the bound, and only the other tokens
-// (a group or a neighbour within 2^-18 or so) go through double precision.
+// keys that matter lie further apart than the bound.  Where neighbours do not,
+// the few candidates alone are ranked again in double precision (sigmoid); where
+// groups do not, or a softmax's terms, all E scores are formed so.  That
+// is many times the usual work: rows that the mask leaves empty (2% of them)
+// and near ties together took 15 of 46 us that way.
 //
 // Organisation.  A token's E logits are spread over one wave (a lane holds
 // every 64th expert, or groups of four neighbours where E fills the wave and
-// rows are aligned), nothing crosses waves, and a block is four independent
-// tokens.
+// rows are aligned), and a block is four tokens whose choices are independent.
 //   - The groups' scores: their values go through LDS once; 64 / G lanes scan
 //     one group each for its two largest and merge by lane exchanges.
 //   - Top-k: the largest threshold with at least k lane maxima at or above it
@@ -378,11 +380,13 @@ __device__ __forceinline__ Chosen choose_exact(const RouteArgs& a, const float (
 // top_groups others that may lie above it, one that goes at least that many
 // that do, by more than twice the bound.  Experts: every entry within 2 eps of
 // the bound on the k-th largest is a candidate, and neighbours among the first
-// k + 1 have to differ by more than 2 eps (a logit is exact).
-// Returns false where it is not certain (equal keys, empty groups).
-template <int NJ, bool SIGMOID, bool VEC>
-__device__ __forceinline__ bool choose_fast(const RouteArgs& a, const float (&l)[NJ], const float (&bias)[NJ], float mx,
-                                            int L, int lane, WaveLds* lds, float* val, int* id) {
+// k + 1 have to differ by more than 2 eps (a logit is exact), or the candidates
+// are ranked by double precision.
+// Returns false where it is not certain (groups within the bound, more than 64
+// candidates).
+template <int NJ, int DT, bool SIGMOID, bool VEC>
+__device__ __forceinline__ bool choose_fast(const RouteArgs& a, int64_t row, const float (&l)[NJ], const float (&bias)[NJ],
+                                            float mx, int L, int lane, WaveLds* lds, float* val, int* id) {
   constexpr float kLog2e = 1.4426950408889634f, u = 5.9604644775390625e-8f;
   float v[NJ];
   if (SIGMOID) {
@@ -404,13 +408,19 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs& a, const float (&l)
   }
   // the largest magnitude as whole numbers: infinities and NaN come out on top
   uint32_t top = 0;
+  uint64_t empty = ~0ull;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     const bool out = l[j] == -INFINITY;
     const float x = v[j] + bias[j];
-    const uint32_t m = out ? 0u : __float_as_uint(x) & 0x7fffffffu;
+    const uint32_t m = __float_as_uint(x) & 0x7fffffffu;
     top = m > top ? m : top;
+    empty &= __ballot(out);
     v[j] = out ? -INFINITY : x;
+  }
+  if (empty == ~0ull) {   // the mask leaves nothing: all keys are equal, the lowest ids stay
+    *id = lane;
+    return true;
   }
   // scores are at most 1: with biases below 3 no exchange is needed
   float big = 4.f;
@@ -448,17 +458,17 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs& a, const float (&l)
     for (int j = 0; j < NJ; ++j) key[j] = VEC || expert_of<VEC>(lane, j) < a.E ? 1u : 0u;
   }
   const bool by_score = a.bias != nullptr;
-  const auto key_of = [](float x) {   // order_key of a number; + 0 gives both zeros one key
-    const uint32_t b = __float_as_uint(x + 0.f);
+  const auto key_of = [](float x) {   // order_key of a number that is not -0
+    const uint32_t b = __float_as_uint(x);
     return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
   };
   // a NaN logit has not come this far: its magnitude was refused above
   if (by_score) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) key[j] = key[j] ? key_of(v[j]) : 0u;
+    for (int j = 0; j < NJ; ++j) key[j] = key[j] ? key_of(v[j]) : 0u;   // a score is not -0, nor is its sum with a bias
   } else {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) key[j] = key[j] ? key_of(l[j]) : 0u;
+    for (int j = 0; j < NJ; ++j) key[j] = key[j] ? key_of(l[j] + 0.f) : 0u;
   }
   const uint32_t theta = kth_bound<NJ>(key, a.k);
   uint32_t from = theta > 1u ? theta : 1u;
@@ -472,7 +482,22 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs& a, const float (&l)
   if (!by_score) return true;
   const float mine = key_float(mykey), below = __shfl_down(mine, 1);
   const bool sure = lane >= a.k || lane + 1 >= cnt || mine - below > 2.f * eps;
-  return __ballot(!sure) == 0;
+  if (__ballot(!sure) == 0) return true;
+  if (!SIGMOID) return false;
+  // the candidates hold the first k for certain
+  double exact = -INFINITY;
+  if (lane < cnt) {
+    const float x = load_scalar<DT>(a.logits, static_cast<size_t>(row + *id));
+    if (x != -INFINITY) exact = 1.0 / (1.0 + exp(-static_cast<double>(x))) + static_cast<double>(a.bias[*id]);
+  }
+  int rank = lane < cnt ? 0 : lane;
+  for (int o = 0; o < cnt; ++o) {
+    const double v = readlane_f(exact, o);
+    const int i = __builtin_amdgcn_readlane(*id, o);
+    if (lane < cnt) rank += v > exact || (v == exact && i < *id) ? 1 : 0;
+  }
+  *id = __builtin_amdgcn_ds_permute(4 * rank, *id);
+  return true;
 }
 
 // One token's logits on the wave.
@@ -513,69 +538,88 @@ __device__ __forceinline__ float row_max(const float (&l)[NJ], int lane) {
 
 // NJ: logits per lane (E <= 64 NJ).  WIDE: experts or groups are compared by
 // scores (a bias or groups).  VEC: E = 64 NJ and aligned rows.
-// Bound by the instructions of a token's wave (607 vector and 315 scalar ones
-// with groups): 32768 tokens of 512 bf16 logits in 8 groups take 46 us, six
-// times the time of reading them; one token of 256 takes 3.4 us, 2048 of 512
-// without groups 4.5 us, both little over a launch.
-// Several tokens per wave, sharing the bias and the evaluation of the weights,
-// were slower (four 62, eight 65, sixteen 87 us against one's 59): fewer waves
-// hide less of each other's exchanges.
+// Bound by the instructions of a token's wave: 32768 tokens of 512 bf16 logits
+// in 8 groups take 31 us, four times the time of reading them; one token of 256
+// takes 3.4 us, 2048 of 512 without groups 4.5 us, both little over a launch.
+// The double-precision weights of a block's four tokens are one wave's work
+// (33.4 against 35.0 us at that point).  Several tokens per wave throughout,
+// sharing the bias too, were slower (four 62, eight 65, sixteen 87 us against
+// one's 59): fewer waves hide less of each other's exchanges.
 template <int NJ, int DT, bool SIGMOID, bool WIDE, bool VEC>
 __global__ __launch_bounds__(kRtWaves* kWave) void k_route(RouteArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ WaveLds wave_lds[kRtWaves];
+  __shared__ int32_t chosen[kRtWaves][kWave / kRtWaves];
+  __shared__ float maxima[kRtWaves];
+  __shared__ double denoms[kRtWaves];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRtWaves + wave;
-  if (t >= a.T) return;   // no barrier below: waves are independent
-  WaveLds* lds = &wave_lds[wave];
-
-  float l[NJ];
-  load_row<NJ, DT, VEC>(a, t, lane, l);
-  const float mx = SIGMOID ? 0.f : row_max<NJ>(l, lane);
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kRtWaves + wave;
+  float mx = 0.f;
   Chosen c{0, 1.0};
-  if constexpr (WIDE) {
-    double* val = reinterpret_cast<double*>(smem) + static_cast<size_t>(wave) * a.E;
-    float bias[NJ] = {};
-    if (a.bias) {
-      if constexpr (VEC) {
+  if (t < a.T) {
+    WaveLds* lds = &wave_lds[wave];
+
+    float l[NJ];
+    load_row<NJ, DT, VEC>(a, t, lane, l);
+    if (!SIGMOID) mx = row_max<NJ>(l, lane);
+    if constexpr (WIDE) {
+      double* val = reinterpret_cast<double*>(smem) + static_cast<size_t>(wave) * a.E;
+      float bias[NJ] = {};
+      if (a.bias) {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int j = 0; j < NJ; j += 4) __builtin_memcpy(bias + j, a.bias + expert_of<VEC>(lane, j), 16);
-      } else {
+          for (int j = 0; j < NJ; j += 4) __builtin_memcpy(bias + j, a.bias + expert_of<VEC>(lane, j), 16);
+        } else {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) bias[j] = lane + j * kWave < a.E ? a.bias[lane + j * kWave] : 0.f;
+          for (int j = 0; j < NJ; ++j) bias[j] = lane + j * kWave < a.E ? a.bias[lane + j * kWave] : 0.f;
+        }
       }
-    }
-    int L = kWave;   // lanes per group
-    while (L * a.G > kWave) L >>= 1;
-    // a softmax that is not divided out again needs the exact denominator anyway
-    if ((!SIGMOID && !a.renorm) ||
-        !choose_fast<NJ, SIGMOID, VEC>(a, l, bias, mx, L, lane, lds, reinterpret_cast<float*>(val), &c.id))
-      c = choose_exact<NJ, SIGMOID, VEC>(a, l, bias, mx, L, lane, lds, val);
-  } else {
-    if (!SIGMOID && !a.renorm) {
-      float sum = 0.f;
+      int L = kWave;   // lanes per group
+      while (L * a.G > kWave) L >>= 1;
+      // a softmax that is not divided out again needs the exact denominator anyway
+      if ((!SIGMOID && !a.renorm) ||
+          !choose_fast<NJ, DT, SIGMOID, VEC>(a, t * a.stride, l, bias, mx, L, lane, lds, reinterpret_cast<float*>(val), &c.id))
+        c = choose_exact<NJ, SIGMOID, VEC>(a, l, bias, mx, L, lane, lds, val);
+    } else {
+      if (!SIGMOID && !a.renorm) {
+        float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) sum += l[j] == -INFINITY ? 0.f : expf(l[j] - mx);
-      c.denom = wave_sum_d(static_cast<double>(sum), lane);
-      if (c.denom == 0.0) c.denom = 1.0;
-    }
-    uint32_t key[NJ];
+        for (int j = 0; j < NJ; ++j) sum += l[j] == -INFINITY ? 0.f : expf(l[j] - mx);
+        c.denom = wave_sum_d(static_cast<double>(sum), lane);
+        if (c.denom == 0.0) c.denom = 1.0;
+      }
+      uint32_t key[NJ];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
-      key[j] = VEC || lane + j * kWave < a.E ? order_key(l[j] != l[j] ? -INFINITY : l[j]) : 0u;
-    const uint32_t theta = kth_bound<NJ>(key, a.k);
-    uint32_t mykey = 0;
-    if (rank32<NJ, VEC>(key, theta > 1u ? theta : 1u, lane, lds, &c.id, &mykey) > kCandMax) {
-      uint64_t key64[NJ];
+      for (int j = 0; j < NJ; ++j)
+        key[j] = VEC || lane + j * kWave < a.E ? order_key(l[j] != l[j] ? -INFINITY : l[j]) : 0u;
+      const uint32_t theta = kth_bound<NJ>(key, a.k);
+      uint32_t mykey = 0;
+      if (rank32<NJ, VEC>(key, theta > 1u ? theta : 1u, lane, lds, &c.id, &mykey) > kCandMax) {
+        uint64_t key64[NJ];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) key64[j] = key[j];
-      c.id = topk64<NJ, VEC>(key, key64, a.k, lane, lds);
+        for (int j = 0; j < NJ; ++j) key64[j] = key[j];
+        c.id = topk64<NJ, VEC>(key, key64, a.k, lane, lds);
+      }
     }
   }
 
-  // weights of the chosen, in double precision (one exp per lane)
-  const bool on = lane < a.k;
+  // weights of the chosen, in double precision (one exp per lane): up to 16 of
+  // each of the block's tokens by one wave, not the same in neighbouring blocks
+  int rank = lane;
+  if (a.k <= kWave / kRtWaves) {
+    if (lane < a.k) chosen[wave][lane] = c.id;
+    if (lane == 0) { maxima[wave] = mx; denoms[wave] = c.denom; }
+    __syncthreads();
+    if (wave != static_cast<int>((blockIdx.x >> 3) & 3)) return;
+    const int part = lane / (kWave / kRtWaves);
+    rank = lane % (kWave / kRtWaves);
+    t = static_cast<int64_t>(blockIdx.x) * kRtWaves + part;
+    c.id = chosen[part][rank];
+    mx = maxima[part];
+    c.denom = denoms[part];
+  }
+  const bool on = rank < a.k && t < a.T;
   const float lc = on ? load_scalar<DT>(a.logits, static_cast<size_t>(t * a.stride + c.id)) : -INFINITY;
   double sc = 0.0;
   if (on && lc != -INFINITY) {
@@ -597,8 +641,8 @@ __global__ __launch_bounds__(kRtWaves* kWave) void k_route(RouteArgs a) {
     sc /= c.denom;
   }
   if (on) {
-    a.ids[t * a.k + lane] = c.id;
-    a.w[t * a.k + lane] = static_cast<float>(sc * static_cast<double>(a.scale));
+    a.ids[t * a.k + rank] = c.id;
+    a.w[t * a.k + rank] = static_cast<float>(sc * static_cast<double>(a.scale));
   }
 }
 

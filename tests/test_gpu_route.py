@@ -132,6 +132,34 @@ def test_many_equal_keys_take_the_lowest_ids():
                 check(R.RouteShape(E, k, "softmax", 2, 1, 2), l, None, "f32")
 
 
+@pytest.mark.parametrize("E,k,G,tg,gt", [(40, 10, 1, 1, 1), (64, 16, 1, 1, 1), (512, 10, 1, 1, 1), (512, 17, 8, 3, 2), (512, 10, 8, 3, 2),
+                                         (1000, 8, 5, 2, 1)])
+@pytest.mark.parametrize("spread", [False, True])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_scores_closer_than_single_precision(E, k, G, tg, gt, spread, score):
+    """Thirty neighbours of a row, in one group or spread over all, have logits one fp32 step apart, in a shuffled order:
+    their scores differ by less than single precision tells apart.  Rows of padding between them."""
+    rng = np.random.default_rng(71 + E + k)
+    T, n, each = 11, 30, E // G
+    l, b = inputs(T, E, 72, "f32")
+    l = np.minimum(l, 1.5)
+    for t in range(T):
+        at = rng.permutation(E if spread else each)[:n] + (0 if spread else (t % G) * each)
+        l[t, at] = 2.0 + rng.permutation(n) * 2.0 ** -22
+    l[4] = NINF
+    check(R.RouteShape(E, k, score, G, tg, gt, True, 2.0), l, np.full(E, 0.125), "f32")
+    check(R.RouteShape(E, k, score, G, tg, gt, True, 2.0), l, np.zeros(E), "f32")
+
+
+def test_values_that_cancel_to_zero_are_no_empty_row():
+    l = np.full((5, 64), NINF)
+    l[0, [40, 7, 63]] = 0.0          # score 1/2, value 0
+    l[1, [9, 8]] = 0.0
+    l[3] = 0.0
+    check(R.RouteShape(64, 4, "sigmoid"), l, np.full(64, -0.5), "f32")
+    check(R.RouteShape(64, 4, "sigmoid", 4, 2, 2), l, np.full(64, -0.5), "f32")
+
+
 def test_zeros_of_either_sign_and_far_logits():
     l = np.array([[0.0, -0.0, 0.0, -0.0, -3e38, 3e38], [-500.0, -600.0, -700.0, -1e30, -501.0, -650.0],
                   [80.0, 90.0, -90.0, 100.0, -100.0, 20.0]])
