@@ -11,8 +11,9 @@
 // keys that matter lie further apart than the bound.  Where neighbours do not,
 // the few candidates alone are ranked again in double precision (sigmoid); where
 // groups do not, or a softmax's terms, all E scores are formed so.  That
-// is many times the usual work: rows that the mask leaves empty (2% of them)
-// and near ties together took 15 of 46 us that way.
+// is many times the usual work (rows that the mask leaves empty, 2% of them,
+// and near ties together took 15 of 46 us that way), so the bound is kept close:
+// a softmax's falls with its denominator, and with the largest value.
 //
 // Organisation.  A token's E logits are spread over one wave (a lane holds
 // every 64th expert, or groups of four neighbours where E fills the wave and
@@ -372,9 +373,10 @@ __device__ __forceinline__ Chosen choose_exact(const RouteArgs& a, const float (
 //   sigmoid   exp2 of a rounded product, a sum and a reciprocal of 1 ulp each
 //             leave |error of s| <= (0.45 + 0.5 + 1 + 2) u < 8 u
 //   softmax   a term exp(d) <= 1 is off by exp(d) (2 |d| + 2) u <= 3 u; the
-//             denominator, whose terms are off by 2 |d| + 2 u and whose mean
+//             denominator D, whose terms are off by 2 |d| + 2 u and whose mean
 //             |d| is at most the entropy, 6.94, by (14 + 2 + 16 + 6) u of
-//             itself; |error of s| < 64 u
+//             itself, the quotient by 3 u of itself; |error of s| <= (3 + 41) u
+//             / D < 64 u / D
 // and a bias adds a rounding of u |v|; `eps` is that bound.  A group's score is
 // off by 2 eps + u |sum| at most.  Groups: one that stays has fewer than
 // top_groups others that may lie above it, one that goes at least that many
@@ -388,7 +390,7 @@ template <int NJ, int DT, bool SIGMOID, bool VEC>
 __device__ __forceinline__ bool choose_fast(const RouteArgs& a, int64_t row, const float (&l)[NJ], const float (&bias)[NJ],
                                             float mx, int L, int lane, WaveLds* lds, float* val, int* id) {
   constexpr float kLog2e = 1.4426950408889634f, u = 5.9604644775390625e-8f;
-  float v[NJ];
+  float v[NJ], eps = 8.f * u;
   if (SIGMOID) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) v[j] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-l[j] * kLog2e));
@@ -405,6 +407,7 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs& a, int64_t row, con
     const float r = __builtin_amdgcn_rcpf(sum);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) v[j] *= r;
+    eps = 64.f * u * r;
   }
   // the largest magnitude as whole numbers: infinities and NaN come out on top
   uint32_t top = 0;
@@ -422,13 +425,16 @@ __device__ __forceinline__ bool choose_fast(const RouteArgs& a, int64_t row, con
     *id = lane;
     return true;
   }
-  // scores are at most 1: with biases below 3 no exchange is needed
-  float big = 4.f;
-  if (__ballot(top >= 0x40800000u)) {
-    big = wave_max_f(__uint_as_float(top), lane);   // passes NaN over, which is not below itself
-    if (__ballot(!(__uint_as_float(top) < 1e30f))) return false;
+  // most values lie below 1 or 4; others take an exchange
+  float big = 1.f;
+  if (__ballot(top >= 0x3f800000u)) {
+    big = 4.f;
+    if (__ballot(top >= 0x40800000u)) {
+      big = wave_max_f(__uint_as_float(top), lane);   // passes NaN over, which is not below itself
+      if (__ballot(!(__uint_as_float(top) < 1e30f))) return false;
+    }
   }
-  const float eps = (SIGMOID ? 8.f : 64.f) * u + 2.f * u * big;
+  eps += 2.f * u * big;
   uint32_t key[NJ];
   if (a.G > 1) {
     if (VEC) {
@@ -539,8 +545,9 @@ __device__ __forceinline__ float row_max(const float (&l)[NJ], int lane) {
 // NJ: logits per lane (E <= 64 NJ).  WIDE: experts or groups are compared by
 // scores (a bias or groups).  VEC: E = 64 NJ and aligned rows.
 // Bound by the instructions of a token's wave: 32768 tokens of 512 bf16 logits
-// in 8 groups take 31 us, four times the time of reading them; one token of 256
-// takes 3.4 us, 2048 of 512 without groups 4.5 us, both little over a launch.
+// in 8 groups take 29.5 us, four times the time of reading them; one token of
+// 256 takes 3.4 us, 2048 of 512 without groups 4.5 us, both little over a
+// launch.
 // The double-precision weights of a block's four tokens are one wave's work
 // (33.4 against 35.0 us at that point).  Several tokens per wave throughout,
 // sharing the bias too, were slower (four 62, eight 65, sixteen 87 us against
@@ -577,11 +584,16 @@ __global__ __launch_bounds__(kRtWaves* kWave) void k_route(RouteArgs a) {
       }
       int L = kWave;   // lanes per group
       while (L * a.G > kWave) L >>= 1;
-      // a softmax that is not divided out again needs the exact denominator anyway
-      if ((!SIGMOID && !a.renorm) ||
-          !choose_fast<NJ, DT, SIGMOID, VEC>(a, t * a.stride, l, bias, mx, L, lane, lds, reinterpret_cast<float*>(val), &c.id))
+      if (!choose_fast<NJ, DT, SIGMOID, VEC>(a, t * a.stride, l, bias, mx, L, lane, lds, reinterpret_cast<float*>(val), &c.id)) {
         c = choose_exact<NJ, SIGMOID, VEC>(a, l, bias, mx, L, lane, lds, val);
-    } else {
+      } else if (!SIGMOID && !a.renorm) {
+        double sum = 0.0;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) sum += l[j] == -INFINITY ? 0.0 : exp(static_cast<double>(l[j]) - static_cast<double>(mx));
+        c.denom = wave_sum_d(sum, lane);
+        if (c.denom == 0.0) c.denom = 1.0;
+      }
+  } else {
       if (!SIGMOID && !a.renorm) {
         float sum = 0.f;
 #pragma unroll
@@ -594,8 +606,17 @@ __global__ __launch_bounds__(kRtWaves* kWave) void k_route(RouteArgs a) {
       for (int j = 0; j < NJ; ++j)
         key[j] = VEC || lane + j * kWave < a.E ? order_key(l[j] != l[j] ? -INFINITY : l[j]) : 0u;
       const uint32_t theta = kth_bound<NJ>(key, a.k);
+      bool empty = false;   // no number in the row: the lowest ids stay
+      if (theta < 0x00800000u) {
+        uint64_t numbers = 0;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) numbers |= __ballot(key[j] >= 0x00800000u);
+        empty = numbers == 0;
+      }
       uint32_t mykey = 0;
-      if (rank32<NJ, VEC>(key, theta > 1u ? theta : 1u, lane, lds, &c.id, &mykey) > kCandMax) {
+      if (empty) {
+        c.id = lane;
+      } else if (rank32<NJ, VEC>(key, theta > 1u ? theta : 1u, lane, lds, &c.id, &mykey) > kCandMax) {
         uint64_t key64[NJ];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) key64[j] = key[j];

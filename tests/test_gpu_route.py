@@ -151,6 +151,19 @@ def test_scores_closer_than_single_precision(E, k, G, tg, gt, spread, score):
     check(R.RouteShape(E, k, score, G, tg, gt, True, 2.0), l, np.zeros(E), "f32")
 
 
+@pytest.mark.parametrize("size", [1e-3, 0.5, 3.0, 100.0, 1e6])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_biases_of_any_size(size, score, renorm):
+    """The larger the bias, the more scores single precision loses in the sum; equal biases leave the order to the scores."""
+    l, b = inputs(9, 256, 81, "f32", masked=True)
+    b = np.float32(size * (1 + (np.arange(256) % 3) * 0.25)).astype(np.float64) * (1 if size < 50 else -1)
+    if size == 1e6:
+        l = np.where(np.isneginf(l), l, np.round(l * 4096) / 4096)   # keeps scores apart beyond a double's sum with 1e6
+    check(R.RouteShape(256, 9, score, 1, 1, 1, renorm, 1.5), l, b, "f32")
+    check(R.RouteShape(256, 9, score, 8, 3, 2, renorm, 1.5), l, b, "f32")
+
+
 def test_values_that_cancel_to_zero_are_no_empty_row():
     l = np.full((5, 64), NINF)
     l[0, [40, 7, 63]] = 0.0          # score 1/2, value 0
