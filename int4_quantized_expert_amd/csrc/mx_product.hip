@@ -34,6 +34,11 @@ constexpr int kDirectPairs = 32;
 // Pairs up to which a token's weighted sum is one block's work: down rows (2048
 // outputs, k = 512) 16.4 us against 17.2 for 80 pairs, 22.7 against 19.2 for 120.
 constexpr int kSumPairs = 80;
+// Bytes of the pairs' codes of W from which either is left to the tiles all the
+// same, whose loads run further ahead: 32 pairs of 4096 x 1024 18.3 us against
+// 20.6, 64 summed ones of 2048 x 2048 30.2 against 33.9; below, 64 summed ones
+// of 2048 x 512 13.3 us against 15.8, 8 pairs of 1024 x 8192 13.1 against 21.9.
+constexpr int64_t kFewBytes = int64_t(1) << 26;
 
 enum Mode { kDense, kDirect, kTiles, kSum };
 
@@ -187,7 +192,8 @@ __device__ __forceinline__ void store_out(void* out, int64_t i, float y, int bf1
 // Few rows of A: a block forms 16 outputs of up to 16 MT rows (kSum: of one
 // token), its waves take the chunks of k in turn and their sums are joined in
 // LDS.  Bound by the reads of W and the chain of dependent loads before them
-// (ids, slots); A is read, and quantised, by every block, while W is on its way.
+// (ids, slots); every block reads A while W is on its way, and quantises it where
+// that is cheaper than a launch before (quantise_in_place).
 // One token by 4096 x 2048: 4.4 us; through ten experts' gate and up rows (512
 // outputs, k = 2048): 7.4 us, 1.5 TB/s.
 //   kDense   rows 16 MT y .. of A
@@ -198,7 +204,7 @@ __device__ __forceinline__ void store_out(void* out, int64_t i, float y, int bf1
 template <int SRC, int ACT, int MODE, int MT, int NW>
 __global__ __launch_bounds__(NW* kWave) void k_mx_narrow(MxArgs a) {
   constexpr int NM = ACT == MX_ACT_SWIGLU ? 2 : 1;
-  static_assert(MT == 1 || (MODE == kDense && SRC == kMxF4), "more row tiles are for the dense product of codes");
+  static_assert(MT == 1 || (MODE == kDense && (MT == 2 || SRC == kMxF4)), "more row tiles are for dense products, more than two for codes");
   __shared__ __align__(16) float red[NM][NW][16][20];   // 20: four-float stores, fewer bank conflicts
   __shared__ int32_t list[kDirectPairs];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -294,7 +300,8 @@ __global__ __launch_bounds__(NW* kWave) void k_mx_narrow(MxArgs a) {
       } else {
         const int c0 = chunk * kChunk + q * 64;
         const auto* av = static_cast<const typename Stored<SRC>::T*>(a.a) + row0 * a.K;
-        load_values<SRC>(av, row[0] * a.K + c0, a.K - c0, r < here, A[0]);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) load_values<SRC>(av, row[t] * a.K + c0, a.K - c0, t * 16 + r < here, A[t]);
       }
       if constexpr (MODE != kDense) {
         usable = o >= 0;   // an unusable expert's product is zero, whatever A holds
@@ -614,7 +621,6 @@ __global__ __launch_bounds__(KS* WM* WN* kWave) void k_mx_tile(MxArgs a) {
   }
 
   // a lane holds four consecutive outputs of one row
-  const bool whole = (a.N & 3) == 0 && (reinterpret_cast<uintptr_t>(a.out) & (a.out_bf16 ? 7 : 15)) == 0;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int m = (wm * TM + i) * 16 + r;
@@ -626,14 +632,15 @@ __global__ __launch_bounds__(KS* WM* WN* kWave) void k_mx_tile(MxArgs a) {
       float y[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) y[x] = NM == 2 ? silu(acc[i][j][x]) * acc[i][j + NM - 1][x] : acc[i][j][x];
-      if (whole && n + 4 <= a.N) {
+      if (n + 4 <= a.N) {   // aligned to an element only if N is not a multiple of four (element
+                            // stores: 35.4 instead of 25.7 us for 4082 x 2683 x 1020)
         if (a.out_bf16) {
-          uint2 w;
-          w.x = to_bf16(y[0]) | (static_cast<uint32_t>(to_bf16(y[1])) << 16);
-          w.y = to_bf16(y[2]) | (static_cast<uint32_t>(to_bf16(y[3])) << 16);
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to + n) = w;
+          uint32_t w[2];
+          w[0] = to_bf16(y[0]) | (static_cast<uint32_t>(to_bf16(y[1])) << 16);
+          w[1] = to_bf16(y[2]) | (static_cast<uint32_t>(to_bf16(y[3])) << 16);
+          __builtin_memcpy(static_cast<uint16_t*>(a.out) + to + n, w, 8);
         } else {
-          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to + n) = float4{y[0], y[1], y[2], y[3]};
+          __builtin_memcpy(static_cast<float*>(a.out) + to + n, y, 16);
         }
       } else {
 #pragma unroll
@@ -954,10 +961,11 @@ void narrow_act(const MxArgs& a, int act, uint32_t blocks, hipStream_t s) {
 
 template <int MODE, int MT, int NW>
 void narrow_src(const MxArgs& a, int src, int act, uint32_t blocks, hipStream_t s) {
-  // more row tiles than one take codes: their values do not fit the registers
-  if (MT > 1 || src == kMxF4) narrow_act<kMxF4, MODE, MT, NW>(a, act, blocks, s);
-  else if (src == kF32) narrow_act<kF32, MODE, 1, NW>(a, act, blocks, s);
-  else narrow_act<kBF16, MODE, 1, NW>(a, act, blocks, s);
+  // more row tiles than two take codes: their values do not fit the registers
+  constexpr int V = MT <= 2 ? MT : 1;
+  if (MT > 2 || src == kMxF4) narrow_act<kMxF4, MODE, MT, NW>(a, act, blocks, s);
+  else if (src == kF32) narrow_act<kF32, MODE, V, NW>(a, act, blocks, s);
+  else narrow_act<kBF16, MODE, V, NW>(a, act, blocks, s);
 }
 
 template <int MODE, int MT = 1>
@@ -1006,6 +1014,19 @@ void prep_src(const PrepArgs& p, uint32_t blocks, hipStream_t s) {
   else launch_kernel(k_mx_prep<SRC, 0>, grid, block, 0, s, p);
 }
 
+// Whether blocks of the kernel of few rows quantise A themselves, which saves a
+// launch: `rows` of them (a multiple of 16, others cost as much) in each of
+// `blocks`.  A block's own part must not hold it up (16 rows of 1024 x 8192 in
+// bf16 take 12.2 us against 10.4 with A quantised before, in fp32 20.2) and all
+// of them together not the GPU (16 rows of 16384 x 2048 12.8 and 20.7 against
+// 10.7; 4096 x 2048 7.0 and 7.1 against 9.3).  By expert the part may be twice
+// as large, while ids and slots are looked up (one token's sum over 8 experts,
+// 2048 outputs, k = 512 in fp32: 9.2 us against 11.0).
+bool quantise_in_place(const mx_product_desc& d, int64_t rows, int64_t blocks, int64_t most) {
+  const int64_t bytes = rows * d.k * (d.a_dtype == MOE_F32 ? 4 : 2);
+  return d.a_dtype != MX_FP4 && bytes <= most && bytes * blocks <= (3 << 24);
+}
+
 MxArgs common_args(const mx_product_desc& d, const void* a, const void* as, void* out, void* ws) {
   MxArgs g{};
   g.a = a;
@@ -1052,19 +1073,18 @@ int mx_linear_forward(const mx_product_desc* d, int32_t M, const void* a, const 
   g.wc = static_cast<const uint8_t*>(w_codes);
   g.wsc = static_cast<const uint8_t*>(w_scales);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (M <= 16) {
-    narrow<kDense>(g, d->a_dtype, d->act, 1, s);
-    return launched();
-  }
   g.arows = M;
-  if (d->a_dtype != MX_FP4) {
+  const bool few = M <= 32 && quantise_in_place(*d, M <= 16 ? 16 : 32, (d->n + 15) / 16, 1 << 17);
+  if (!few && d->a_dtype != MX_FP4) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     launch_mx_quantize(d->a_dtype, M, d->k, a, d->k, ws + L.codes, ws + L.scales, s);
     g.a = ws + L.codes;
     g.as = ws + L.scales;
   }
   if (M <= 64) {
-    if (M <= 32) narrow<kDense, 2>(g, MX_FP4, d->act, 1, s);
+    const int src = few ? d->a_dtype : MX_FP4;
+    if (M <= 16) narrow<kDense>(g, src, d->act, 1, s);
+    else if (M <= 32) narrow<kDense, 2>(g, src, d->act, 1, s);
     else narrow<kDense, 4>(g, MX_FP4, d->act, 1, s);
     return launched();
   }
@@ -1123,16 +1143,27 @@ int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const
   g.pool_bytes = d->pool_bytes;
   // a gated product is not linear in its sums, so the weighted sum of a token
   // in one block is for the plain one
-  if (topk_w && P <= kSumPairs && d->act == MX_ACT_NONE) {
-    narrow<kSum>(g, d->a_dtype, d->act, T, s);
+  const int nblk = (d->n + 15) / 16;
+  const bool little = P * mx_codes_bytes(wrows, d->k) < kFewBytes;
+  const bool sum = topk_w && P <= kSumPairs && d->act == MX_ACT_NONE && little, direct = !sum && P <= kDirectPairs && little;
+  int src = d->a_dtype;
+  if ((sum || direct) && src != MX_FP4 &&
+      !quantise_in_place(*d, sum ? 16 * d->top_k : 16, static_cast<int64_t>(nblk) * (sum ? T : P), 1 << 18)) {
+    launch_mx_quantize(src, rows, d->k, a, d->k, ws + L.codes, ws + L.scales, s);
+    g.a = ws + L.codes;
+    g.as = ws + L.scales;
+    src = MX_FP4;
+  }
+  if (sum) {
+    narrow<kSum>(g, src, d->act, T, s);
     return launched();
   }
   if (topk_w) {
     g.out = ws + L.rows;
     g.out_bf16 = 0;
   }
-  if (P <= kDirectPairs) {
-    narrow<kDirect>(g, d->a_dtype, d->act, P, s);
+  if (direct) {
+    narrow<kDirect>(g, src, d->act, P, s);
   } else {
     g.arows = static_cast<int>(rows);
     // rows per tile by the pairs that an expert has on average (gate and up

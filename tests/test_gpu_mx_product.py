@@ -69,6 +69,22 @@ def test_linear_row_counts(Mr):
     linear(Mr, 80, 300, a="bf16", out="f32", act="swiglu", seed=6)
 
 
+@pytest.mark.parametrize("Mr,N,K", [(16, 40, 2000), (16, 40, 4200), (3, 33, 9000), (17, 50, 500), (32, 33, 1000), (32, 33, 2100),
+                                    (25, 20, 4500), (16, 16500, 700), (32, 6600, 1000)])
+@pytest.mark.parametrize("a", ["f32", "bf16", "mx"])
+def test_linear_few_rows_quantised_in_the_product_or_before(Mr, N, K, a):
+    linear(Mr, N, K, a=a)
+    linear(Mr, N // 3, K, a=a, out="bf16", act="swiglu")
+
+
+@pytest.mark.parametrize("N", [129, 130, 131, 132, 515])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_linear_rows_of_any_alignment(N, out):
+    """Four outputs a store wherever a row starts, and the columns past the last four."""
+    linear(150, N, 300, out=out)
+    linear(150, N, 300, out=out, act="swiglu")
+
+
 def test_linear_long_and_wide():
     linear(3, 40, 20000, seed=7)
     linear(70, 24, 9000, seed=8, act="swiglu")
@@ -208,6 +224,18 @@ def test_experts_types(act, a):
         for out in ("f32", "bf16"):
             run_experts(x, T, 5, a, out, False, False, seed=4)
             run_experts(x, T, 5, a, out, True, True, seed=5)
+
+
+@pytest.mark.parametrize("a", ["f32", "bf16", "mx"])
+@pytest.mark.parametrize("T,k,N,K,act,combine", [
+    (1, 8, 40, 500, "none", True), (1, 8, 40, 1100, "none", True), (9, 8, 40, 600, "none", True),      # sums in one block
+    (2, 8, 40, 2000, "none", False), (2, 8, 40, 8300, "none", False), (8, 4, 1500, 300, "swiglu", False),
+    (16, 2, 4096, 1024, "none", False), (16, 2, 4096, 1024, "none", True)])                              # much of W: tiles
+def test_experts_few_pairs_on_every_path(T, k, N, K, act, combine, a):
+    x = Experts(np.random.default_rng(17), 9, N, K, act)
+    run_experts(x, T, k, a=a, combine=combine)
+    if combine:
+        run_experts(x, T, k, a=a, combine=True, pair_rows=True)
 
 
 @pytest.mark.parametrize("T", [4, 16, 60, 300])
