@@ -27,18 +27,20 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr int kMxF4 = 2;                 // a_dtype code MX_FP4
 constexpr int kChunk = kMxPad;           // k values per step
-// Pairs up to which the blocks find their expert's pairs by themselves instead
-// of a grouping launch: gate and up rows of top-10 experts (512 outputs, k =
-// 2048) take 10.2 us against 12.3 for 20 pairs, 15.1 against 13.0 for 40.
-constexpr int kDirectPairs = 32;
-// Pairs up to which a token's weighted sum is one block's work: down rows (2048
-// outputs, k = 512) 16.4 us against 17.2 for 80 pairs, 22.7 against 19.2 for 120.
-constexpr int kSumPairs = 80;
-// Bytes of the pairs' codes of W from which either is left to the tiles all the
-// same, whose loads run further ahead: 32 pairs of 4096 x 1024 18.3 us against
-// 20.6, 64 summed ones of 2048 x 2048 30.2 against 33.9; below, 64 summed ones
-// of 2048 x 512 13.3 us against 15.8, 8 pairs of 1024 x 8192 13.1 against 21.9.
-constexpr int64_t kFewBytes = int64_t(1) << 26;
+// Pairs up to which the blocks find their expert's pairs by themselves (one id a
+// lane) instead of a grouping launch, and up to which a token's weighted sum is
+// one block's work, unless the pairs' codes of W are so many bytes that the
+// tiles, whose loads run further ahead, make up for the launches.  Measured
+// (bf16, here against tiles, us):
+//   gate and up rows, 512 outputs, k = 2048: 20 pairs 10.3, 13.0; 40 pairs 14.2,
+//     15.8; 50 pairs (52 MB) 16.6, 16.4; 60 pairs 18.6, 17.3
+//   512 outputs, k = 512: 48 pairs 7.2, 10.0
+//   sums of 2048 outputs, k = 512: 80 pairs 14.5, 18.5; 120 pairs (63 MB) 17.6,
+//     22.1; of 2048 x 2048: 64 pairs (134 MB) 33.9, 30.2
+//   sums of 512 outputs, k = 512: 256 pairs (34 MB) 13.4, 14.9; 384 pairs 15.4,
+//     16.2, through 16 experts 14.8, 14.2; of 128 outputs: 1024 pairs 12.7, 13.5
+constexpr int kDirectPairs = 64, kSumPairs = 1024;
+constexpr int64_t kDirectBytes = 3 << 24, kSumBytes = 1 << 26;
 
 enum Mode { kDense, kDirect, kTiles, kSum };
 
@@ -1144,8 +1146,9 @@ int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const
   // a gated product is not linear in its sums, so the weighted sum of a token
   // in one block is for the plain one
   const int nblk = (d->n + 15) / 16;
-  const bool little = P * mx_codes_bytes(wrows, d->k) < kFewBytes;
-  const bool sum = topk_w && P <= kSumPairs && d->act == MX_ACT_NONE && little, direct = !sum && P <= kDirectPairs && little;
+  const int64_t w_bytes = P * mx_codes_bytes(wrows, d->k);
+  const bool sum = topk_w && d->act == MX_ACT_NONE && P <= kSumPairs && w_bytes < kSumBytes;
+  const bool direct = !sum && P <= kDirectPairs && w_bytes < kDirectBytes;
   int src = d->a_dtype;
   if ((sum || direct) && src != MX_FP4 &&
       !quantise_in_place(*d, sum ? 16 * d->top_k : 16, static_cast<int64_t>(nblk) * (sum ? T : P), 1 << 18)) {

@@ -230,6 +230,8 @@ def test_experts_types(act, a):
 @pytest.mark.parametrize("T,k,N,K,act,combine", [
     (1, 8, 40, 500, "none", True), (1, 8, 40, 1100, "none", True), (9, 8, 40, 600, "none", True),      # sums in one block
     (2, 8, 40, 2000, "none", False), (2, 8, 40, 8300, "none", False), (8, 4, 1500, 300, "swiglu", False),
+    (16, 4, 50, 300, "none", False), (16, 4, 50, 300, "swiglu", True), (13, 5, 50, 300, "none", False), # 64 and 65 pairs
+    (128, 8, 40, 300, "none", True), (205, 5, 40, 300, "none", True),                                    # 1024 and 1025
     (16, 2, 4096, 1024, "none", False), (16, 2, 4096, 1024, "none", True)])                              # much of W: tiles
 def test_experts_few_pairs_on_every_path(T, k, N, K, act, combine, a):
     x = Experts(np.random.default_rng(17), 9, N, K, act)
@@ -468,7 +470,12 @@ def test_launch_timer_counts_the_kernels():
     out, ws = torch.zeros(60, 40, device=DEV), workspace(d, 60)
     timer = M.LaunchTimer(8)
     timer.arm()
-    M.mx_experts(d, 60, a, None, it, wt, x.slots, x.pool, out, ws)      # grouping, product, weighted sum
+    M.mx_experts(d, 60, a, None, it, wt, x.slots, x.pool, out, ws)      # the weighted sums in one kernel
+    torch.cuda.synchronize()
+    assert timer.n_recorded == 2 and all(0 < t < 1e5 for t in timer.kernel_us())
+    x = Experts(np.random.default_rng(16), 8, 40, 300, "swiglu")
+    timer.arm()
+    M.mx_experts(x.desc(3), 60, a, None, it, wt, x.slots, x.pool, out, ws)   # grouping, gated product, weighted sum
     torch.cuda.synchronize()
     assert timer.n_recorded == 6 and all(0 < t < 1e5 for t in timer.kernel_us())
     M.mx_experts(d, 60, a, None, it, wt, x.slots, x.pool, out, ws)      # not armed again
