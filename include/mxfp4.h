@@ -116,7 +116,8 @@ size_t mx_workspace_bytes(const mx_product_desc* d, int32_t T_max);
  *   w_scales
  *   out          [M, n], out_dtype, aligned to its element
  *   workspace    ws_bytes >= mx_workspace_bytes(d, M), 256-byte aligned
- * Errors: MOE_EINVAL, MOE_ENOMEM (workspace), MOE_EHIP.
+ * Errors: MOE_EINVAL (also for 2^37 values of A to quantise, which a launch
+ * does not hold), MOE_ENOMEM (workspace), MOE_EHIP.
  */
 int mx_linear_forward(const mx_product_desc* d, int32_t M, const void* a, const void* a_scales, const void* w_codes,
                       const void* w_scales, void* out, void* workspace, size_t ws_bytes, void* stream);
@@ -136,8 +137,9 @@ int mx_linear_forward(const mx_product_desc* d, int32_t M, const void* a, const 
  * nothing, whatever its row of A and its weight hold (its row of the output is
  * zero), and raises MOE_ERANGE in moe_status_check(workspace).  An expert may
  * occur twice in a token's ids.  MOE_EINVAL also where a launch would need 2^32
- * threads or more (T n of 2^32 columns, 2^35 values of A to quantise).  Errors
- * as above.
+ * threads or more (T n of 2^32 columns, 2^35 values of A to quantise, the tiles
+ * of the grouped pairs: 2 n threads for each expert that has pairs and for
+ * every 128 pairs, 4 n with MX_ACT_SWIGLU).  Errors as above.
  */
 int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const void* a_scales,
                        const int32_t* topk_ids, const float* topk_w, const int64_t* slot_table, const void* pool_base,

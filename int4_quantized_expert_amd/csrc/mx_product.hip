@@ -868,21 +868,48 @@ int check_product(const mx_product_desc* d, bool experts) {
 // The tiles' offsets into A have 32 bits.
 bool far_rows(int64_t rows, int k) { return rows * (mx_padded(k) / 2) >= (int64_t(1) << 32) - 65536; }
 
+constexpr int64_t kMostThreads = int64_t(1) << 32;   // a launch holds fewer
+
+// How P pairs are grouped: rows per tile, the most tiles, and the threads of
+// their launch.
+//   By the pairs that an expert has on average (gate and up rows, 512 outputs,
+// k = 2048; tiles of 32, 64 and 128 rows): 16 pairs 63, 65, 76 us; 32 pairs 77,
+// 72, 83; 64 pairs 102, 90, 92; 96 pairs 70, 61, 56; 256 pairs 76, 63, 58.
+// Where the launch would hold too many threads the tiles are higher.  An A
+// beyond 4 GiB takes the kernel of few rows.
+struct Grouping {
+  int bm;
+  int64_t tiles, threads;
+};
+
+Grouping grouping(const mx_product_desc& d, int64_t P, int64_t rows) {
+  const int64_t some = P < d.n_experts + 1 ? P : d.n_experts + 1;   // experts with pairs, and the pairs without one
+  if (far_rows(rows, d.k)) {
+    const int64_t tiles = some + P / 16;
+    return {16, tiles, tiles * ((d.n + 15) / 16) * (8 * kWave)};
+  }
+  const int64_t each = P / d.n_experts;
+  const int cols = d.act == MX_ACT_SWIGLU ? 64 : 128;   // outputs of a tile; its block is four waves
+  for (int bm = each >= 96 ? 128 : each >= 24 ? 64 : 32;; bm *= 2) {
+    const int64_t tiles = some + P / bm, threads = (tiles * ((d.n + cols - 1) / cols) + 7) / 8 * 8 * (4 * kWave);
+    if (threads < kMostThreads || bm == 128) return {bm, tiles, threads};
+  }
+}
+
 int check_rows(const mx_product_desc& d, int32_t T, bool experts) {
   if (T < 0 || T > (experts ? 65536 : (1 << 20))) return bad("%lld rows are negative or too many", T);
-  if (static_cast<int64_t>(T) * (experts ? d.top_k : 1) * ((d.n + 15) / 16) >= (int64_t(1) << 31))
-    return bad("%lld rows of %lld columns are too many for one launch", static_cast<long long>(T) * (experts ? d.top_k : 1), d.n);
-  if (!experts) return MOE_OK;
-  const int64_t P = static_cast<int64_t>(T) * d.top_k;
-  if (P >= (1 << 22)) return bad("T * top_k = %lld must be below 2^22", P);
-  // a launch holds fewer than 2^32 threads: those of the sums over a token's
-  // experts, of the quantisation and of the few-row kernel over grouped rows
-  const int64_t rows = d.pair_rows ? P : T, row_codes = mx_padded(d.k) / 2, most = int64_t(1) << 32;
-  if (T * ((d.n + 255) / 256 * int64_t(256)) >= most) return bad("%lld rows of %lld columns are too many for one launch", T, d.n);
-  if (d.a_dtype != MX_FP4 && rows * row_codes / 4 >= most - 2048)
+  const int64_t P = static_cast<int64_t>(T) * (experts ? d.top_k : 1), rows = experts && !d.pair_rows ? T : P;
+  if (P * ((d.n + 15) / 16) >= (int64_t(1) << 31)) return bad("%lld rows of %lld columns are too many for one launch", P, d.n);
+  // every launch that may follow: the quantisation (of a launch before a dense
+  // product four pieces a thread, with the grouping one), the sums over a
+  // token's experts, the products of grouped rows
+  const int64_t pieces = rows * (mx_padded(d.k) / 8);
+  if (d.a_dtype != MX_FP4 && pieces / (experts ? 1 : 4) >= kMostThreads - 2048)
     return bad("%lld rows of %lld values are too many to quantise in one launch", rows, d.k);
-  if (far_rows(rows, d.k) && (P / 16 + d.n_experts + 1) * ((d.n + 15) / 16) * 512 >= most)
-    return bad("%lld pairs of %lld columns are too many for one launch", P, d.n);
+  if (!experts) return MOE_OK;
+  if (P >= (1 << 22)) return bad("T * top_k = %lld must be below 2^22", P);
+  if (T * ((d.n + 255) / 256 * int64_t(256)) >= kMostThreads) return bad("%lld rows of %lld columns are too many for one launch", T, d.n);
+  if (grouping(d, P, rows).threads >= kMostThreads) return bad("%lld pairs of %lld columns are too many for one launch", P, d.n);
   return MOE_OK;
 }
 
@@ -1169,16 +1196,11 @@ int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const
     narrow<kDirect>(g, src, d->act, P, s);
   } else {
     g.arows = static_cast<int>(rows);
-    // rows per tile by the pairs that an expert has on average (gate and up
-    // rows, 512 outputs, k = 2048; tiles of 32, 64 and 128 rows): 16 pairs 63,
-    // 65, 76 us; 32 pairs 77, 72, 83; 64 pairs 102, 90, 92; 96 pairs 70, 61,
-    // 56; 256 pairs 76, 63, 58.  An A beyond 4 GiB takes the kernel of few rows
-    const int each = P / d->n_experts;
-    const int bm = far_rows(rows, d->k) ? 16 : each >= 96 ? 128 : each >= 24 ? 64 : 32;
+    const Grouping by = grouping(*d, P, rows);
     PrepArgs p{};
     p.g = g;
     p.P = P;
-    p.rows = bm;
+    p.rows = by.bm;
     p.place = reinterpret_cast<int32_t*>(ws + L.place);
     p.plist = reinterpret_cast<int32_t*>(ws + L.plist);
     p.tiles = reinterpret_cast<MxTile*>(ws + L.tiles);
@@ -1201,11 +1223,10 @@ int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const
     g.plist = p.plist;
     g.tiles = p.tiles;
     g.ntiles = p.ntiles;
-    const int64_t most = (P < d->n_experts + 1 ? P : d->n_experts + 1) + static_cast<int64_t>(P) / bm;
-    if (bm == 16) narrow<kTiles>(g, MX_FP4, d->act, static_cast<int>(most), s);
-    else if (bm == 32) rc = tile<1, 4, 2, 2, 3, 1, true>(g, d->act, most, s);
-    else if (bm == 64) rc = tile<1, 4, 4, 2, 3, 1, true>(g, d->act, most, s);
-    else rc = tile<2, 2, 4, 4, 2, 1, true>(g, d->act, most, s);
+    if (by.bm == 16) narrow<kTiles>(g, MX_FP4, d->act, static_cast<int>(by.tiles), s);
+    else if (by.bm == 32) rc = tile<1, 4, 2, 2, 3, 1, true>(g, d->act, by.tiles, s);
+    else if (by.bm == 64) rc = tile<1, 4, 4, 2, 3, 1, true>(g, d->act, by.tiles, s);
+    else rc = tile<2, 2, 4, 4, 2, 1, true>(g, d->act, by.tiles, s);
     if (rc != MOE_OK) return api_fail(MOE_EHIP, "the product kernel's LDS size was refused");
   }
   if (topk_w) {
