@@ -361,7 +361,11 @@ def status_check(ws, stream=None) -> None:
 #
 # Where an argument is a torch tensor, its type, size and layout are checked
 # here against what the entry point will read or write, and the call runs on
-# the tensors' device; plain addresses are passed on as they are.
+# the tensors' device; plain addresses are passed on as they are.  Tensors only:
+# workspaces, whose size the entry points check, and the values that mx_quantize
+# reads and mx_dequantize writes, whose sizes say what to do.  Pools, workspaces,
+# activations and router weights may be of any type that holds the bytes (but
+# not of another floating-point type than the descriptor's).
 
 MX_FP4 = 2
 MX_ACT_NONE, MX_ACT_SWIGLU = 0, 1
@@ -411,6 +415,27 @@ def _misfit(name: str, t, dtype, need: int):
 def _check_tensor(name: str, t, dtype, need: int) -> None:
     if not _fits(t, dtype, need):
         _misfit(name, t, dtype, need)
+
+
+def _check_bytes(name: str, t, need: int, dtype=None) -> None:
+    """That t, unless it is None or an address, is `need` adjacent bytes; dtype: the floating-point type that they hold."""
+    if t is None or type(t) is int:
+        return
+    if not t.is_contiguous():
+        _bad(f"{name} is not contiguous")
+    if t.numel() * t.element_size() < need:
+        _bad(f"{name} has {_nbytes(t)} bytes, {need} needed")
+    if dtype is not None and t.dtype is not dtype and t.dtype.is_floating_point:
+        _bad(f"{name} is {t.dtype}, {dtype} expected")
+
+
+def _ws_bytes(ws) -> int:
+    """Bytes of a workspace (the entry point compares them with its need)."""
+    if ws is None or type(ws) is int:
+        _bad("the workspace has to be a tensor")
+    if not ws.is_contiguous():
+        _bad("the workspace is not contiguous")
+    return ws.numel() * ws.element_size()
 
 
 def _call_on(tensors, stream, fn, *args) -> None:
@@ -478,12 +503,15 @@ def route(r: RouteDesc, T: int, logits, bias, topk_ids, topk_w, logits_stride=No
 def router_route(d: MoeDesc, r: RouteDesc, T: int, x, router_w, bias, topk_ids, topk_w, ws, stream=None) -> None:
     """router_topk with routing from scores: logits R x, then route (moe_router_route)."""
     torch = _torch or _load_torch()
+    act, row = _torch_dtype(d.act_dtype), d.hidden * (4 if d.act_dtype == MOE_F32 else 2)
+    _check_bytes("x", x, T * row, act)
+    _check_bytes("router_w", router_w, d.n_experts * row, act)
     _check_tensor("bias", bias, torch.float32, r.n_experts)
     _check_tensor("topk_ids", topk_ids, torch.int32, T * r.top_k)
     _check_tensor("topk_w", topk_w, torch.float32, T * r.top_k)
     _call_on((x, router_w, bias, topk_ids, topk_w, ws), stream, lib().moe_router_route, ctypes.byref(d),
              ctypes.byref(r), T, _ptr(x), _ptr(router_w), _ptr(bias), _ptr(topk_ids), _ptr(topk_w), _ptr(ws),
-             _nbytes(ws))
+             _ws_bytes(ws))
 
 
 def mx_shapes(rows: int, cols: int) -> tuple[tuple[int, int], tuple[int, int]]:
@@ -501,6 +529,8 @@ def _mx_padded(rows: int, cols: int) -> int:
 def _mx_rows(name: str, t):
     """(dtype code, rows, cols, row stride) of a 2-d tensor whose rows are adjacent values."""
     torch = _torch or _load_torch()
+    if t is None or type(t) is int:
+        _bad(f"{name} has to be a tensor")
     shape = t.shape
     if len(shape) != 2 or (shape[1] > 1 and t.stride(1) != 1):
         _bad(f"{name} of shape {tuple(shape)}, strides {t.stride()}: a matrix with adjacent values in its rows expected")
@@ -565,7 +595,7 @@ def mx_linear(d: MxProductDesc, M: int, a, a_scales, w_codes, w_scales, out, ws,
     _check_mx("w", w_codes, w_scales, d.n * (2 if d.act == MX_ACT_SWIGLU else 1), d.k)
     _check_tensor("out", out, _torch_dtype(d.out_dtype), M * d.n)
     _call_on((a, a_scales, w_codes, w_scales, out, ws), stream, lib().mx_linear_forward, ctypes.byref(d), M, _ptr(a),
-             _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), _ptr(out), _ptr(ws), _nbytes(ws))
+             _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), _ptr(out), _ptr(ws), _ws_bytes(ws))
 
 
 def mx_experts(d: MxProductDesc, T: int, a, a_scales, topk_ids, topk_w, slot_table, pool, out, ws, stream=None) -> None:
@@ -576,12 +606,11 @@ def mx_experts(d: MxProductDesc, T: int, a, a_scales, topk_ids, topk_w, slot_tab
     _check_tensor("topk_ids", topk_ids, torch.int32, pairs)
     _check_tensor("topk_w", topk_w, torch.float32, pairs)
     _check_tensor("slot_table", slot_table, torch.int64, d.n_experts)
-    if type(pool) is not int and _nbytes(pool) < d.pool_bytes:
-        _bad(f"pool has {_nbytes(pool)} bytes, pool_bytes is {d.pool_bytes}")
+    _check_bytes("pool", pool, d.pool_bytes)
     _check_tensor("out", out, _torch_dtype(d.out_dtype), (pairs if topk_w is None else T) * d.n)
     _call_on((a, a_scales, topk_ids, topk_w, slot_table, pool, out, ws), stream, lib().mx_experts_forward,
              ctypes.byref(d), T, _ptr(a), _ptr(a_scales), _ptr(topk_ids), _ptr(topk_w), _ptr(slot_table), _ptr(pool),
-             _ptr(out), _ptr(ws), _nbytes(ws))
+             _ptr(out), _ptr(ws), _ws_bytes(ws))
 
 
 class LaunchTimer:

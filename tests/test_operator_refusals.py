@@ -46,3 +46,58 @@ def test_a_dense_quantisation_that_no_grid_holds(a):
     assert M.lib().mx_workspace_bytes(ctypes.byref(d), 1 << 16) > 0
     mx = M.mx_product_desc(16, 1 << 20, a="mx")
     assert M.lib().mx_workspace_bytes(ctypes.byref(mx), 1 << 17) > 0
+
+
+def u8(n, step=1):
+    return torch.zeros(n * step, dtype=torch.uint8)[::step]
+
+
+def test_router_route_checks_its_tensors():
+    """x and router_w of too few values, another floating-point type or strided rows; the same as raw bytes pass on to the
+    next check (tensors that are not on a GPU)."""
+    d = M.desc_for(256, 16, 2, 128, 128, 4, "bf16", "f32", "f32", pool_bytes=1 << 20)
+    r = M.route_desc(16, 2)
+    ids, w, ws = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2), u8(M.workspace_bytes(d, 3))
+
+    def refused(x=None, router=None, ws=ws):
+        x = torch.zeros(3, 256, dtype=torch.bfloat16) if x is None else x
+        router = torch.zeros(16, 256, dtype=torch.bfloat16) if router is None else router
+        with pytest.raises(M.MoeError) as err:
+            M.router_route(d, r, 3, x, router, None, ids, w, ws)
+        return str(err.value)
+    assert "not on a GPU" in refused()
+    assert "not on a GPU" in refused(x=u8(3 * 512), router=u8(16 * 512))
+    assert "x has" in refused(x=torch.zeros(2, 256, dtype=torch.bfloat16)) and "x has" in refused(x=u8(3 * 512 - 1))
+    assert "x is torch.float32" in refused(x=torch.zeros(3, 256)) and "x is torch.float16" in refused(x=torch.zeros(3, 256, dtype=torch.float16))
+    assert "not contiguous" in refused(x=torch.zeros(3, 512, dtype=torch.bfloat16)[:, :256])
+    assert "router_w has" in refused(router=torch.zeros(15, 256, dtype=torch.bfloat16))
+    assert "router_w is" in refused(router=torch.zeros(16, 256))
+    assert "not contiguous" in refused(router=torch.zeros(256, 16, dtype=torch.bfloat16).t())
+    assert "workspace" in refused(ws=BIG) and "workspace" in refused(ws=None) and "not contiguous" in refused(ws=u8(ws.numel(), 2))
+
+
+def test_products_check_their_pool_and_workspace():
+    d = M.mx_product_desc(32, 64, n_experts=4, top_k=2, scales_off=4096, pool_bytes=65536)
+    a, ids, slots = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, dtype=torch.int64)
+    out, need = torch.zeros(8, 32, dtype=torch.bfloat16), M.mx_workspace_bytes(d, 4)
+
+    def refused(pool=u8(65536), ws=u8(need)):
+        with pytest.raises(M.MoeError) as err:
+            M.mx_experts(d, 4, a, None, ids, None, slots, pool, out, ws)
+        return str(err.value)
+    assert "not on a GPU" in refused() and "not on a GPU" in refused(pool=torch.zeros(16384))
+    assert "pool has" in refused(pool=u8(65535)) and "not contiguous" in refused(pool=u8(65536, 2))
+    assert "workspace" in refused(ws=BIG) and "workspace" in refused(ws=None) and "not contiguous" in refused(ws=u8(need, 2))
+    d = M.mx_product_desc(32, 64)
+    need = M.mx_workspace_bytes(d, 4)
+    for ws in (BIG, None, u8(need, 2)):
+        with pytest.raises(M.MoeError) as err:
+            M.mx_linear(d, 4, a, None, u8(32 * 128), u8(32 * 8), out, ws)
+        assert "workspace" in str(err.value)
+
+
+def test_quantisation_takes_tensors():
+    for call in (lambda: M.mx_quantize(BIG, BIG, BIG), lambda: M.mx_dequantize(BIG, BIG, BIG), lambda: M.mx_quantize(None, BIG, BIG)):
+        with pytest.raises(M.MoeError) as err:
+            call()
+        assert "has to be a tensor" in str(err.value)
