@@ -84,6 +84,8 @@ int moe_route_forward(const moe_route_desc* r, int32_t T, const void* logits, in
  * topk_w go to moe_experts_forward as they are.  r->n_experts and r->top_k
  * must equal d's, and r->logit_dtype must be MOE_F32.  Workspace and x,
  * router_w as in moe_router_topk; bias, topk_ids and topk_w as above.
+ * MOE_EINVAL also where x, router_w, bias or an output overlaps the workspace,
+ * or an output an input.
  */
 int moe_router_route(const moe_desc* d, const moe_route_desc* r, int32_t T, const void* x, const void* router_w,
                      const float* bias, int32_t* topk_ids, float* topk_w, void* workspace, size_t ws_bytes,

@@ -280,8 +280,18 @@ int moe_router_route(const moe_desc* d, const moe_route_desc* r, int32_t T, cons
   if ((rc = moe::check_route_out(r, T, bias, topk_ids, topk_w))) return rc;
   moe::WsLayout L;
   if ((rc = check_ws(*d, T, workspace, ws_bytes, &L))) return rc;
-  // the outputs are written while other tokens' logits are still read
-  const size_t n_o = static_cast<size_t>(T) * d->top_k * 4;
+  // the outputs are written while other tokens' logits are still read, and the
+  // logits before the bias is; neither may destroy an input
+  const size_t n_o = static_cast<size_t>(T) * d->top_k * 4, item = d->act_dtype == MOE_F32 ? 4 : 2;
+  const size_t n_b = static_cast<size_t>(d->n_experts) * 4, row = d->hidden * item;
+  const void* ins[3] = {x, router_w, bias};
+  const size_t in_n[3] = {T * row, d->n_experts * row, bias ? n_b : 0};
+  for (int i = 0; i < 3; ++i) {
+    if (overlaps(ins[i], in_n[i], workspace, L.total))
+      return fail(MOE_EINVAL, "x, router_w or bias overlaps the workspace");
+    if (overlaps(topk_ids, n_o, ins[i], in_n[i]) || overlaps(topk_w, n_o, ins[i], in_n[i]))
+      return fail(MOE_EINVAL, "topk_ids or topk_w overlaps x, router_w or bias");
+  }
   if (overlaps(topk_ids, n_o, workspace, L.total) || overlaps(topk_w, n_o, workspace, L.total))
     return fail(MOE_EINVAL, "topk_ids or topk_w overlaps the workspace");
   if (T == 0) return ok();

@@ -101,3 +101,23 @@ def test_quantisation_takes_tensors():
         with pytest.raises(M.MoeError) as err:
             call()
         assert "has to be a tensor" in str(err.value)
+
+
+def test_router_route_refuses_buffers_that_the_call_would_overwrite():
+    d = M.desc_for(256, 16, 2, 128, 128, 4, "f32", "f32", "f32", pool_bytes=1 << 20)
+    r, need = M.route_desc(16, 2), M.workspace_bytes(d, 3)
+    buf = ctypes.create_string_buffer(need + (1 << 18))
+    p = ctypes.addressof(buf) // 256 * 256 + 256
+    x, router, bias, ids, w, ws = p, p + 4096, p + 32768, p + 36864, p + 40960, p + 65536
+
+    def call(x=x, router=router, bias=bias, ids=ids, w=w, T=3):
+        return M.lib().moe_router_route(ctypes.byref(d), ctypes.byref(r), T, x, router, bias, ids, w, ws, need, None)
+    end = ws + need // 256 * 256
+    # the logits would be written over them, or read in their place
+    assert call(bias=ws + 1024) == -1 and call(x=ws + 4096) == -1 and call(router=ws + 4096) == -1 and call(bias=end - 4) == -1
+    assert call(x=ws - 3 * 1024 + 16) == -1 and call(bias=ws - 60) == -1
+    # the outputs over an input
+    assert call(ids=x + 3 * 1024 - 4) == -1 and call(w=x) == -1 and call(ids=router + 16 * 1024 - 4) == -1 and call(w=router - 20) == -1
+    assert call(ids=bias + 60) == -1
+    # T = 0 reads and writes nothing
+    assert call(T=0) == 0
