@@ -70,7 +70,7 @@ struct MxArgs {
   int arows;                // rows of A that exist
   int N, K, chunks;
   int nblk;                 // blocks along N; the grid is flat, these fastest
-  int T, k, E, pair_rows, out_bf16;
+  int k, E, pair_rows, out_bf16;
 };
 
 // The blob offset of expert e, -1 if the id or the slot is unusable.
@@ -206,6 +206,8 @@ __device__ __forceinline__ void store_out(void* out, int64_t i, float y, int bf1
 template <int SRC, int ACT, int MODE, int MT, int NW>
 __global__ __launch_bounds__(NW* kWave) void k_mx_narrow(MxArgs a) {
   constexpr int NM = ACT == MX_ACT_SWIGLU ? 2 : 1;
+  static_assert(MODE != kSum || ACT == MX_ACT_NONE, "a gated product is not linear in its sums");
+  static_assert(MODE != kTiles || SRC == kMxF4, "grouped rows are quantised beside the grouping");
   static_assert(MT == 1 || (MODE == kDense && (MT == 2 || SRC == kMxF4)), "more row tiles are for dense products, more than two for codes");
   __shared__ __align__(16) float red[NM][NW][16][20];   // 20: four-float stores, fewer bank conflicts
   __shared__ int32_t list[kDirectPairs];
@@ -984,17 +986,24 @@ int launched() {
 template <int SRC, int MODE, int MT, int NW>
 void narrow_act(const MxArgs& a, int act, uint32_t blocks, hipStream_t s) {
   const dim3 grid(blocks), block(NW * kWave);
-  if (act == MX_ACT_SWIGLU) launch_kernel(k_mx_narrow<SRC, MX_ACT_SWIGLU, MODE, MT, NW>, grid, block, 0, s, a);
-  else launch_kernel(k_mx_narrow<SRC, MX_ACT_NONE, MODE, MT, NW>, grid, block, 0, s, a);
+  if constexpr (MODE != kSum) {
+    if (act == MX_ACT_SWIGLU) {
+      launch_kernel(k_mx_narrow<SRC, MX_ACT_SWIGLU, MODE, MT, NW>, grid, block, 0, s, a);
+      return;
+    }
+  }
+  launch_kernel(k_mx_narrow<SRC, MX_ACT_NONE, MODE, MT, NW>, grid, block, 0, s, a);
 }
 
+// Row tiles of more than two take codes (their values do not fit the
+// registers), and so do grouped rows.
 template <int MODE, int MT, int NW>
 void narrow_src(const MxArgs& a, int src, int act, uint32_t blocks, hipStream_t s) {
-  // more row tiles than two take codes: their values do not fit the registers
-  constexpr int V = MT <= 2 ? MT : 1;
-  if (MT > 2 || src == kMxF4) narrow_act<kMxF4, MODE, MT, NW>(a, act, blocks, s);
-  else if (src == kF32) narrow_act<kF32, MODE, V, NW>(a, act, blocks, s);
-  else narrow_act<kBF16, MODE, V, NW>(a, act, blocks, s);
+  if constexpr (MT <= 2 && MODE != kTiles) {
+    if (src == kF32) return narrow_act<kF32, MODE, MT, NW>(a, act, blocks, s);
+    if (src == kBF16) return narrow_act<kBF16, MODE, MT, NW>(a, act, blocks, s);
+  }
+  narrow_act<kMxF4, MODE, MT, NW>(a, act, blocks, s);
 }
 
 template <int MODE, int MT = 1>
@@ -1158,7 +1167,6 @@ int mx_experts_forward(const mx_product_desc* d, int32_t T, const void* a, const
   const int64_t wrows = static_cast<int64_t>(d->n) * (d->act == MX_ACT_SWIGLU ? 2 : 1);
   const int64_t end_c = d->codes_off + mx_codes_bytes(wrows, d->k), end_s = d->scales_off + mx_scales_bytes(wrows, d->k);
   g.M = P;
-  g.T = T;
   g.k = d->top_k;
   g.E = d->n_experts;
   g.pair_rows = d->pair_rows;
