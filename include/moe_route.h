@@ -25,7 +25,8 @@
  * mask leaves fewer than k experts still gets k distinct ids; the masked ones
  * have weight 0, and a row that it leaves empty has weights 0 only.  Where
  * every chosen score is 0, renormalize leaves the weights 0.  NaN scores give
- * NaN weights, and so does a logit of +inf under softmax, by the formula.
+ * NaN weights; under softmax a logit that is NaN or +inf makes the denominator
+ * NaN, and so every score and weight of its row.
  *
  * Scores that order experts or groups (a bias, or more than one group) are
  * formed in double precision, so that the choice does not depend on single-

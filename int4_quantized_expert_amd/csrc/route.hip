@@ -586,6 +586,8 @@ __global__ __launch_bounds__(kRtWaves* kWave) void k_route(RouteArgs a) {
       while (L * a.G > kWave) L >>= 1;
       if (!choose_fast<NJ, DT, SIGMOID, VEC>(a, t * a.stride, l, bias, mx, L, lane, lds, reinterpret_cast<float*>(val), &c.id)) {
         c = choose_exact<NJ, SIGMOID, VEC>(a, l, bias, mx, L, lane, lds, val);
+        // a NaN or an infinity (choose_fast leaves such rows) makes every score NaN, also where it is not chosen
+        if (!SIGMOID && c.denom != c.denom) mx = NAN;
       } else if (!SIGMOID && !a.renorm) {
         double sum = 0.0;
 #pragma unroll
@@ -602,9 +604,13 @@ __global__ __launch_bounds__(kRtWaves* kWave) void k_route(RouteArgs a) {
         if (c.denom == 0.0) c.denom = 1.0;
       }
       uint32_t key[NJ];
+      uint64_t nans = 0;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
+      for (int j = 0; j < NJ; ++j) {
+        nans |= __ballot(l[j] != l[j]);
         key[j] = VEC || lane + j * kWave < a.E ? order_key(l[j] != l[j] ? -INFINITY : l[j]) : 0u;
+      }
+      if (!SIGMOID && nans) mx = NAN;   // every score is NaN, also where the NaN is not chosen
       const uint32_t theta = kth_bound<NJ>(key, a.k);
       bool empty = false;   // no number in the row: the lowest ids stay
       if (theta < 0x00800000u) {
@@ -643,7 +649,7 @@ __global__ __launch_bounds__(kRtWaves* kWave) void k_route(RouteArgs a) {
   const bool on = rank < a.k && t < a.T;
   const float lc = on ? load_scalar<DT>(a.logits, static_cast<size_t>(t * a.stride + c.id)) : -INFINITY;
   double sc = 0.0;
-  if (on && lc != -INFINITY) {
+  if (on && (lc != -INFINITY || (!SIGMOID && mx != mx))) {
     if (SIGMOID) sc = 1.0 / (1.0 + exp(-static_cast<double>(lc)));
     else sc = exp(static_cast<double>(lc) - static_cast<double>(mx));
   }

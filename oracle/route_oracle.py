@@ -33,9 +33,8 @@ def scores(row, kind: str) -> list[float]:
     if kind == "sigmoid":
         return [0.0 if l == NINF else (1 / (1 + math.exp(-l)) if l > -700 else math.exp(l)) if l == l else math.nan
                 for l in row]
-    if any(l != l for l in row) or any(l == math.inf for l in row):
-        return [math.nan if not (any(x == math.inf for x in row) and not any(x != x for x in row) and l != math.inf)
-                else 0.0 for l in row]
+    if any(l != l or l == math.inf for l in row):   # exp(inf - inf), and with it the denominator
+        return [math.nan] * len(row)
     m = max(row)
     if m == NINF:
         return [0.0] * len(row)

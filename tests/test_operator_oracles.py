@@ -117,3 +117,14 @@ def test_mx_planted_mistakes_are_caught(monkeypatch, mistake):
         test_mx_worked_block()
         v = X.values(*X.quantize(np.array([[6.0, 1.0, -3.0]])), 3)
         assert v.tolist() == [[6.0, 1.0, -3.0]]
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_route_a_softmax_that_is_not_a_number(bad, renormalize):
+    """exp(inf - inf) or exp(nan) in the denominator: every score of the row is NaN, whichever experts are chosen."""
+    sh = R.RouteShape(4, 2, renormalize=renormalize)
+    ids, w = R.route_row(sh, [1.0, bad, 3.0, NINF])
+    assert ids == ([1, 2] if bad == math.inf else [2, 0]) and all(x != x for x in w)
+    ids, w = R.route_row(sh, [NINF, NINF, 3.0, bad], [0.0] * 4)      # NaN keys: by id, none of the finite ones first
+    assert ids == [0, 1] and all(x != x for x in w)
