@@ -124,7 +124,9 @@ int check_matrix(int32_t dtype, int64_t rows, int64_t cols, const void* x, int64
   if (dtype != MOE_F32 && dtype != MOE_BF16) return bad("dtype=%lld is neither MOE_F32 nor MOE_BF16", dtype);
   if (mx_codes_bytes(rows, cols) < 0) return bad("rows=%lld must be in [0, 2^31), cols=%lld in [0, 2^20]", rows, cols);
   if (rows == 0 || cols == 0) return MOE_OK;
-  if (rows > 1 && (stride < cols || stride > (int64_t(1) << 40))) return bad("row stride %lld is smaller than cols=%lld or too large", stride, cols);
+  // the last row's place in bytes has to fit 64 bits
+  if (rows > 1 && (stride < cols || stride > (int64_t(1) << 56) / (rows - 1)))
+    return bad("row stride %lld is smaller than cols=%lld or too large", stride, cols);
   if (!x || !codes || !scales) return bad("NULL pointer argument");
   const int64_t sz = dtype == MOE_F32 ? 4 : 2;
   if (!at(x, sz) || !at(codes, 16) || !at(scales, 16))

@@ -121,3 +121,13 @@ def test_router_route_refuses_buffers_that_the_call_would_overwrite():
     assert call(ids=bias + 60) == -1
     # T = 0 reads and writes nothing
     assert call(T=0) == 0
+
+
+def test_rows_whose_last_place_does_not_fit_64_bits():
+    """2^30 rows a stride of 2^33 apart and more: their extent is no 64-bit number of bytes, so that nothing could be said
+    about what they overlap."""
+    L = M.lib()
+    for rows, stride in ((1 << 30, 1 << 33), ((1 << 31) - 1, 1 << 40), (1 << 20, 1 << 37)):
+        assert L.mx_quantize(0, rows, 4, BIG, stride, BIG << 1, BIG << 2, None) == -1
+        assert L.mx_dequantize(0, rows, 4, BIG << 1, BIG << 2, BIG, stride, None) == -1
+        assert "stride" in M.last_error()
