@@ -534,12 +534,17 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, int64_t t, int lane
   }
 }
 
+// The row's largest logit, NaN if one is: then every score of a softmax is NaN,
+// also where the NaN is not chosen.
 template <int NJ>
 __device__ __forceinline__ float row_max(const float (&l)[NJ], int lane) {
-  float m = l[0];   // fmaxf passes NaN over
+  float m = l[0];
 #pragma unroll
-  for (int j = 1; j < NJ; ++j) m = fmaxf(m, l[j]);
-  return wave_max_f(m, lane);
+  for (int j = 1; j < NJ; ++j) m = __builtin_elementwise_maximum(m, l[j]);
+#define STEP(S) m = __builtin_elementwise_maximum(m, lane_xor_f<S>(m, lane))
+  STEP(1); STEP(2); STEP(4); STEP(8); STEP(16); STEP(32);
+#undef STEP
+  return m;
 }
 
 // NJ: logits per lane (E <= 64 NJ).  WIDE: experts or groups are compared by
@@ -586,8 +591,7 @@ __global__ __launch_bounds__(kRtWaves* kWave) void k_route(RouteArgs a) {
       while (L * a.G > kWave) L >>= 1;
       if (!choose_fast<NJ, DT, SIGMOID, VEC>(a, t * a.stride, l, bias, mx, L, lane, lds, reinterpret_cast<float*>(val), &c.id)) {
         c = choose_exact<NJ, SIGMOID, VEC>(a, l, bias, mx, L, lane, lds, val);
-        // a NaN or an infinity (choose_fast leaves such rows) makes every score NaN, also where it is not chosen
-        if (!SIGMOID && c.denom != c.denom) mx = NAN;
+        if (!SIGMOID && c.denom != c.denom) mx = NAN;   // +inf (choose_fast leaves such rows), chosen or not
       } else if (!SIGMOID && !a.renorm) {
         double sum = 0.0;
 #pragma unroll
@@ -604,13 +608,9 @@ __global__ __launch_bounds__(kRtWaves* kWave) void k_route(RouteArgs a) {
         if (c.denom == 0.0) c.denom = 1.0;
       }
       uint32_t key[NJ];
-      uint64_t nans = 0;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        nans |= __ballot(l[j] != l[j]);
+      for (int j = 0; j < NJ; ++j)
         key[j] = VEC || lane + j * kWave < a.E ? order_key(l[j] != l[j] ? -INFINITY : l[j]) : 0u;
-      }
-      if (!SIGMOID && nans) mx = NAN;   // every score is NaN, also where the NaN is not chosen
       const uint32_t theta = kth_bound<NJ>(key, a.k);
       bool empty = false;   // no number in the row: the lowest ids stay
       if (theta < 0x00800000u) {
