@@ -196,8 +196,9 @@ __device__ __forceinline__ void store_out(void* out, int64_t i, float y, int bf1
 // LDS.  Bound by the reads of W and the chain of dependent loads before them
 // (ids, slots); every block reads A while W is on its way, and quantises it where
 // that is cheaper than a launch before (quantise_in_place).
-// One token by 4096 x 2048: 4.4 us; through ten experts' gate and up rows (512
-// outputs, k = 2048): 7.4 us, 1.5 TB/s.
+// One token by 4096 x 2048: 4.3 us; through ten experts' gate and up rows (512
+// outputs, k = 2048): 7.1 us, 1.6 TB/s; its sum over eight experts (2048 outputs,
+// k = 512): 5.7 us.  64 rows by 4096 x 4096: 10.2 us.
 //   kDense   rows 16 MT y .. of A
 //   kDirect  y is a pair; the block of the first pair of an expert takes all
 //            of that expert's pairs, the others end
@@ -400,12 +401,16 @@ __global__ __launch_bounds__(NW* kWave) void k_mx_narrow(MxArgs a) {
 //   but the newest chunk's have landed once no more than that number is left.
 //   Bound: 8192^3 by the clock that its power leaves (2.0 GHz, the matrix units
 // busy 40% of the time; the same instructions on registers alone, with random
-// codes, reach 7.1 PFLOP/s), 3.9 PFLOP/s; experts by the reads of W, 4.4 TB/s.
+// codes, reach 7.1 PFLOP/s): 282 to 320 us by what ran before it, 3.4 to 3.9
+// PFLOP/s (the figures above, "instead of", were taken in turn on one card);
+// experts by the reads of W, 4.4 TB/s where a pure read reaches 6.4.
 //   KS = 2: a stage is two chunks, and two groups of waves multiply one each,
 //   their sums joined at the end.  For long rows of tiles that do not fill the
-//   GPU: 512 x 2048 x 8192 takes 19.0 instead of 21.8 us, 256 x 4096 x 4096
-//   12.1 instead of 12.9; with five chunks joining costs more than it saves
-//   (333 x 2000 x 1111 11.4 instead of 10.9).
+//   GPU.  512 x 2048 outputs, one group and two, us in the product: 4 chunks
+//   5.75, 5.81; 5 chunks 6.31, 6.45; 6 chunks 6.88, 6.63; 8 chunks 7.99, 7.40; 12
+//   chunks 10.3, 8.95; 16 chunks 12.6, 10.5; 32 chunks 21.7, 17.0; the same steps
+//   with 8 to 256 tiles.  mx_linear_forward takes two from 16 chunks on, which
+//   leaves out 6 to 15, where two are faster too.
 template <int WM, int WN, int TM, int TN, int S, int KS>
 struct TileCfg {
   static constexpr int kGroup = WM * WN, kWaves = KS * kGroup;
@@ -665,7 +670,7 @@ __global__ __launch_bounds__(KS* WM* WN* kWave) void k_mx_tile(MxArgs a) {
 // where the list is written in order (scattered 4-byte stores to memory took
 // half of 18 us for 20480 pairs); more are read again and placed in memory
 // (NI = 0).  20480 pairs and 2048 x 2048 bf16 values take 11 us, 512 pairs and
-// 512 x 512 values 3.9 us.
+// 512 x 512 values 4.0 us.
 constexpr int kPrepThr = 1024;
 
 struct PrepArgs {
@@ -801,7 +806,8 @@ __global__ __launch_bounds__(kPrepThr) void k_mx_prep(PrepArgs p) {
 // expert (a weight of another pair may be anything).  The rows are fp32: half
 // the bytes would round every product before the sum.  Ids, rows and slots are
 // requested in this order, so that the rows come while the slots are looked up.
-// 64 tokens' 8 rows of 2048: 4.0 us, little over a launch.
+// 64 tokens' 8 rows of 2048: 4.0 to 4.6 us, little over a launch; 2048 tokens'
+// 10 rows: 36 us, 5.2 TB/s.
 __global__ __launch_bounds__(256) void k_mx_combine(MxArgs a, const float* rows) {
   constexpr int kStep = 8;
   const int t = blockIdx.x / a.nblk, lane = threadIdx.x & (kWave - 1);
@@ -1057,9 +1063,12 @@ void prep_src(const PrepArgs& p, uint32_t blocks, hipStream_t s) {
 // `blocks`.  A block's own part must not hold it up (16 rows of 1024 x 8192 in
 // bf16 take 12.2 us against 10.4 with A quantised before, in fp32 20.2) and all
 // of them together not the GPU (16 rows of 16384 x 2048 12.8 and 20.7 against
-// 10.7; 4096 x 2048 7.0 and 7.1 against 9.3).  By expert the part may be twice
-// as large, while ids and slots are looked up (one token's sum over 8 experts,
-// 2048 outputs, k = 512 in fp32: 9.2 us against 11.0).
+// 10.4).  16 rows of 4096 x 2048 take 5.6 us in bf16 and 7.1 in fp32 against 6.8
+// and 6.7 in a row of launches (7.0 and 7.1 against 9.3 where a program's calls
+// are as slow as its host: a launch more is 2 us of it), one row 3.8 and 4.7
+// against 6.1 and 6.3.  By expert the part may be twice as large, while ids and
+// slots are looked up (one token's sum over 8 experts, 2048 outputs, k = 512 in
+// fp32: 9.2 us a call against 11.0).
 bool quantise_in_place(const mx_product_desc& d, int64_t rows, int64_t blocks, int64_t most) {
   const int64_t bytes = rows * d.k * (d.a_dtype == MOE_F32 ? 4 : 2);
   return d.a_dtype != MX_FP4 && bytes <= most && bytes * blocks <= (3 << 24);
@@ -1131,7 +1140,11 @@ int mx_linear_forward(const mx_product_desc* d, int32_t M, const void* a, const 
   };
   // the largest tile that still gives most of the 256 CUs one (a 256 x 256 tile
   // reads half as much per product as a 128 x 128 one: 8192^3 takes 309 against
-  // 454 us; 2048^3, with 64 and 256 tiles, is left to the smaller)
+  // 454 us).  us in the product by k = 1024 and 4096, 256 x 256 against 128 x 128:
+  // 160 of the larger tiles 17.9, 16.4 and 38.6, 38.4; 176 tiles 18.2, 16.3 and
+  // 38.9, 39.0; 208 tiles 18.5, 19.9 and 39.1, 44.0; 256 tiles 19.3, 21.0 and
+  // 41.2, 49.6.  128 x 128 against 64 x 128: 176 of the larger 8.0, 7.4 and 17.4,
+  // 17.2; 256 tiles 8.6, 8.0 and 18.0, 18.0; 384 tiles 11.5, 11.7 and 23.8, 27.8
   if (tiles(256, 256) >= 192) rc = tile<2, 4, 8, 4, 2, 1, false>(g, d->act, (M + 255) / 256, s);
   else if (tiles(128, 128) >= 192) rc = tile<2, 2, 4, 4, 2, 1, false>(g, d->act, (M + 127) / 128, s);
   else if (tiles(64, 128) > 256 || g.chunks < 16) rc = tile<1, 4, 4, 2, 3, 1, false>(g, d->act, (M + 63) / 64, s);

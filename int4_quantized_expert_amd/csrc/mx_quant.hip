@@ -5,9 +5,10 @@
 // values a lane, so that a wave's 16-byte loads and 4-byte stores are
 // contiguous; the block's largest magnitude takes two lane exchanges.  A
 // thread handles kIter such pieces, kQThr pieces apart, all requested before
-// any is used.  131072 x 2048 bf16 values take 149 us to quantise (4.6 TB/s; a
-// large copy reaches 4.75) and 103 us back (6.6 TB/s, part of it into the
-// last-level cache); 8 x 2048 take 2.7 and 2.5 us, an empty kernel's time.
+// any is used.  131072 x 2048 bf16 values take 148 us to quantise (4.6 TB/s; a
+// copy of 4 GiB reaches 4.7, one of 0.5 GiB 5.3) and 105 us back (6.5 TB/s,
+// part of it out of and into the last-level cache); 8 x 2048 take 2.5 and 2.3
+// us, an empty kernel's time.
 #include <hip/hip_runtime.h>
 
 #include <cstdio>

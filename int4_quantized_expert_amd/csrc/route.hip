@@ -550,9 +550,10 @@ __device__ __forceinline__ float row_max(const float (&l)[NJ], int lane) {
 // NJ: logits per lane (E <= 64 NJ).  WIDE: experts or groups are compared by
 // scores (a bias or groups).  VEC: E = 64 NJ and aligned rows.
 // Bound by the instructions of a token's wave: 32768 tokens of 512 bf16 logits
-// in 8 groups take 29.5 us, four times the time of reading them; one token of
-// 256 takes 3.4 us, 2048 of 512 without groups 4.5 us, both little over a
-// launch.
+// in 8 groups (sigmoid) take 31 us, six times the time of reading them; 16384
+// of 512 fp32 logits with a softmax, bias and groups 23.7 us renormalised, 31.5
+// with the exact denominator, with a bias alone 17.5; one token of 256 takes
+// 3.6 us, 2048 of 512 without groups 4.5 us, both little over a launch.
 // The double-precision weights of a block's four tokens are one wave's work
 // (33.4 against 35.0 us at that point).  Several tokens per wave throughout,
 // sharing the bias too, were slower (four 62, eight 65, sixteen 87 us against
