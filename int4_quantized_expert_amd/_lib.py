@@ -100,6 +100,24 @@ class MxProductDesc(ctypes.Structure):
     ]
 
 
+class AttnDesc(ctypes.Structure):
+    """Descriptor of attention over a paged cache (attention.h)."""
+    _fields_ = [
+        ("n_q_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("rotary_pairs", ctypes.c_int32),
+        ("n_pages", ctypes.c_int64),
+        ("scale", ctypes.c_float),
+        ("eps", ctypes.c_float),
+        ("norm_offset", ctypes.c_float),
+    ]
+
+
 _lib = None
 
 
@@ -196,6 +214,17 @@ def lib() -> ctypes.CDLL:
         L.mx_linear_forward.restype = ctypes.c_int
         L.mx_experts_forward.argtypes = [mp, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.mx_experts_forward.restype = ctypes.c_int
+        gp, ap = ctypes.POINTER(GdnDesc), ctypes.POINTER(AttnDesc)
+        L.gdn_chunk_workspace_bytes.argtypes = [gp, i32, i32]
+        L.gdn_chunk_workspace_bytes.restype = sz
+        L.gdn_chunk_forward.argtypes = [gp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.gdn_chunk_forward.restype = ctypes.c_int
+        L.attn_append.argtypes = [ap, i32, i32, vp, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp]
+        L.attn_append.restype = ctypes.c_int
+        L.attn_workspace_bytes.argtypes = [ap, i32, i32, i32, i32]
+        L.attn_workspace_bytes.restype = sz
+        L.attn_forward.argtypes = [ap, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.attn_forward.restype = ctypes.c_int
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
@@ -611,6 +640,114 @@ def mx_experts(d: MxProductDesc, T: int, a, a_scales, topk_ids, topk_w, slot_tab
     _call_on((a, a_scales, topk_ids, topk_w, slot_table, pool, out, ws), stream, lib().mx_experts_forward,
              ctypes.byref(d), T, _ptr(a), _ptr(a_scales), _ptr(topk_ids), _ptr(topk_w), _ptr(slot_table), _ptr(pool),
              _ptr(out), _ptr(ws), _ws_bytes(ws))
+
+
+# ---------------------------------------------------------------------------
+# The gated delta rule over prompts (gdn_chunk.h) and attention over a paged
+# cache (attention.h); arguments checked as above.
+
+ATTN_ROTARY_HALF, ATTN_ROTARY_ADJACENT = 0, 1
+
+
+def _size(n: int) -> int:
+    if n == ctypes.c_size_t(-1).value:
+        raise MoeError(-1, last_error())
+    return n
+
+
+def gdn_chunk_workspace_bytes(d: GdnDesc, B: int, N: int) -> int:
+    """Bytes of workspace for gdn_chunk_forward with B sequences of N tokens together."""
+    return _size(lib().gdn_chunk_workspace_bytes(ctypes.byref(d), B, N))
+
+
+def gdn_chunk_forward(d: GdnDesc, B: int, N: int, T_max: int, cu, q, k, v, alpha, beta, state_in, state_out, out, ws,
+                      stream=None) -> None:
+    """The gated delta rule over B sequences packed in N rows, sequence b in rows cu[b] .. cu[b + 1] - 1, at most T_max of
+    them.  cu: int32 [B + 1]; state_in: float32 [B, n_v, d_v, d_k] or None (zeros); state_out may be state_in."""
+    torch = _torch or _load_torch()
+    act, n_k, n_v = _torch_dtype(d.act_dtype), N * d.n_k_heads * d.d_k, N * d.n_v_heads * d.d_v
+    n_s = B * d.n_v_heads * d.d_v * d.d_k
+    for name, t, dtype, need in (("cu", cu, torch.int32, B + 1), ("q", q, act, n_k), ("k", k, act, n_k), ("v", v, act, n_v),
+                                 ("alpha", alpha, torch.float32, N * d.n_v_heads), ("beta", beta, torch.float32, N * d.n_v_heads),
+                                 ("state_in", state_in, torch.float32, n_s), ("state_out", state_out, torch.float32, n_s),
+                                 ("out", out, _torch_dtype(d.out_dtype), n_v)):
+        if not _fits(t, dtype, need):
+            _misfit(name, t, dtype, need)
+    _call_on((cu, q, k, v, alpha, beta, state_in, state_out, out, ws), stream, lib().gdn_chunk_forward, ctypes.byref(d), B, N,
+             T_max, _ptr(cu), _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(state_in), _ptr(state_out), _ptr(out),
+             _ptr(ws), _ws_bytes(ws))
+
+
+def attn_desc(n_q_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages, dtype="bf16", rotary_dim=0, rotary="half",
+              scale=None, eps=1e-6, norm_offset=0.0) -> AttnDesc:
+    """Descriptor of attention over a paged cache; rotary "half" or "adjacent"; scale defaults to 1/sqrt(head_dim)."""
+    return AttnDesc(n_q_heads, n_kv_heads, head_dim, {"f32": MOE_F32, "bf16": MOE_BF16}[dtype], page_size, max_pages, rotary_dim,
+                    {"half": ATTN_ROTARY_HALF, "adjacent": ATTN_ROTARY_ADJACENT}[rotary], n_pages,
+                    float(head_dim ** -0.5 if scale is None else scale), float(eps), float(norm_offset))
+
+
+def _check_cache(d: AttnDesc, B: int, cu, lens, table, pages) -> None:
+    torch = _torch or _load_torch()
+    i32 = torch.int32
+    for name, t, dtype, need in (("cu", cu, i32, B + 1), ("lens", lens, i32, B), ("table", table, i32, B * d.max_pages),
+                                 ("pages", pages, _torch_dtype(d.dtype), d.n_pages * 2 * d.n_kv_heads * d.page_size * d.head_dim)):
+        if not _fits(t, dtype, need):
+            _misfit(name, t, dtype, need)
+
+
+def _head_rows(name: str, t, dtype, N: int, heads: int, D: int) -> int:
+    """The stride from token to token of a [N, heads, D] tensor whose rows are adjacent values (of an address: packed)."""
+    if t is None or type(t) is int:
+        return heads * D
+    shape, strides = t.shape, t.stride()
+    if t.dtype is not dtype:
+        _bad(f"{name} is {t.dtype}, {dtype} expected")
+    if (len(shape) != 3 or shape[0] < N or shape[1] != heads or shape[2] != D or strides[2] != 1 or
+            (heads > 1 and strides[1] != D)):
+        _bad(f"{name} of shape {tuple(shape)}, strides {strides}: [{N}, {heads}, {D}] with adjacent values in a row expected")
+    return strides[0] if shape[0] > 1 else heads * D
+
+
+def attn_append(d: AttnDesc, B: int, N: int, cu, lens, table, positions, q, k, v, q_norm, k_norm, inv_freq, q_out, pages,
+                stream=None) -> None:
+    """Norms and rotation of q and k, q into q_out, k and v into the cache (attn_append).  q, k, v: [N, heads, head_dim],
+    tokens may be strided (the parts of one product's rows); q and q_out None: k and v only."""
+    torch = _torch or _load_torch()
+    dtype, D = _torch_dtype(d.dtype), d.head_dim
+    qs = _head_rows("q", q, dtype, N, d.n_q_heads, D)
+    ks = _head_rows("k", k, dtype, N, d.n_kv_heads, D)
+    vs = _head_rows("v", v, dtype, N, d.n_kv_heads, D)
+    _check_cache(d, B, cu, lens, table, pages)
+    f32 = torch.float32
+    for name, t, dt, need in (("positions", positions, torch.int32, N), ("q_norm", q_norm, f32, D), ("k_norm", k_norm, f32, D),
+                              ("inv_freq", inv_freq, f32, d.rotary_dim // 2), ("q_out", q_out, dtype, N * d.n_q_heads * D)):
+        if not _fits(t, dt, need):
+            _misfit(name, t, dt, need)
+    _call_on((cu, lens, table, positions, q, k, v, q_norm, k_norm, inv_freq, q_out, pages), stream, lib().attn_append,
+             ctypes.byref(d), B, N, _ptr(cu), _ptr(lens), _ptr(table), _ptr(positions), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs,
+             _ptr(q_norm), _ptr(k_norm), _ptr(inv_freq), _ptr(q_out), _ptr(pages))
+
+
+def attn_workspace_bytes(d: AttnDesc, B: int, N: int, new_max: int, len_max: int) -> int:
+    """Bytes of workspace for attn_forward (0: none is needed)."""
+    return _size(lib().attn_workspace_bytes(ctypes.byref(d), B, N, new_max, len_max))
+
+
+def attn_forward(d: AttnDesc, B: int, N: int, new_max: int, len_max: int, cu, lens, table, tree, q, pages, out, ws=None,
+                 stream=None) -> None:
+    """Attention of the new tokens over the cache (attn_forward).  q, out: [N, n_q_heads, head_dim]; tree: int64 [N], the
+    bits that a row sees of its sequence's new tokens, or None (those up to itself)."""
+    torch = _torch or _load_torch()
+    _check_cache(d, B, cu, lens, table, pages)
+    dtype, need = _torch_dtype(d.dtype), N * d.n_q_heads * d.head_dim
+    if tree is not None and type(tree) is not int and tree.dtype is torch.uint64:
+        tree = tree.view(torch.int64)
+    for name, t, dt, n in (("tree", tree, torch.int64, N), ("q", q, dtype, need), ("out", out, dtype, need)):
+        if not _fits(t, dt, n):
+            _misfit(name, t, dt, n)
+    _call_on((cu, lens, table, tree, q, pages, out, ws), stream, lib().attn_forward, ctypes.byref(d), B, N, new_max, len_max,
+             _ptr(cu), _ptr(lens), _ptr(table), _ptr(tree), _ptr(q), _ptr(pages), _ptr(out), _ptr(ws),
+             0 if ws is None else _ws_bytes(ws))
 
 
 class LaunchTimer:
