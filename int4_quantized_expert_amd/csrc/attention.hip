@@ -13,6 +13,7 @@
 // out of S^T, is already the operand that the second product takes.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 
@@ -39,6 +40,7 @@ struct AttnArgs {
   int nq, nkv, each;
   int new_max, len_max;
   int tiles;            // row tiles a sequence and key head
+  int64_t units;        // blocks a row tile
   int splits, chunk;    // keys a split, a multiple of what a block takes a step
   float scale2;         // scale log2 e
 };
@@ -52,20 +54,16 @@ struct Rows {
 };
 
 __device__ __forceinline__ bool find_rows(const AttnArgs& a, int64_t blk, Rows& r) {
-  // the row tiles that read the same keys go to one XCD (blocks are dealt out
-  // in turns over eight)
-  int64_t unit;
-  if (a.tiles > 1) {
-    const int64_t pos = blk / 8;
-    unit = (pos / a.tiles) * 8 + blk % 8;
-    r.tile = static_cast<int>(pos % a.tiles);
-  } else {
-    unit = blk;
-    r.tile = 0;
-  }
-  if (unit >= static_cast<int64_t>(a.at.B) * a.nkv * a.splits) return false;
-  r.split = static_cast<int>(unit % a.splits);
-  const int64_t bh = unit / a.splits;
+  // The last row tiles first: they see the most keys.  Blocks are dealt out in
+  // turns over eight XCDs; with a power of two of units the tiles that read the
+  // same keys meet in the same XCDs' caches.
+  const int64_t unit = blk % a.units;
+  r.tile = a.tiles - 1 - static_cast<int>(blk / a.units);
+  // The splits of a key head are as many units apart as there are key heads,
+  // and one more, so that a long sequence's go to all XCDs.
+  const int64_t heads = static_cast<int64_t>(a.at.B) * a.nkv;
+  r.split = static_cast<int>(unit / heads);
+  const int64_t bh = (unit + r.split) % heads;
   r.h = static_cast<int>(bh % a.nkv);
   r.b = static_cast<int>(bh / a.nkv);
   const int begin = a.at.cu[r.b], end = a.at.cu[r.b + 1];
@@ -86,12 +84,30 @@ __device__ __forceinline__ int page_at(const AttnArgs& a, int b, int key) {
   return a.at.table[static_cast<int64_t>(b) * a.at.max_pages + (key >> a.at.shift)];
 }
 
-// Offset in elements of a key of head h; page 0 stands in for one that is not there.
+// The page that holds a key, 0 in place of one that is not there.
+__device__ __forceinline__ bool there(const AttnArgs& a, int page) {
+  return (static_cast<uint32_t>(page >= 0) & static_cast<uint32_t>(page < a.at.n_pages)) != 0;
+}
+
+// Offset in elements of a key of head h.
 template <int D>
 __device__ __forceinline__ int64_t key_at(const AttnArgs& a, int page, int h, int key) {
-  const int64_t p = page >= 0 && page < a.at.n_pages ? page : 0;
+  const int64_t p = there(a, page) ? page : 0;
   return p * a.at.page_elems + ((static_cast<int64_t>(h) << a.at.shift) + (key & ((1 << a.at.shift) - 1))) * D;
 }
+
+// A direct load of 16 bytes a lane as lds_load<16>, each lane from an address of its own.
+__device__ __forceinline__ void lds_load_at(const void* p, uint8_t* lds) {
+  const uint32_t la = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_u8*)lds)));
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, off\n\ts_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(la), "v"(p)
+      : "memory");
+}
+
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Whether new token i sees new token j (negative: one before the new ones, seen
 // by all), 0 or 1: what the tree says, or the tokens up to itself.  Without
@@ -116,6 +132,50 @@ __device__ __forceinline__ float xor_add(float x, int lane) {
 __device__ __forceinline__ bf16x4 read_tr(const uint8_t* p) {
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
   return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
+}
+
+// Values that are not finite.  0 times them is NaN, so a product over all keys
+// would carry them to rows that do not see them.  Where a tile with unseen keys
+// holds one, the product runs over the finite values (the others as 0), and a
+// second one counts what each row sees of the others: +inf as 1, -inf as 128,
+// NaN as 129 (both), exact in bf16 and in sums over 64 keys.
+__device__ __forceinline__ bf16x8 finite_part(bf16x8 v) {
+  u32x4 w = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = (w[i] & 0x7f80u) == 0x7f80u ? 0u : w[i] & 0xffffu;
+    const uint32_t hi = (w[i] & 0x7f800000u) == 0x7f800000u ? 0u : w[i] & 0xffff0000u;
+    w[i] = lo | hi;
+  }
+  return __builtin_bit_cast(bf16x8, w);
+}
+__device__ __forceinline__ uint32_t odd_code(uint32_t h) { // of a bf16's bits: 0 for a finite one
+  const uint32_t inf = (h & 0x8000u) ? 0x4300u : 0x3f80u;  // 128 or 1
+  const uint32_t c = (h & 0x7fu) ? 0x4301u : inf;          // 129
+  return (h & 0x7f80u) == 0x7f80u ? c : 0u;
+}
+__device__ __forceinline__ bf16x8 odd_part(bf16x8 v) {
+  u32x4 w = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = odd_code(w[i] & 0xffffu) | (odd_code(w[i] >> 16) << 16);
+  return __builtin_bit_cast(bf16x8, w);
+}
+__device__ __forceinline__ float odd_code_f32(float f) {
+  const float inf = f < 0.f ? 128.f : 1.f;
+  return isnan(f) ? 129.f : (isinf(f) ? inf : 0.f);
+}
+// What the counted values add up to.
+__device__ __forceinline__ float odd_sum(float count) {
+  const float neg = floorf(count * (1.0f / 128.0f)), pos = count - 128.0f * neg;
+  const float one = neg > 0.f ? -INFINITY : (pos > 0.f ? INFINITY : 0.f);
+  return neg > 0.f && pos > 0.f ? __uint_as_float(0x7fc00000u) : one;
+}
+// Eight bits as eight bf16, 0 or 1.
+__device__ __forceinline__ bf16x8 bits_bf16(uint32_t bits) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = ((bits >> (2 * i)) & 1u) * 0x3f80u + ((bits >> (2 * i + 1)) & 1u) * 0x3f800000u;
+  return __builtin_bit_cast(bf16x8, w);
 }
 
 // The joined sums of a block's waves go out: divided and rounded, or as one
@@ -148,31 +208,43 @@ __device__ __forceinline__ float part_weight(float m, float l, float M) { return
 
 // ---------------------------------------------------------------------------
 // Few rows: a block takes 16 RT rows of a key head and a run of its keys, its
-// four waves in turn 32 keys each; they join at the end.
+// four waves in turn 16 X keys each; they join at the end.
 //
 // The reads of K and V bound it.  K goes from memory straight into the operand
-// of S^T (a lane reads 16 bytes of one key), V through registers and LDS, where
-// the transposing read gives four keys of a dim; the next 32 keys are
-// requested before the current ones are worked on.
+// of S^T (a lane reads 16 bytes of one key), V by direct loads into the wave's
+// own part of LDS, where the transposing read gives four keys of a dim; the
+// next keys are under way while the current ones are worked on.  Pieces of
+// 16 bytes lie turned by their row, so that the transposing reads of eight rows
+// fall into different banks.  A step is 32 keys a wave, for 256 dims 16, which
+// leaves room for two blocks on a CU: a block's start (lengths, then pages, then
+// keys: three trips to memory) hides behind the other's work.
+//
+// WHOLE: 16 keys from a multiple of 16 on lie in one page (pages of 16 tokens or
+// more), so their address is one for the wave.  Other pages are looked up key
+// by key.
 template <int D, int RT>
 struct FewLds {
-  static constexpr int kKeys = 32;
-  static constexpr int kV = kKeys * D * 2;                 // a wave's tile of V
-  static constexpr int kCut = RT == 4 ? 32 : 64;           // dims joined at once
+  static constexpr int kX = D == 256 ? 1 : 2;              // runs of 16 keys a step
+  static constexpr int kV = 16 * kX * D * 2;               // a wave's tile of V
+  static constexpr int kCut = 64;                          // dims joined at once
   static constexpr int kRow = kCut + 4;
   static constexpr int kJoin = 4 * 16 * RT * kRow * 4 + 4 * 16 * RT * 2 * 4;
-  static constexpr int kBytes = 4 * kV > kJoin ? 4 * kV : kJoin;
+  static constexpr int kBytes = 8 * kV > kJoin ? 8 * kV : kJoin;
 };
 
-template <int D, int RT>
-__global__ __launch_bounds__(256) void k_attn_few(AttnArgs a) {
+template <int D, int RT, bool WHOLE>
+__global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_few(AttnArgs a) {
   using L = FewLds<D, RT>;
   constexpr int KS = D / 32;                 // steps of 32 dims
   constexpr int DT = D / 16;                 // tiles of 16 dims
-  constexpr int VL = D * 2 * 32 / 16 / 64;   // 16-byte pieces of a V tile a lane
-  __shared__ __align__(16) uint8_t smem[L::kBytes];
+  constexpr int kPer = D / 8;                // 16-byte pieces a row
+  constexpr int kRpl = 64 / kPer;            // rows a direct load
+  constexpr int X = L::kX, kKeys = 16 * X;
+  constexpr int VL = kKeys / kRpl;           // direct loads a tile of V
+  constexpr int kVary = D == 256 ? 4 : (D == 128 ? 2 : 1);   // loads until the turn comes round
+  extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & (kWave - 1);
-  const int wave = threadIdx.x / kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int n16 = lane & 15, g = lane >> 4;
   Rows r;
   if (!find_rows(a, blockIdx.x, r)) return;
@@ -218,94 +290,144 @@ __global__ __launch_bounds__(256) void k_attn_few(AttnArgs a) {
   }
 
   const uint16_t* pool = static_cast<const uint16_t*>(a.pages);
-  uint8_t* vt = smem + wave * L::kV;
-  // piece j of a V tile: 16 bytes at (row, column) of lane + 64 j in row order,
-  // kept at the column turned by the row so that the transposing reads of
-  // eight rows fall into different banks
-  constexpr int kPer = D * 2 / 16;           // pieces a row
   const auto turn = [](int row) { return D == 64 ? ((row >> 1) & 3) * 2 : (row & 7) * 2; };
+  uint32_t voff[kVary];
+#pragma unroll
+  for (int j = 0; j < kVary; ++j)
+    voff[j] = (lane / kPer) * D * 2 + (((lane % kPer) ^ turn(j * kRpl + lane / kPer)) << 4);
+  const int koff = n16 * D + 8 * g;
 
-  u32x4 Kn[2][KS], Vn[VL];
-  bool okn[2];
-  const auto request = [&](int kt) {         // the 32 keys from kt on
+  u32x4 Kn[X][KS];
+  int ids[X];                                // WHOLE: pages of the runs of 16 keys
+  const auto look = [&](int kt) {
+    if constexpr (WHOLE) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      int key = kt + 16 * t + n16;
-      key = key < kend ? key : kend - 1;
-      const int page = page_at(a, r.b, key);
-      okn[t] = page >= 0 && page < a.at.n_pages;
-      const uint16_t* p = pool + key_at<D>(a, page, r.h, key);
-#pragma unroll
-      for (int s = 0; s < KS; ++s) Kn[t][s] = load16(p + 32 * s + 8 * g);
+      for (int t = 0; t < X; ++t) ids[t] = page_at(a, r.b, kt + 16 * t < kend ? kt + 16 * t : kend - 1);
     }
+  };
+  const auto request = [&](int kt, uint8_t* vt) {   // the keys of a step from kt on
+    if constexpr (WHOLE) {
 #pragma unroll
-    for (int j = 0; j < VL; ++j) {
-      const int piece = lane + 64 * j;
-      int key = kt + piece / kPer;
-      key = key < kend ? key : kend - 1;
-      const uint16_t* p = pool + a.at.half_elems + key_at<D>(a, page_at(a, r.b, key), r.h, key);
-      Vn[j] = load16(p + (piece % kPer) * 8);
+      for (int t = 0; t < X; ++t) {
+        // keys behind the end: rows of the last one's page, or of the run's own, that nobody sees
+        const uint16_t* p = pool + key_at<D>(a, ids[t], r.h, kt + 16 * t);
+        const u32x4 rs = raw_rsrc(p + a.at.half_elems, 16 * D * 2);
+#pragma unroll
+        for (int j = t * VL / X; j < (t + 1) * VL / X; ++j)
+          lds_load<16>(rs, vt + j * 1024, voff[j % kVary], ((j * kRpl) & 15) * D * 2);
+      }
+#pragma unroll
+      for (int t = 0; t < X; ++t) {
+        const uint16_t* p = pool + key_at<D>(a, ids[t], r.h, kt + 16 * t);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) Kn[t][s] = load16(p + koff + 32 * s);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VL; ++j) {
+        const int row = j * kRpl + lane / kPer;
+        const int key = kt + row < kend ? kt + row : kend - 1;
+        lds_load_at(pool + a.at.half_elems + key_at<D>(a, page_at(a, r.b, key), r.h, key) + ((lane % kPer) ^ turn(row)) * 8, vt + j * 1024);
+      }
+#pragma unroll
+      for (int t = 0; t < X; ++t) {
+        const int key = kt + 16 * t + n16 < kend ? kt + 16 * t + n16 : kend - 1;
+        const uint16_t* p = pool + key_at<D>(a, page_at(a, r.b, key), r.h, key) + 8 * g;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) Kn[t][s] = load16(p + 32 * s);
+      }
     }
   };
 
-  int kt = kbeg + 32 * wave;
-  if (kt < kend) request(kt);
-  for (; kt < kend; kt += 128) {
-    f32x4 S[RT][2];
-    const bool ok0 = okn[0], ok1 = okn[1];
+  constexpr int kStep = 4 * kKeys;
+  int kt = kbeg + kKeys * wave;
+  uint8_t* const part = smem + wave * 2 * L::kV;
+  int stage = 0;
+  uint32_t gone = 0;                         // WHOLE: runs of 16 keys whose page is not there
+  const auto missing = [&]() {
+    uint32_t w = 0;
+    if constexpr (WHOLE) {
+#pragma unroll
+      for (int t = 0; t < X; ++t) w |= static_cast<uint32_t>(!there(a, ids[t])) << t;
+    }
+    return w;
+  };
+  if (kt < kend) {
+    look(kt);
+    request(kt, part);
+    gone = missing();
+    look(kt + kStep);
+  }
+  for (; kt < kend; kt += kStep) {
+    const uint8_t* vt = part + stage * L::kV;
+    wait_loads();
+    f32x4 S[RT][X];
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < X; ++x) {
         S[t][x] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < KS; ++s)
           S[t][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, Kn[x][s]), Q[t][s], S[t][x], 0, 0, 0);
       }
-#pragma unroll
-    for (int j = 0; j < VL; ++j) {
-      const int piece = lane + 64 * j, row = piece / kPer, col = piece % kPer;
-      *reinterpret_cast<u32x4*>(vt + row * D * 2 + ((col ^ turn(row)) << 4)) = Vn[j];
+    const uint32_t none = WHOLE ? gone : 0;
+    stage ^= 1;
+    if (kt + kStep < kend) {
+      request(kt + kStep, part + stage * L::kV);
+      gone = missing();
+      look(kt + 2 * kStep);
     }
+
     // keys that some row of the tile does not see, or that are not there
-    const uint32_t there = (static_cast<uint32_t>(__ballot(ok0)) & 0xffffu) | (static_cast<uint32_t>(__ballot(ok1)) << 16);
-    const bool careful = there != 0xffffffffu || kt + 32 > kend || kt + 32 > r.prefix;
+    const bool careful = !WHOLE || none != 0 || kt + kKeys > kend || kt + kKeys > r.prefix;
     bool bad = false;                        // such a tile holds a value that is not finite
+    uint32_t seen[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) seen[t] = 0xffu;
     if (careful) {
+      uint32_t in = 0;
+#pragma unroll
+      for (int x = 0; x < X; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = kt + 16 * x + 4 * g + i;
+          uint32_t ok = static_cast<uint32_t>(key < kend);
+          if constexpr (WHOLE) ok &= ~(none >> x);
+          else ok &= static_cast<uint32_t>(there(a, page_at(a, r.b, key < kend ? key : kend - 1)));
+          in |= ok << (4 * x + i);
+        }
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        uint32_t of = 0;
+#pragma unroll
+        for (int x = 0; x < X; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) of |= sees(tree, mask[t], itok[t], kt + 16 * x + 4 * g + i - r.prefix) << (4 * x + i);
+        seen[t] = in & of;
+      }
       typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
       u16x2 big = {0, 0};
 #pragma unroll
-      for (int j = 0; j < VL; ++j)
+      for (int j = 0; j < VL; ++j) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(vt + j * 1024 + lane * 16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) big = __builtin_elementwise_max(big, __builtin_bit_cast(u16x2, Vn[j][i] & 0x7fff7fffu));
+        for (int i = 0; i < 4; ++i) big = __builtin_elementwise_max(big, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
+      }
       bad = __ballot(big[0] >= 0x7f80u || big[1] >= 0x7f80u) != 0;
     }
-    if (kt + 128 < kend) request(kt + 128);
-    wave_sync_lds();
-
+    // P in two bf16 parts: one alone would add an error as large as the output's
+    // own rounding.  With 16 keys a step both go into one product, V twice.
     bf16x8 P[RT], Plo[RT];
-    uint32_t seen[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      seen[t] = 0xffu;
-      if (careful) {
-        seen[t] = 0;
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int at = 16 * x + 4 * g + i;
-            const uint32_t in = static_cast<uint32_t>(kt + at < kend) & (there >> at);
-            seen[t] |= (in & sees(tree, mask[t], itok[t], kt + at - r.prefix)) << (4 * x + i);
-          }
-      }
       float mx = -INFINITY;
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < X; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           S[t][x][i] *= a.scale2;
-          if (careful && !((seen[t] >> (4 * x + i)) & 1u)) S[t][x][i] = -INFINITY;
+          if (careful) S[t][x][i] = ((seen[t] >> (4 * x + i)) & 1u) ? S[t][x][i] : -INFINITY;
           mx = fmaxf(mx, S[t][x][i]);
         }
       mx = xor_max(mx, lane);
@@ -320,63 +442,49 @@ __global__ __launch_bounds__(256) void k_attn_few(AttnArgs a) {
       const float mu = m[t] == -INFINITY ? 0.f : m[t];
       float add = 0.f;
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < X; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float p = __builtin_amdgcn_exp2f(S[t][x][i] - mu);
           add += p;
-          // P in two bf16 parts: one alone would add an error as large as the output's own rounding
-          const __bf16 hi = static_cast<__bf16>(p);
+          const __bf16 hi = static_cast<__bf16>(p), lo = static_cast<__bf16>(p - static_cast<float>(hi));
           P[t][4 * x + i] = hi;
-          Plo[t][4 * x + i] = static_cast<__bf16>(p - static_cast<float>(hi));
+          if constexpr (X == 2) Plo[t][4 * x + i] = lo;
+          else P[t][4 + i] = lo;
         }
       l[t] += add;                           // this lane's keys; the four lanes of a row are joined at the end
     }
-    if (!bad) {
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        // rows 4 g + r, then 16 + 4 g + r; this lane names row (n16 / 4), columns 4 (n16 % 4) ..
-        bf16x8 V;
+    for (int d = 0; d < DT; ++d) {
+      // rows 4 g + r, then 16 + 4 g + r; this lane names row (n16 / 4), columns 4 (n16 % 4) ..
+      bf16x8 V;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int row = 16 * x + 4 * g + (n16 >> 2);
-          const int col = 2 * d + ((n16 & 3) >> 1);
-          const bf16x4 v = read_tr(vt + row * D * 2 + ((col ^ turn(row)) << 4) + (n16 & 1) * 8);
+      for (int x = 0; x < X; ++x) {
+        const int row = 16 * x + 4 * g + (n16 >> 2);
+        const int col = 2 * d + ((n16 & 3) >> 1);
+        const bf16x4 v = read_tr(vt + row * D * 2 + ((col ^ turn(row)) << 4) + (n16 & 1) * 8);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) V[4 * x + i] = v[i];
-        }
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          O[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(V, Plo[t], O[t][d], 0, 0, 0);
-          O[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(V, P[t], O[t][d], 0, 0, 0);
+        for (int i = 0; i < 4; ++i) {
+          V[4 * x + i] = v[i];
+          if constexpr (X == 1) V[4 + i] = v[i];
         }
       }
-    } else {
-      // only the rows that see a value that is not finite may take it (in the
-      // product above 0 times it is NaN): key by key
-      for (int kk = 0; kk < 32; ++kk) {
-        const int from = n16 + 16 * ((kk & 15) >> 2), idx = 4 * (kk >> 4) + (kk & 3);
+      if (bad) {
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-          float p = 0.f;
+          f32x4 c = {0.f, 0.f, 0.f, 0.f};
+          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd_part(V), bits_bf16(seen[t]), c, 0, 0, 0);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) p = x == idx ? static_cast<float>(P[t][x]) + static_cast<float>(Plo[t][x]) : p;
-          p = __shfl(p, from);
-          const bool s = (__shfl(static_cast<int>(seen[t]), from) >> idx) & 1;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            const uint2 w = *reinterpret_cast<const uint2*>(vt + kk * D * 2 + (((2 * d + (g >> 1)) ^ turn(kk)) << 4) + (g & 1) * 8);
-            if (s) {
-              O[t][d][0] = fmaf(p, __uint_as_float(w.x << 16), O[t][d][0]);
-              O[t][d][1] = fmaf(p, __uint_as_float(w.x & 0xffff0000u), O[t][d][1]);
-              O[t][d][2] = fmaf(p, __uint_as_float(w.y << 16), O[t][d][2]);
-              O[t][d][3] = fmaf(p, __uint_as_float(w.y & 0xffff0000u), O[t][d][3]);
-            }
-          }
+          for (int i = 0; i < 4; ++i) O[t][d][i] += odd_sum(c[i]);
         }
+        V = finite_part(V);
+      }
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        if constexpr (X == 2) O[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(V, Plo[t], O[t][d], 0, 0, 0);
+        O[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(V, P[t], O[t][d], 0, 0, 0);
       }
     }
-    wave_sync_lds();                         // the tile's reads before the next one's writes
   }
 
   // join the waves
@@ -420,6 +528,261 @@ __global__ __launch_bounds__(256) void k_attn_few(AttnArgs a) {
     }
     __syncthreads();
   }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: a block takes 128 rows of a key head, 32 a wave, and walks their
+// keys 64 at a time through LDS, which all four waves read; the next 64 are
+// under way by direct loads meanwhile.  32x32x16 products: a lane has 16 of a
+// tile's 32 keys of one row, its partner (lane ^ 32) the others.
+//
+// The matrix units and the reads of LDS bound it alike (each wave reads the
+// whole tile for its 32 rows).  Pieces of 16 bytes lie turned by their row so
+// that the 16 rows, or the four rows of a transposing read, that are read at
+// once fall into different banks.
+//
+// WHOLE as above, with runs of 16 keys (32 for 64 dims).
+template <int D>
+struct TileLds {
+  static constexpr int kTile = 64 * D * 2;                 // bytes of K, and of V
+  static constexpr int kBytes = 4 * kTile;                 // two stages
+};
+
+template <int D>
+__device__ __forceinline__ int k_turn(int key) { return D == 64 ? (key >> 1) & 7 : key & 15; }
+template <int D>
+__device__ __forceinline__ int v_turn(int key) { return D == 64 ? ((key >> 1) & 1) * 4 : (key & 3) * 4; }
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <int D, bool WHOLE>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_tile(AttnArgs a) {
+  using L = TileLds<D>;
+  constexpr int KS = D / 16;                 // steps of 16 dims
+  constexpr int DT = D / 32;                 // tiles of 32 dims
+  constexpr int kPer = D / 8;                // 16-byte pieces a row
+  constexpr int kRpl = 64 / kPer;            // rows a direct load
+  constexpr int kRun = D == 64 ? 32 : 16;    // keys whose page is one
+  constexpr int kRuns = 64 / kRun;
+  constexpr int kLoads = kRun / kRpl / 4;    // direct loads of a wave for a run of K, and of V
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int n32 = lane & 31, g = lane >> 5;
+  Rows r;
+  if (!find_rows(a, blockIdx.x, r)) return;
+  const int rows = r.n * a.each;
+  const int row0 = r.tile * 128;
+  if (row0 >= rows) return;
+  const bool tree = a.tree != nullptr;
+
+  int kend = r.len;
+  if (!tree) {
+    const int last = (row0 + 128 < rows ? row0 + 128 : rows) - 1;
+    const int most = r.prefix + last / a.each + 1;
+    if (most < kend) kend = most > 0 ? most : 0;
+  }
+  const int64_t k0 = static_cast<int64_t>(r.split) * a.chunk;
+  const int kbeg = k0 < kend ? static_cast<int>(k0) : kend;
+  if (kend - kbeg > a.chunk) kend = kbeg + a.chunk;
+
+  const int row = row0 + 32 * wave + n32;
+  const int rr = row < rows ? row : rows - 1;
+  const int itok = rr / a.each;
+  const int64_t token = r.begin + itok;
+  const uint64_t mask = tree ? a.tree[token] : 0;
+  const bool idle = row0 + 32 * wave >= rows;              // a wave without rows only fetches
+  bf16x8 Q[KS];
+  {
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + (token * a.nq + r.h * a.each + rr % a.each) * D;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) Q[s] = __builtin_bit_cast(bf16x8, load16(q + 16 * s + 8 * g));
+  }
+  f32x16 O[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) O[d][i] = 0.f;
+  float m = -INFINITY, l = 0.f;
+
+  // Row (i 4 + wave) kRpl + lane / kPer of a run is load i's; its turn is the same in every run.
+  const uint16_t* pool = static_cast<const uint16_t*>(a.pages);
+  uint32_t koff[kLoads], voff[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int rw = (4 * i + wave) * kRpl + lane / kPer;
+    koff[i] = rw * D * 2 + (((lane % kPer) ^ k_turn<D>(rw)) << 4);
+    voff[i] = rw * D * 2 + (((lane % kPer) ^ v_turn<D>(rw)) << 4);
+  }
+  int ids[kRuns];
+  const auto look = [&](int kt) {
+    if constexpr (WHOLE) {
+#pragma unroll
+      for (int c = 0; c < kRuns; ++c) ids[c] = page_at(a, r.b, kt + kRun * c < kend ? kt + kRun * c : kend - 1);
+    }
+  };
+  const auto request = [&](int kt, uint8_t* st) {
+#pragma unroll
+    for (int c = 0; c < kRuns; ++c) {
+      if constexpr (WHOLE) {
+        // keys behind the end: rows of the last one's page, or of the run's own, that nobody sees
+        const uint16_t* p = pool + key_at<D>(a, ids[c], r.h, kt + kRun * c);
+        const u32x4 rk = raw_rsrc(p, kRun * D * 2), rv = raw_rsrc(p + a.at.half_elems, kRun * D * 2);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          uint8_t* to = st + (c * kRun + (4 * i + wave) * kRpl) * D * 2;
+          lds_load<16>(rk, to, koff[i], 0);
+          lds_load<16>(rv, to + L::kTile, voff[i], 0);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int rw = c * kRun + (4 * i + wave) * kRpl + lane / kPer;
+          const int key = kt + rw < kend ? kt + rw : kend - 1;
+          const uint16_t* p = pool + key_at<D>(a, page_at(a, r.b, key), r.h, key);
+          uint8_t* to = st + (c * kRun + (4 * i + wave) * kRpl) * D * 2;
+          lds_load_at(p + ((lane % kPer) ^ k_turn<D>(rw)) * 8, to);
+          lds_load_at(p + a.at.half_elems + ((lane % kPer) ^ v_turn<D>(rw)) * 8, to + L::kTile);
+        }
+      }
+    }
+  };
+  const auto missing = [&]() {               // runs whose page is not there
+    uint32_t w = 0;
+    if constexpr (WHOLE) {
+#pragma unroll
+      for (int c = 0; c < kRuns; ++c) w |= static_cast<uint32_t>(!there(a, ids[c])) << c;
+    }
+    return w;
+  };
+
+  int stage = 0;
+  uint32_t gone = 0;
+  if (kbeg < kend) {
+    look(kbeg);
+    request(kbeg, smem);
+    gone = missing();
+    look(kbeg + 64);
+  }
+  for (int kt = kbeg; kt < kend; kt += 64) {
+    const uint8_t* Kt = smem + stage * 2 * L::kTile;
+    const uint8_t* Vt = Kt + L::kTile;
+    stage ^= 1;
+    wait_loads();
+    __syncthreads();                         // the tile is there, and nobody reads the other stage any more
+    const uint32_t none = gone;
+    if (kt + 64 < kend) {
+      request(kt + 64, smem + stage * 2 * L::kTile);
+      gone = missing();
+      look(kt + 128);
+    }
+    if (idle) continue;
+    const bool careful = !WHOLE || none != 0 || kt + 64 > kend || kt + 64 > r.prefix;
+    bool bad = false;                        // such a tile holds a value that is not finite
+    if (careful) {
+      typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+      u16x2 big = {0, 0};
+      for (int i = lane; i < 64 * kPer; i += kWave) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(Vt + i * 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) big = __builtin_elementwise_max(big, __builtin_bit_cast(u16x2, w[j] & 0x7fff7fffu));
+      }
+      bad = __ballot(big[0] >= 0x7f80u || big[1] >= 0x7f80u) != 0;
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {            // 32 keys each
+      f32x16 S;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) S[i] = 0.f;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const int key = 32 * x + n32;
+        const u32x4 kv = *reinterpret_cast<const u32x4*>(Kt + key * D * 2 + (((2 * s + g) ^ k_turn<D>(key)) << 4));
+        S = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kv), Q[s], S, 0, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);     // or the reads of V are moved up until registers run out
+      uint32_t seen = 0xffffu;               // bit i: key 32 x + 8 (i / 4) + 4 g + i % 4
+      if (careful) {
+        seen = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int at = kt + 32 * x + 8 * (i >> 2) + 4 * g + (i & 3);
+          uint32_t in = static_cast<uint32_t>(at < kend);
+          if constexpr (WHOLE) in &= ~(none >> ((32 * x + 8 * (i >> 2)) / kRun));
+          else in &= static_cast<uint32_t>(there(a, page_at(a, r.b, at < kend ? at : kend - 1)));
+          seen |= (in & sees(tree, mask, itok, at - r.prefix)) << i;
+        }
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        S[i] *= a.scale2;
+        if (careful) S[i] = ((seen >> i) & 1u) ? S[i] : -INFINITY;
+        mx = fmaxf(mx, S[i]);
+      }
+      mx = fmaxf(mx, __uint_as_float(lane_xor<32>(__float_as_uint(mx), lane)));
+      if (__ballot(mx > m)) {
+        const float mn = fmaxf(m, mx);
+        const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) O[d] *= f;
+      }
+      const float mu = m == -INFINITY ? 0.f : m;
+      bf16x8 P[2];                           // 16 keys each, in the order of the lane's S
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float p = __builtin_amdgcn_exp2f(S[i] - mu);
+        l += p;
+        P[i >> 3][i & 7] = static_cast<__bf16>(p);
+      }
+      const auto value = [&](int d, int j) { // keys 32 x + 16 j + 8 y + 4 g + 0 .. 3, dims 32 d + 16 (lane / 16 % 2) ..
+        bf16x8 V;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int key = 32 * x + 16 * j + 8 * y + 4 * g + ((lane & 15) >> 2);
+          const int col = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+          const bf16x4 v = read_tr(Vt + key * D * 2 + ((col ^ v_turn<D>(key)) << 4) + (lane & 1) * 8);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) V[4 * y + i] = v[i];
+        }
+        return V;
+      };
+      __builtin_amdgcn_sched_barrier(0);
+      if (bad) {
+        // O d by d, with little held at once: this is rare
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          f32x16 c;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) c[i] = 0.f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(odd_part(value(d, j)), bits_bf16(seen >> (8 * j)), c, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) O[d][i] += odd_sum(c[i]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          bf16x8 V = value(d, j);
+          if (bad) V = finite_part(V);
+          O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(V, P[j], O[d], 0, 0, 0);
+        }
+    }
+  }
+  if (row >= rows) return;
+  l += __uint_as_float(lane_xor<32>(__float_as_uint(l), lane));
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float o[4] = {O[d][4 * i], O[d][4 * i + 1], O[d][4 * i + 2], O[d][4 * i + 3]};
+      store_row<kBF16, D>(a, r, row, 32 * d + 8 * i + 4 * g, o, m, l);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -561,29 +924,27 @@ __global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
         p[i] = __builtin_amdgcn_exp2f(S[i] - mu);
         l[t] += p[i];
       }
-      if (!bad) {
+#pragma unroll
+      for (int d = 0; d < DQ; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float v = V[k][d][i];
+            if (bad) v = (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u ? 0.f : v;
+            O[t][d][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, p[k], O[t][d][i], 0, 0, 0);
+          }
+      if (bad) {
 #pragma unroll
         for (int d = 0; d < DQ; ++d)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 4; ++i) {
+            f32x4 c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) O[t][d][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(V[k][d][i], p[k], O[t][d][i], 0, 0, 0);
-      } else {
-        // as above: key 4 kg + k for its rows only; dim 64 d + 4 (4 g + j) + i of it is with lane 4 g + j of group kg
-        for (int kg = 0; kg < 4; ++kg)
+            for (int k = 0; k < 4; ++k)
+              c = __builtin_amdgcn_mfma_f32_16x16x4f32(odd_code_f32(V[k][d][i]), static_cast<float>((seen >> k) & 1u), c, 0, 0, 0);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float pk = __shfl(p[k], n16 + 16 * kg);
-            const bool s = (__shfl(static_cast<int>(seen), n16 + 16 * kg) >> k) & 1;
-#pragma unroll
-            for (int d = 0; d < DQ; ++d)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const float v = __shfl(V[k][d][i], 16 * kg + 4 * g + j);
-                  if (s) O[t][d][i][j] = fmaf(pk, v, O[t][d][i][j]);
-                }
+            for (int j = 0; j < 4; ++j) O[t][d][i][j] += odd_sum(c[j]);
           }
       }
     }
@@ -636,37 +997,59 @@ __global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// The splits of a row joined: D / 4 lanes a row, four dims each.
+// The splits of a row joined: a block a row.  Every wave forms all weights (a
+// split a lane); D / 4 lanes take one split's sums, the groups of them in turn.
+constexpr int kMaxSplits = kWave;
+
 template <int DT, int D>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  constexpr int LR = D / 4;
-  const int per = 256 / LR;                  // rows a block
-  const int64_t steps = (static_cast<int64_t>(a.new_max) * a.nq + per - 1) / per;
-  const int b = static_cast<int>(blockIdx.x / steps);
-  const int64_t row = (blockIdx.x % steps) * per + threadIdx.x / LR;
-  const int c0 = (threadIdx.x % LR) * 4;
+  constexpr int LR = D / 4, G = 256 / LR;
+  __shared__ __align__(16) float sums[G][D];
+  const int64_t per = static_cast<int64_t>(a.new_max) * a.nq;
+  const int b = static_cast<int>(blockIdx.x / per);
+  const int64_t row = blockIdx.x % per;
   const int begin = a.at.cu[b], end = a.at.cu[b + 1];
-  if (begin < 0 || end > a.at.N || end <= begin) return;
-  const int n = end - begin < a.new_max ? end - begin : a.new_max;
-  if (row >= static_cast<int64_t>(n) * a.nq) return;
+  if (begin < 0 || end > a.at.N || row >= static_cast<int64_t>(end - begin) * a.nq) return;
   const int64_t o = static_cast<int64_t>(begin) * a.nq + row;
-  const float* ml = a.ml + o * a.splits * 2;
-  const float* part = a.part + o * a.splits * D + c0;
-  float M = -INFINITY;
-  for (int s = 0; s < a.splits; ++s) M = fmaxf(M, ml[2 * s]);
-  float l = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < a.splits; ++s) {
-    const float ls = ml[2 * s + 1];
-    if (ls == 0.f) continue;
-    const float f = part_weight(ml[2 * s], ls, M);
-    l = fmaf(ls, f, l);
-    const f32x4 v = *reinterpret_cast<const f32x4*>(part + static_cast<int64_t>(s) * D);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sum[j] = fmaf(v[j], f, sum[j]);
+  const int lane = threadIdx.x & (kWave - 1), grp = threadIdx.x / LR, c0 = (threadIdx.x % LR) * 4;
+  float m = -INFINITY, l = 0.f;
+  if (lane < a.splits) {
+    const float2 w = *reinterpret_cast<const float2*>(a.ml + (o * a.splits + lane) * 2);
+    m = w.x;
+    l = w.y;
   }
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  float M = m;
+  for (int s = 1; s < kWave; s <<= 1) M = fmaxf(M, __shfl_xor(M, s));
+  const float f = part_weight(m, l, M);
+  float total = l * f;
+  for (int s = 1; s < kWave; s <<= 1) total += __shfl_xor(total, s);
+  const float* part = a.part + o * a.splits * D + c0;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < a.splits; s0 += 4 * G) {
+    f32x4 v[4];
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = s0 + G * i + grp;
+      w[i] = __shfl(l == 0.f ? -1.f : f, s < kWave ? s : 0);   // a split without keys has written no sums
+      if (s >= a.splits) w[i] = -1.f;
+      v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (w[i] != -1.f) v[i] = *reinterpret_cast<const f32x4*>(part + static_cast<int64_t>(s) * D);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (w[i] != -1.f)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] = fmaf(v[i][j], w[i], sum[j]);
+  }
+  *reinterpret_cast<f32x4*>(&sums[grp][c0]) = sum;
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int i = 1; i < G; ++i) sum += *reinterpret_cast<const f32x4*>(&sums[i][c0]);
+  const float inv = total == 0.f ? 0.f : 1.0f / total;
   if constexpr (DT == kF32) {
-    *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o * D + c0) = f32x4{sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv};
+    *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o * D + c0) = sum * inv;
   } else {
     uint2 w;
     w.x = f32_to_bf16(sum[0] * inv) | (static_cast<uint32_t>(f32_to_bf16(sum[1] * inv)) << 16);
@@ -677,10 +1060,10 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 
 // ---------------------------------------------------------------------------
 struct AttnPlan {
-  int rt;               // tiles of 16 rows a block
+  int rt;               // 16 rows a block times this
   int tiles;            // row tiles a sequence and key head
   int splits, chunk;
-  int64_t blocks;
+  int64_t units, blocks;
   size_t part, total;   // workspace: sums, then maxima and denominators
 };
 
@@ -690,14 +1073,14 @@ int attn_plan(const attn_desc* d, int32_t B, int32_t N, int32_t new_max, int32_t
   const int each = d->n_q_heads / d->n_kv_heads;
   const int most = new_max < N ? new_max : N;
   const int64_t rows = static_cast<int64_t>(most) * each;
-  const int cap = d->dtype == MOE_F32 ? 2 : (d->head_dim == 256 ? 2 : 4);
-  p->rt = rows <= 16 ? 1 : (rows <= 32 || cap == 2 ? 2 : 4);
+  p->rt = d->dtype == MOE_F32 ? (rows <= 16 ? 1 : 2) : (rows <= 16 ? 1 : (rows <= 32 && d->head_dim < 256 ? 2 : 8));
   p->tiles = static_cast<int>((rows + 16 * p->rt - 1) / (16 * p->rt));
   if (p->tiles < 1) p->tiles = 1;
-  const int step = d->dtype == MOE_F32 ? 64 : 128;
+  const int step = d->dtype == MOE_F32 || p->rt == 8 || d->head_dim == 256 ? 64 : 128;   // keys a block takes at once
   const int64_t units = static_cast<int64_t>(B) * d->n_kv_heads * p->tiles;
-  int64_t splits = units > 0 ? 1024 / units : 1;
-  if (splits > 64) splits = 64;
+  static const int64_t target = getenv("ATTN_T") ? atoll(getenv("ATTN_T")) : 1024;
+  int64_t splits = units > 0 ? target / units : 1;
+  if (splits > kMaxSplits) splits = kMaxSplits;
   if (splits < 1) splits = 1;
   int64_t chunk = (len_max + splits - 1) / splits;
   chunk = (chunk + step - 1) / step * step;
@@ -705,9 +1088,10 @@ int attn_plan(const attn_desc* d, int32_t B, int32_t N, int32_t new_max, int32_t
   p->chunk = static_cast<int>(chunk);
   p->splits = static_cast<int>((len_max + chunk - 1) / chunk);
   if (p->splits < 1) p->splits = 1;
-  const int64_t groups = static_cast<int64_t>(B) * d->n_kv_heads * p->splits;
-  p->blocks = (p->tiles > 1 ? (groups + 7) / 8 * 8 : groups) * p->tiles;
-  if (p->blocks >= (int64_t(1) << 24)) return attn_bad("%lld blocks are too many for one launch", p->blocks);
+  p->units = static_cast<int64_t>(B) * d->n_kv_heads * p->splits;
+  p->blocks = p->units * p->tiles;
+  const int64_t join = p->splits > 1 ? static_cast<int64_t>(B) * most * d->n_q_heads : 0;
+  if (p->blocks >= (int64_t(1) << 24) || join >= (int64_t(1) << 24)) return attn_bad("B=%lld sequences of new_max=%lld tokens are too many blocks for one launch", B, new_max);
   p->part = 0;
   p->total = 0;
   if (p->splits > 1) {
@@ -717,24 +1101,46 @@ int attn_plan(const attn_desc* d, int32_t B, int32_t N, int32_t new_max, int32_t
   return MOE_OK;
 }
 
+// Launch with dynamic LDS, whose size is set once per kernel and device.
+template <void (*KERNEL)(AttnArgs), int BYTES>
+bool launch_lds(const AttnArgs& a, dim3 grid, hipStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return false;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!bit || !(done.load(std::memory_order_relaxed) & bit)) {
+    if (hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize, BYTES) != hipSuccess)
+      return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+  }
+  launch_kernel(KERNEL, grid, dim3(256), BYTES, s, a);
+  return true;
+}
+
+template <int D, bool WHOLE>
+bool launch_bf16(const AttnArgs& a, int rt, dim3 grid, hipStream_t s) {
+  if (rt == 1) return launch_lds<k_attn_few<D, 1, WHOLE>, FewLds<D, 1>::kBytes>(a, grid, s);
+  if constexpr (D < 256)
+    if (rt == 2) return launch_lds<k_attn_few<D, 2, WHOLE>, FewLds<D, 2>::kBytes>(a, grid, s);
+  return launch_lds<k_attn_tile<D, WHOLE>, TileLds<D>::kBytes>(a, grid, s);
+}
+
 template <int D>
-void launch_attn_d(const AttnArgs& a, const AttnPlan& p, int dtype, hipStream_t s) {
+bool launch_attn_d(const AttnArgs& a, const AttnPlan& p, int dtype, hipStream_t s) {
   const dim3 grid(static_cast<uint32_t>(p.blocks)), block(256);
   if (dtype == MOE_F32) {
     if (p.rt == 1) launch_kernel(k_attn_f32<D, 1>, grid, block, 0, s, a);
     else launch_kernel(k_attn_f32<D, 2>, grid, block, 0, s, a);
   } else {
-    if (p.rt == 1) launch_kernel(k_attn_few<D, 1>, grid, block, 0, s, a);
-    else if (p.rt == 2) launch_kernel(k_attn_few<D, 2>, grid, block, 0, s, a);
-    else if constexpr (D < 256) launch_kernel(k_attn_few<D, 4>, grid, block, 0, s, a);
+    const bool whole = a.at.shift >= (p.rt == 8 && D == 64 ? 5 : 4);
+    if (!(whole ? launch_bf16<D, true>(a, p.rt, grid, s) : launch_bf16<D, false>(a, p.rt, grid, s))) return false;
   }
   if (p.splits > 1) {
-    const int64_t per = 256 / (D / 4);
-    const int64_t steps = (static_cast<int64_t>(a.new_max) * a.nq + per - 1) / per;
-    const dim3 jg(static_cast<uint32_t>(steps * a.at.B));
+    const dim3 jg(static_cast<uint32_t>(static_cast<int64_t>(a.new_max) * a.nq * a.at.B));
     if (dtype == MOE_F32) launch_kernel(k_attn_join<kF32, D>, jg, block, 0, s, a);
     else launch_kernel(k_attn_join<kBF16, D>, jg, block, 0, s, a);
   }
+  return true;
 }
 
 }  // namespace
@@ -794,15 +1200,16 @@ extern "C" int attn_forward(const attn_desc* d, int32_t B, int32_t N, int32_t ne
   a.new_max = new_max < N ? new_max : N;
   a.len_max = len_max;
   a.tiles = p.tiles;
+  a.units = p.units;
   a.splits = p.splits;
   a.chunk = p.chunk;
   a.scale2 = d->scale * 1.4426950408889634f;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (d->head_dim == 64) launch_attn_d<64>(a, p, d->dtype, s);
-  else if (d->head_dim == 128) launch_attn_d<128>(a, p, d->dtype, s);
-  else launch_attn_d<256>(a, p, d->dtype, s);
+  const bool sent = d->head_dim == 64    ? launch_attn_d<64>(a, p, d->dtype, s)
+                    : d->head_dim == 128 ? launch_attn_d<128>(a, p, d->dtype, s)
+                                         : launch_attn_d<256>(a, p, d->dtype, s);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) {
+  if (e != hipSuccess || !sent) {
     char buf[256];
     snprintf(buf, sizeof(buf), "attention launch failed: %s", hipGetErrorString(e));
     return api_fail(MOE_EHIP, buf);
