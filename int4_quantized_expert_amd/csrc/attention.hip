@@ -35,49 +35,139 @@ struct AttnArgs {
   const void* q;
   const void* pages;
   void* out;
-  float* part;          // [N n_q][splits][D] sums, where keys are split
-  float* ml;            // [N n_q][splits][2] their maxima and denominators
+  float* part;          // even: [blocks][2][rows of a tile][D] sums
+  float* ml;            // even: [blocks][2][rows of a tile][2] their maxima and denominators
+  int* shares;          // even: steps a block, then the steps up to and with each sequence
   int nq, nkv, each;
   int new_max, len_max;
-  int tiles;            // row tiles a sequence and key head
-  int64_t units;        // blocks a row tile
-  int splits, chunk;    // keys a split, a multiple of what a block takes a step
+  int tiles;            // row tiles a sequence and key head, at most
+  int blocks;
   float scale2;         // scale log2 e
 };
 
-// What one block works on; false: nothing.
+// One unit of work: a tile of rows of one key head of one sequence.
 struct Rows {
-  int b, h, tile, split;
+  int b, h, tile;
   int begin, n;         // first row of the sequence, its new tokens (at most new_max)
   int prefix;           // tokens before the new ones (negative: the first new ones are not in the sequence)
   int len;              // tokens that may be seen
 };
 
-__device__ __forceinline__ bool find_rows(const AttnArgs& a, int64_t blk, Rows& r) {
-  // The last row tiles first: they see the most keys.  Blocks are dealt out in
-  // turns over eight XCDs; with a power of two of units the tiles that read the
-  // same keys meet in the same XCDs' caches.
-  const int64_t unit = blk % a.units;
-  r.tile = a.tiles - 1 - static_cast<int>(blk / a.units);
-  // The splits of a key head are as many units apart as there are key heads,
-  // and one more, so that a long sequence's go to all XCDs.
-  const int64_t heads = static_cast<int64_t>(a.at.B) * a.nkv;
-  r.split = static_cast<int>(unit / heads);
-  const int64_t bh = (unit + r.split) % heads;
-  r.h = static_cast<int>(bh % a.nkv);
-  r.b = static_cast<int>(bh / a.nkv);
-  const int begin = a.at.cu[r.b], end = a.at.cu[r.b + 1];
-  if (begin < 0 || end > a.at.N || end <= begin) return false;
+// Sequence b; false: it brings no token, or does not fit the rows.
+__device__ __forceinline__ bool sequence(const AttnArgs& a, int b, Rows& r) {
+  const int begin = a.at.cu[b], end = a.at.cu[b + 1], len = a.at.lens[b];
+  r.b = b;
   r.begin = begin;
   const int n = end - begin;
   r.n = n < a.new_max ? n : a.new_max;
   const int64_t room = static_cast<int64_t>(a.at.max_pages) << a.at.shift;
-  const int len = a.at.lens[r.b];
   r.prefix = (len > 0 ? len : 0) - n;
   int64_t seen = len < a.len_max ? len : a.len_max;
   if (seen > room) seen = room;
   r.len = seen > 0 ? static_cast<int>(seen) : 0;
-  return true;
+  return begin >= 0 && end <= a.at.N && end > begin;
+}
+
+// What the rows [row0, row0 + count) of a sequence see at most.
+__device__ __forceinline__ int last_key(const AttnArgs& a, const Rows& r, int row0, int count) {
+  if (a.tree) return r.len;
+  const int rows = r.n * a.each;
+  const int last = (row0 + count < rows ? row0 + count : rows) - 1;
+  const int most = r.prefix + last / a.each + 1;
+  return most < r.len ? (most > 0 ? most : 0) : r.len;
+}
+
+// Even shares.  The units in order (sequence, key head, tile) have as many
+// steps of STEP keys each as the sequence has; every block takes a share of
+// all steps, so a long context is many blocks' work and a block takes many
+// short ones.  A block finishes all units but, at most, the first and the last
+// of its share; their sums go to the workspace and are joined by a second launch,
+// which finds the share and the steps before each sequence there too.
+template <int STEP>
+__device__ __forceinline__ int steps_of(const Rows& r) { return (r.len + STEP - 1) / STEP; }
+template <int ROWS>
+__device__ __forceinline__ int tiles_of(const AttnArgs& a, const Rows& r) { return (r.n * a.each + ROWS - 1) / ROWS; }
+
+// Steps of sequence b; all of them together are below 2^31 (the host sees to that).
+template <int ROWS, int STEP>
+__device__ __forceinline__ int work_of(const AttnArgs& a, int b) {
+  Rows r;
+  if (b >= a.at.B || !sequence(a, b, r)) return 0;
+  return a.nkv * tiles_of<ROWS>(a, r) * steps_of<STEP>(r);
+}
+
+__device__ __forceinline__ int wave_scan(int x, int lane) {      // inclusive
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int o = __shfl_up(x, d);
+    x += lane >= d ? o : 0;
+  }
+  return x;
+}
+
+// Calls unit(rows, first key, last key + 1, whole, slot) for everything that
+// this block works on; not whole: the sums go to its slot.
+template <int ROWS, int STEP, bool EVEN, typename F>
+__device__ __forceinline__ void walk(const AttnArgs& a, int lane, F unit) {
+  Rows r;
+  if constexpr (!EVEN) {
+    // The last row tiles first: they see the most keys.  Blocks are dealt out in
+    // turns over eight XCDs; with a power of two of heads the tiles that read the
+    // same keys meet in the same XCDs' caches.
+    const int heads = a.at.B * a.nkv;
+    const int bh = blockIdx.x % heads;
+    r.tile = a.tiles - 1 - static_cast<int>(blockIdx.x / heads);
+    r.h = bh % a.nkv;
+    if (!sequence(a, bh / a.nkv, r) || r.tile >= tiles_of<ROWS>(a, r)) return;
+    unit(r, 0, last_key(a, r, r.tile * ROWS, ROWS), true, 0);
+  } else {
+    const bool writes = blockIdx.x == 0 && threadIdx.x < kWave;
+    // all steps, and with a batch that one wave holds the steps up to each sequence
+    int in = wave_scan(work_of<ROWS, STEP>(a, lane), lane);
+    int total = __shfl(in, kWave - 1);
+    if (writes && lane < a.at.B) a.shares[1 + lane] = in;
+    for (int i = kWave; i < a.at.B; i += kWave) {
+      const int more = total + wave_scan(work_of<ROWS, STEP>(a, i + lane), lane);
+      if (writes && i + lane < a.at.B) a.shares[1 + i + lane] = more;
+      total = __shfl(more, kWave - 1);
+    }
+    total = __builtin_amdgcn_readfirstlane(total);
+    const int per = total > 0 ? (total + a.blocks - 1) / a.blocks : 1;
+    if (writes && lane == 0) a.shares[0] = per;
+    // neighbouring shares, which may be of one sequence, are neighbouring blocks and go to different XCDs
+    if (static_cast<int64_t>(blockIdx.x) * per >= total) return;
+    const int first = static_cast<int>(blockIdx.x) * per;
+    const int end = total - first < per ? total : first + per;
+    int pos = first, b = 0, rem = first;
+    for (int i = 0;; i += kWave) {
+      const int n = __popcll(__ballot(in <= first));         // sequences that end before the share
+      b = i + n;
+      if (n > 0) rem = first - __shfl(in, n - 1);
+      if (n < kWave || i + kWave >= a.at.B) break;
+      in = __shfl(in, kWave - 1) + wave_scan(work_of<ROWS, STEP>(a, i + kWave + lane), lane);
+    }
+    b = __builtin_amdgcn_readfirstlane(b);
+    rem = __builtin_amdgcn_readfirstlane(rem);
+    while (pos < end && b < a.at.B) {
+      const bool ok = sequence(a, b, r);
+      const int steps = ok ? steps_of<STEP>(r) : 0, tiles = tiles_of<ROWS>(a, r);
+      const int all = a.nkv * tiles * steps;
+      if (rem >= all) {
+        rem -= all;
+        ++b;
+        continue;
+      }
+      const int idx = rem / steps, step = rem % steps;
+      const int count = steps - step < end - pos ? steps - step : end - pos;
+      r.h = idx / tiles;
+      r.tile = idx % tiles;
+      const int most = last_key(a, r, r.tile * ROWS, ROWS);
+      const int k1 = (step + count) * STEP;
+      unit(r, step * STEP, k1 < most ? k1 : most, count == steps, pos == first ? 0 : 1);
+      pos += count;
+      rem += count;
+    }
+  }
 }
 
 __device__ __forceinline__ int page_at(const AttnArgs& a, int b, int key) {
@@ -178,29 +268,33 @@ __device__ __forceinline__ bf16x8 bits_bf16(uint32_t bits) {
   return __builtin_bit_cast(bf16x8, w);
 }
 
-// The joined sums of a block's waves go out: divided and rounded, or as one
-// split's part.  `sum` holds dims [c0, c0 + 4) of row r of the tile.
-template <int DT, int D>
-__device__ __forceinline__ void store_row(const AttnArgs& a, const Rows& r, int row, int c0, const float (&sum)[4], float m, float l) {
-  const int64_t token = r.begin + row / a.each;
-  const int64_t o = token * a.nq + r.h * a.each + row % a.each;
-  if (a.splits > 1) {
-    *reinterpret_cast<f32x4*>(a.part + (o * a.splits + r.split) * D + c0) = f32x4{sum[0], sum[1], sum[2], sum[3]};
-    if (c0 == 0) {
-      a.ml[(o * a.splits + r.split) * 2] = m;
-      a.ml[(o * a.splits + r.split) * 2 + 1] = l;
-    }
-    return;
-  }
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
+// Four sums over their denominator, rounded; no denominator: zeros.
+template <int DT>
+__device__ __forceinline__ void put_row(void* out, int64_t at, const f32x4& sum, float l) {
+  const f32x4 y = sum * (l == 0.f ? 0.f : 1.0f / l);
   if constexpr (DT == kF32) {
-    *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o * D + c0) = f32x4{sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv};
+    *reinterpret_cast<f32x4*>(static_cast<float*>(out) + at) = y;
   } else {
     uint2 w;
-    w.x = f32_to_bf16(sum[0] * inv) | (static_cast<uint32_t>(f32_to_bf16(sum[1] * inv)) << 16);
-    w.y = f32_to_bf16(sum[2] * inv) | (static_cast<uint32_t>(f32_to_bf16(sum[3] * inv)) << 16);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o * D + c0) = w;
+    w.x = f32_to_bf16(y[0]) | (static_cast<uint32_t>(f32_to_bf16(y[1])) << 16);
+    w.y = f32_to_bf16(y[2]) | (static_cast<uint32_t>(f32_to_bf16(y[3])) << 16);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = w;
   }
+}
+
+// The joined sums of a block's waves go out: divided and rounded, or as one
+// share's part.  `sum` holds dims [c0, c0 + 4) of row `row` of the sequence's.
+template <int DT, int D, int ROWS>
+__device__ __forceinline__ void store_row(const AttnArgs& a, const Rows& r, int row, int c0, const f32x4& sum, float m, float l,
+                                          bool whole, int slot) {
+  if (!whole) {
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * ROWS + row - r.tile * ROWS;
+    *reinterpret_cast<f32x4*>(a.part + at * D + c0) = sum;
+    if (c0 == 0) *reinterpret_cast<float2*>(a.ml + at * 2) = float2{m, l};
+    return;
+  }
+  const int64_t o = (r.begin + static_cast<int64_t>(row / a.each)) * a.nq + r.h * a.each + row % a.each;
+  put_row<DT>(a.out, o * D + c0, sum, l);
 }
 
 // Weight of a part whose maximum is m among parts whose largest is M.
@@ -232,7 +326,7 @@ struct FewLds {
   static constexpr int kBytes = 8 * kV > kJoin ? 8 * kV : kJoin;
 };
 
-template <int D, int RT, bool WHOLE>
+template <int D, int RT, bool WHOLE, bool EVEN>
 __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_few(AttnArgs a) {
   using L = FewLds<D, RT>;
   constexpr int KS = D / 32;                 // steps of 32 dims
@@ -246,23 +340,10 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_few(AttnArgs a) {
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int n16 = lane & 15, g = lane >> 4;
-  Rows r;
-  if (!find_rows(a, blockIdx.x, r)) return;
+  walk<16 * RT, 4 * 16 * L::kX, EVEN>(a, lane, [&](const Rows& r, int kbeg, int kend, bool whole, int slot) {
   const int rows = r.n * a.each;
   const int row0 = r.tile * 16 * RT;
-  if (row0 >= rows) return;
   const bool tree = a.tree != nullptr;
-
-  // what the tile's last row sees at most
-  int kend = r.len;
-  if (!tree) {
-    const int last = (row0 + 16 * RT < rows ? row0 + 16 * RT : rows) - 1;
-    const int most = r.prefix + last / a.each + 1;
-    if (most < kend) kend = most > 0 ? most : 0;
-  }
-  const int64_t k0 = static_cast<int64_t>(r.split) * a.chunk;
-  const int kbeg = k0 < kend ? static_cast<int>(k0) : kend;
-  if (kend - kbeg > a.chunk) kend = kbeg + a.chunk;
 
   // this lane's row of each of the RT tiles
   bf16x8 Q[RT][KS];
@@ -510,7 +591,8 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_few(AttnArgs a) {
     for (int i = threadIdx.x; i < 16 * RT * (L::kCut / 4); i += 256) {
       const int row = i / (L::kCut / 4), cc = (i % (L::kCut / 4)) * 4;
       if (row0 + row < rows) {
-        float M = -INFINITY, ll = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
+        float M = -INFINITY, ll = 0.f;
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < 4; ++w) M = fmaxf(M, mlw[(w * 16 * RT + row) * 2]);
 #pragma unroll
@@ -523,11 +605,12 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_few(AttnArgs a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum[j] = fmaf(v[j], f, sum[j]);
         }
-        store_row<kBF16, D>(a, r, row0 + row, c * L::kCut + cc, sum, M, ll);
+        store_row<kBF16, D, 16 * RT>(a, r, row0 + row, c * L::kCut + cc, sum, M, ll, whole, slot);
       }
     }
     __syncthreads();
   }
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -555,7 +638,7 @@ __device__ __forceinline__ int v_turn(int key) { return D == 64 ? ((key >> 1) & 
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-template <int D, bool WHOLE>
+template <int D, bool WHOLE, bool EVEN>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_tile(AttnArgs a) {
   using L = TileLds<D>;
   constexpr int KS = D / 16;                 // steps of 16 dims
@@ -569,22 +652,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_tile(AttnArgs a)
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int n32 = lane & 31, g = lane >> 5;
-  Rows r;
-  if (!find_rows(a, blockIdx.x, r)) return;
+  walk<128, 64, EVEN>(a, lane, [&](const Rows& r, int kbeg, int kend, bool whole, int slot) {
   const int rows = r.n * a.each;
   const int row0 = r.tile * 128;
-  if (row0 >= rows) return;
   const bool tree = a.tree != nullptr;
-
-  int kend = r.len;
-  if (!tree) {
-    const int last = (row0 + 128 < rows ? row0 + 128 : rows) - 1;
-    const int most = r.prefix + last / a.each + 1;
-    if (most < kend) kend = most > 0 ? most : 0;
-  }
-  const int64_t k0 = static_cast<int64_t>(r.split) * a.chunk;
-  const int kbeg = k0 < kend ? static_cast<int>(k0) : kend;
-  if (kend - kbeg > a.chunk) kend = kbeg + a.chunk;
 
   const int row = row0 + 32 * wave + n32;
   const int rr = row < rows ? row : rows - 1;
@@ -774,15 +845,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_tile(AttnArgs a)
         }
     }
   }
-  if (row >= rows) return;
   l += __uint_as_float(lane_xor<32>(__float_as_uint(l), lane));
+  if (row < rows)
 #pragma unroll
-  for (int d = 0; d < DT; ++d)
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float o[4] = {O[d][4 * i], O[d][4 * i + 1], O[d][4 * i + 2], O[d][4 * i + 3]};
-      store_row<kBF16, D>(a, r, row, 32 * d + 8 * i + 4 * g, o, m, l);
-    }
+      for (int i = 0; i < 4; ++i)
+        store_row<kBF16, D, 128>(a, r, row, 32 * d + 8 * i + 4 * g,
+                                 f32x4{O[d][4 * i], O[d][4 * i + 1], O[d][4 * i + 2], O[d][4 * i + 3]}, m, l, whole, slot);
+  __syncthreads();                           // nobody reads this unit's tiles when the next one's arrive
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -797,7 +869,7 @@ struct F32Lds {
   static constexpr int kBytes = 4 * 16 * RT * kRow * 4 + 4 * 16 * RT * 2 * 4;
 };
 
-template <int D, int RT>
+template <int D, int RT, bool EVEN>
 __global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
   using L = F32Lds<D, RT>;
   constexpr int KS = D / 16;                 // 16-byte pieces of a row for a lane's quarter
@@ -806,22 +878,10 @@ __global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = threadIdx.x / kWave;
   const int n16 = lane & 15, g = lane >> 4;
-  Rows r;
-  if (!find_rows(a, blockIdx.x, r)) return;
+  walk<16 * RT, 64, EVEN>(a, lane, [&](const Rows& r, int kbeg, int kend, bool whole, int slot) {
   const int rows = r.n * a.each;
   const int row0 = r.tile * 16 * RT;
-  if (row0 >= rows) return;
   const bool tree = a.tree != nullptr;
-
-  int kend = r.len;
-  if (!tree) {
-    const int last = (row0 + 16 * RT < rows ? row0 + 16 * RT : rows) - 1;
-    const int most = r.prefix + last / a.each + 1;
-    if (most < kend) kend = most > 0 ? most : 0;
-  }
-  const int64_t k0 = static_cast<int64_t>(r.split) * a.chunk;
-  const int kbeg = k0 < kend ? static_cast<int>(k0) : kend;
-  if (kend - kbeg > a.chunk) kend = kbeg + a.chunk;
 
   f32x4 Q[RT][KS];
   int itok[RT];
@@ -976,7 +1036,8 @@ __global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
     for (int i = threadIdx.x; i < 16 * RT * (L::kCut / 4); i += 256) {
       const int row = i / (L::kCut / 4), cc = (i % (L::kCut / 4)) * 4;
       if (row0 + row < rows) {
-        float M = -INFINITY, ll = 0.f, sum[4] = {0.f, 0.f, 0.f, 0.f};
+        float M = -INFINITY, ll = 0.f;
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < 4; ++w) M = fmaxf(M, mlw[(w * 16 * RT + row) * 2]);
 #pragma unroll
@@ -989,121 +1050,139 @@ __global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum[j] = fmaf(v[j], f, sum[j]);
         }
-        store_row<kF32, D>(a, r, row0 + row, c * L::kCut + cc, sum, M, ll);
+        store_row<kF32, D, 16 * RT>(a, r, row0 + row, c * L::kCut + cc, sum, M, ll, whole, slot);
       }
     }
     __syncthreads();
   }
+  });
 }
 
 // ---------------------------------------------------------------------------
-// The splits of a row joined: a block a row.  Every wave forms all weights (a
-// split a lane); D / 4 lanes take one split's sums, the groups of them in turn.
-constexpr int kMaxSplits = kWave;
-
-template <int DT, int D>
+// The parts of a row joined, where blocks shared its keys, and zeros for rows
+// without any.  A wave takes 64 dims of a row, 16 lanes a part (four parts at
+// once, four loads each on the way); WIDE: the block's four waves share them.
+template <int DT, int D, int ROWS, int STEP, bool WIDE>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  constexpr int LR = D / 4, G = 256 / LR;
-  __shared__ __align__(16) float sums[G][D];
-  const int64_t per = static_cast<int64_t>(a.new_max) * a.nq;
-  const int b = static_cast<int>(blockIdx.x / per);
-  const int64_t row = blockIdx.x % per;
-  const int begin = a.at.cu[b], end = a.at.cu[b + 1];
-  if (begin < 0 || end > a.at.N || row >= static_cast<int64_t>(end - begin) * a.nq) return;
-  const int64_t o = static_cast<int64_t>(begin) * a.nq + row;
-  const int lane = threadIdx.x & (kWave - 1), grp = threadIdx.x / LR, c0 = (threadIdx.x % LR) * 4;
-  float m = -INFINITY, l = 0.f;
-  if (lane < a.splits) {
-    const float2 w = *reinterpret_cast<const float2*>(a.ml + (o * a.splits + lane) * 2);
-    m = w.x;
-    l = w.y;
+  constexpr int kSlices = D / 64;
+  __shared__ f32x4 sums[4][16];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int64_t item = WIDE ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 4 + wave;
+  const int64_t per = static_cast<int64_t>(a.new_max) * a.nq * kSlices;
+  if (item >= per * a.at.B) return;
+  const int b = static_cast<int>(item / per), slice = static_cast<int>(item % kSlices);
+  const int idx = static_cast<int>((item % per) / kSlices);
+  const int h = idx / (a.new_max * a.each), row = idx % (a.new_max * a.each);
+  Rows r;
+  if (!sequence(a, b, r) || row >= r.n * a.each) return;
+  const int steps = steps_of<STEP>(r);
+  const int64_t o = ((r.begin + static_cast<int64_t>(row / a.each)) * a.nq + h * a.each + row % a.each) * D + slice * 64 + (lane & 15) * 4;
+  if (steps == 0) {
+    if (lane < 16 && (!WIDE || wave == 0)) put_row<DT>(a.out, o, f32x4{0.f, 0.f, 0.f, 0.f}, 0.f);
+    return;
   }
-  float M = m;
-  for (int s = 1; s < kWave; s <<= 1) M = fmaxf(M, __shfl_xor(M, s));
-  const float f = part_weight(m, l, M);
-  float total = l * f;
-  for (int s = 1; s < kWave; s <<= 1) total += __shfl_xor(total, s);
-  const float* part = a.part + o * a.splits * D + c0;
+  const int share = a.shares[0], before = b > 0 ? a.shares[b] : 0;
+  const int w0 = before + (h * tiles_of<ROWS>(a, r) + row / ROWS) * steps;
+  const int k0 = w0 / share, k1 = (w0 + steps - 1) / share;
+  if (k0 == k1) return;                      // one block had all of it
+  const int parts = k1 - k0 + 1;
+  const auto place = [&](int p) {            // the first block's part lies in slot 1 unless its share begins with it
+    return (static_cast<int64_t>(k0 + p) * 2 + (p == 0 && w0 != k0 * share ? 1 : 0)) * ROWS + row % ROWS;
+  };
+  float M = -INFINITY;
+  for (int p = lane; p < parts; p += kWave) M = fmaxf(M, a.ml[place(p) * 2]);
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) M = fmaxf(M, __shfl_xor(M, d));
   f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-  for (int s0 = 0; s0 < a.splits; s0 += 4 * G) {
+  float l = 0.f;
+  constexpr int kGroups = WIDE ? 16 : 4;
+  for (int p0 = (WIDE ? wave * 4 : 0) + (lane >> 4); p0 < parts; p0 += 4 * kGroups) {
     f32x4 v[4];
-    float w[4];
+    float2 ml[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int s = s0 + G * i + grp;
-      w[i] = __shfl(l == 0.f ? -1.f : f, s < kWave ? s : 0);   // a split without keys has written no sums
-      if (s >= a.splits) w[i] = -1.f;
-      v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (w[i] != -1.f) v[i] = *reinterpret_cast<const f32x4*>(part + static_cast<int64_t>(s) * D);
+      const int p = p0 + kGroups * i < parts ? p0 + kGroups * i : p0;
+      const int64_t at = place(p);
+      ml[i] = *reinterpret_cast<const float2*>(a.ml + at * 2);
+      v[i] = *reinterpret_cast<const f32x4*>(a.part + at * D + slice * 64 + (lane & 15) * 4);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (w[i] != -1.f)
+      if (p0 + kGroups * i < parts && ml[i].y != 0.f) {
+        const float f = part_weight(ml[i].x, ml[i].y, M);
+        l = fmaf(ml[i].y, f, l);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum[j] = fmaf(v[i][j], w[i], sum[j]);
+        for (int j = 0; j < 4; ++j) sum[j] = fmaf(v[i][j], f, sum[j]);
+      }
   }
-  *reinterpret_cast<f32x4*>(&sums[grp][c0]) = sum;
-  __syncthreads();
-  if (grp != 0) return;
 #pragma unroll
-  for (int i = 1; i < G; ++i) sum += *reinterpret_cast<const f32x4*>(&sums[i][c0]);
-  const float inv = total == 0.f ? 0.f : 1.0f / total;
-  if constexpr (DT == kF32) {
-    *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + o * D + c0) = sum * inv;
-  } else {
-    uint2 w;
-    w.x = f32_to_bf16(sum[0] * inv) | (static_cast<uint32_t>(f32_to_bf16(sum[1] * inv)) << 16);
-    w.y = f32_to_bf16(sum[2] * inv) | (static_cast<uint32_t>(f32_to_bf16(sum[3] * inv)) << 16);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o * D + c0) = w;
+  for (int j = 0; j < 4; ++j) sum[j] = xor_add(sum[j], lane);
+  l = xor_add(l, lane);
+  if constexpr (WIDE) {
+    __shared__ float ls[4];
+    if (lane < 16) sums[wave][lane] = sum;
+    if (lane == 0) ls[wave] = l;
+    __syncthreads();
+    sum = sums[0][lane & 15] + sums[1][lane & 15] + sums[2][lane & 15] + sums[3][lane & 15];
+    l = ls[0] + ls[1] + ls[2] + ls[3];
+    if (wave != 0) return;
   }
+  if (lane < 16) put_row<DT>(a.out, o, sum, l);
 }
 
 // ---------------------------------------------------------------------------
 struct AttnPlan {
-  int rt;               // 16 rows a block times this
+  int rt;               // bf16: 1 or 2 times 16 rows a block (few), 8 (tiles); fp32: 1 or 2
   int tiles;            // row tiles a sequence and key head
-  int splits, chunk;
-  int64_t units, blocks;
-  size_t part, total;   // workspace: sums, then maxima and denominators
+  bool even, wide;
+  int64_t blocks, join;
+  size_t part, ml, total;   // workspace: sums, maxima and denominators, shares
 };
 
 int attn_plan(const attn_desc* d, int32_t B, int32_t N, int32_t new_max, int32_t len_max, AttnPlan* p) {
   if (B < 0 || B > (1 << 16) || N < 0 || N > (1 << 20)) return attn_bad("B=%lld must be in [0, 2^16], N=%lld in [0, 2^20]", B, N);
   if (new_max < 0 || len_max < 0 || len_max > 0x7ffff000) return attn_bad("new_max=%lld and len_max=%lld must not be negative or too large", new_max, len_max);
-  const int each = d->n_q_heads / d->n_kv_heads;
+  const int each = d->n_q_heads / d->n_kv_heads, D = d->head_dim;
   const int most = new_max < N ? new_max : N;
   const int64_t rows = static_cast<int64_t>(most) * each;
-  p->rt = d->dtype == MOE_F32 ? (rows <= 16 ? 1 : 2) : (rows <= 16 ? 1 : (rows <= 32 && d->head_dim < 256 ? 2 : 8));
+  const bool f32 = d->dtype == MOE_F32;
+  p->rt = f32 ? (rows <= 16 || D == 256 ? 1 : 2) : (rows <= 16 ? 1 : (rows <= 32 && D < 256 ? 2 : 8));
   p->tiles = static_cast<int>((rows + 16 * p->rt - 1) / (16 * p->rt));
   if (p->tiles < 1) p->tiles = 1;
-  const int step = d->dtype == MOE_F32 || p->rt == 8 || d->head_dim == 256 ? 64 : 128;   // keys a block takes at once
+  const int step = f32 || p->rt == 8 || D == 256 ? 64 : 128;   // keys a block takes at once
+  // Even shares go to as many blocks as the chip holds at once, by their
+  // registers and LDS.  64 contexts of 100 to 32768 tokens, 16 heads of 256: half as
+  // many blocks 176 us, these 151, twice as many 155; a block for each (sequence, key
+  // head) with its keys cut in runs of 2048 181.
+  const int fit = f32 ? (D == 64 ? (p->rt == 1 ? 3 : 2) : (D == 128 && p->rt == 1 ? 2 : 1))
+                      : (p->rt == 1 ? (D == 64 ? 4 : 2) : (D == 256 || (D == 128 && p->rt == 2) ? 1 : 2));
+  const int64_t slots = 256 * fit;
   const int64_t units = static_cast<int64_t>(B) * d->n_kv_heads * p->tiles;
-  static const int64_t target = getenv("ATTN_T") ? atoll(getenv("ATTN_T")) : 1024;
-  int64_t splits = units > 0 ? target / units : 1;
-  if (splits > kMaxSplits) splits = kMaxSplits;
-  if (splits < 1) splits = 1;
-  int64_t chunk = (len_max + splits - 1) / splits;
-  chunk = (chunk + step - 1) / step * step;
-  if (chunk < step) chunk = step;
-  p->chunk = static_cast<int>(chunk);
-  p->splits = static_cast<int>((len_max + chunk - 1) / chunk);
-  if (p->splits < 1) p->splits = 1;
-  p->units = static_cast<int64_t>(B) * d->n_kv_heads * p->splits;
-  p->blocks = p->units * p->tiles;
-  const int64_t join = p->splits > 1 ? static_cast<int64_t>(B) * most * d->n_q_heads : 0;
-  if (p->blocks >= (int64_t(1) << 24) || join >= (int64_t(1) << 24)) return attn_bad("B=%lld sequences of new_max=%lld tokens are too many blocks for one launch", B, new_max);
-  p->part = 0;
-  p->total = 0;
-  if (p->splits > 1) {
-    p->part = static_cast<size_t>(N) * d->n_q_heads * p->splits * d->head_dim * 4;
-    p->total = p->part + static_cast<size_t>(N) * d->n_q_heads * p->splits * 8;
+  const int64_t steps = (static_cast<int64_t>(len_max) + step - 1) / step;
+  p->even = steps > 4 && units * steps < (int64_t(1) << 31) && (p->tiles == 1 || units < slots);
+  p->blocks = units;
+  p->join = 0;
+  p->part = p->ml = p->total = 0;
+  p->wide = false;
+  if (p->even) {
+    if (units * steps < slots) p->blocks = units * steps;
+    else p->blocks = slots;
+    p->wide = p->blocks > 32 * units;
+    const int64_t items = static_cast<int64_t>(B) * rows * d->n_kv_heads * (D / 64);
+    p->join = p->wide ? items : (items + 3) / 4;
+    const size_t at = static_cast<size_t>(p->blocks) * 2 * 16 * p->rt;
+    p->part = at * D * 4;
+    p->ml = at * 8;
+    p->total = p->part + p->ml + (static_cast<size_t>(B) + 1) * 4;
   }
+  if (p->blocks >= (int64_t(1) << 24) || p->join >= (int64_t(1) << 24))
+    return attn_bad("B=%lld sequences of new_max=%lld tokens are too many blocks for one launch", B, new_max);
   return MOE_OK;
 }
 
 // Launch with dynamic LDS, whose size is set once per kernel and device.
 template <void (*KERNEL)(AttnArgs), int BYTES>
-bool launch_lds(const AttnArgs& a, dim3 grid, hipStream_t s) {
+bool launch_lds(const AttnArgs& a, hipStream_t s) {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) return false;
@@ -1113,32 +1192,47 @@ bool launch_lds(const AttnArgs& a, dim3 grid, hipStream_t s) {
       return false;
     done.fetch_or(bit, std::memory_order_relaxed);
   }
-  launch_kernel(KERNEL, grid, dim3(256), BYTES, s, a);
+  launch_kernel(KERNEL, dim3(a.blocks), dim3(256), BYTES, s, a);
   return true;
 }
 
-template <int D, bool WHOLE>
-bool launch_bf16(const AttnArgs& a, int rt, dim3 grid, hipStream_t s) {
-  if (rt == 1) return launch_lds<k_attn_few<D, 1, WHOLE>, FewLds<D, 1>::kBytes>(a, grid, s);
+template <int D, bool WHOLE, bool EVEN>
+bool launch_bf16(const AttnArgs& a, int rt, hipStream_t s) {
+  if (rt == 1) return launch_lds<k_attn_few<D, 1, WHOLE, EVEN>, FewLds<D, 1>::kBytes>(a, s);
   if constexpr (D < 256)
-    if (rt == 2) return launch_lds<k_attn_few<D, 2, WHOLE>, FewLds<D, 2>::kBytes>(a, grid, s);
-  return launch_lds<k_attn_tile<D, WHOLE>, TileLds<D>::kBytes>(a, grid, s);
+    if (rt == 2) return launch_lds<k_attn_few<D, 2, WHOLE, EVEN>, FewLds<D, 2>::kBytes>(a, s);
+  return launch_lds<k_attn_tile<D, WHOLE, EVEN>, TileLds<D>::kBytes>(a, s);
+}
+
+template <int D, bool EVEN>
+bool launch_keys(const AttnArgs& a, int rt, int dtype, hipStream_t s) {
+  if (dtype == MOE_F32) {
+    if (rt == 1) launch_kernel(k_attn_f32<D, 1, EVEN>, dim3(a.blocks), dim3(256), 0, s, a);
+    else if constexpr (D < 256) launch_kernel(k_attn_f32<D, 2, EVEN>, dim3(a.blocks), dim3(256), 0, s, a);
+    return true;
+  }
+  const bool whole = a.at.shift >= (rt == 8 && D == 64 ? 5 : 4);
+  return whole ? launch_bf16<D, true, EVEN>(a, rt, s) : launch_bf16<D, false, EVEN>(a, rt, s);
+}
+
+template <int DT, int D, int ROWS, int STEP>
+void launch_join(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+  const dim3 grid(static_cast<uint32_t>(p.join));
+  if (p.wide) launch_kernel(k_attn_join<DT, D, ROWS, STEP, true>, grid, dim3(256), 0, s, a);
+  else launch_kernel(k_attn_join<DT, D, ROWS, STEP, false>, grid, dim3(256), 0, s, a);
 }
 
 template <int D>
 bool launch_attn_d(const AttnArgs& a, const AttnPlan& p, int dtype, hipStream_t s) {
-  const dim3 grid(static_cast<uint32_t>(p.blocks)), block(256);
+  if (!(p.even ? launch_keys<D, true>(a, p.rt, dtype, s) : launch_keys<D, false>(a, p.rt, dtype, s))) return false;
+  if (!p.even) return true;
   if (dtype == MOE_F32) {
-    if (p.rt == 1) launch_kernel(k_attn_f32<D, 1>, grid, block, 0, s, a);
-    else launch_kernel(k_attn_f32<D, 2>, grid, block, 0, s, a);
+    if (p.rt == 1) launch_join<kF32, D, 16, 64>(a, p, s);
+    else if constexpr (D < 256) launch_join<kF32, D, 32, 64>(a, p, s);
   } else {
-    const bool whole = a.at.shift >= (p.rt == 8 && D == 64 ? 5 : 4);
-    if (!(whole ? launch_bf16<D, true>(a, p.rt, grid, s) : launch_bf16<D, false>(a, p.rt, grid, s))) return false;
-  }
-  if (p.splits > 1) {
-    const dim3 jg(static_cast<uint32_t>(static_cast<int64_t>(a.new_max) * a.nq * a.at.B));
-    if (dtype == MOE_F32) launch_kernel(k_attn_join<kF32, D>, jg, block, 0, s, a);
-    else launch_kernel(k_attn_join<kBF16, D>, jg, block, 0, s, a);
+    if (p.rt == 1) launch_join<kBF16, D, 16, D == 256 ? 64 : 128>(a, p, s);
+    else if (p.rt == 8) launch_join<kBF16, D, 128, 64>(a, p, s);
+    else if constexpr (D < 256) launch_join<kBF16, D, 32, 128>(a, p, s);
   }
   return true;
 }
@@ -1194,15 +1288,14 @@ extern "C" int attn_forward(const attn_desc* d, int32_t B, int32_t N, int32_t ne
   a.out = out;
   a.part = static_cast<float*>(workspace);
   a.ml = p.total ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.part) : nullptr;
+  a.shares = p.total ? reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + p.part + p.ml) : nullptr;
   a.nq = d->n_q_heads;
   a.nkv = d->n_kv_heads;
   a.each = a.nq / a.nkv;
   a.new_max = new_max < N ? new_max : N;
   a.len_max = len_max;
   a.tiles = p.tiles;
-  a.units = p.units;
-  a.splits = p.splits;
-  a.chunk = p.chunk;
+  a.blocks = static_cast<int>(p.blocks);
   a.scale2 = d->scale * 1.4426950408889634f;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool sent = d->head_dim == 64    ? launch_attn_d<64>(a, p, d->dtype, s)
