@@ -14,6 +14,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 
@@ -42,7 +43,8 @@ struct AttnArgs {
   int new_max, len_max;
   int tiles;            // row tiles a sequence and key head, at most
   int blocks;
-  float scale2;         // scale log2 e
+  float scale2;         // |scale| log2 e, not 0
+  uint32_t flip;        // the sign bits of q, set where scale is negative
 };
 
 // One unit of work: a tile of rows of one key head of one sequence.
@@ -207,6 +209,10 @@ __device__ __forceinline__ uint32_t sees(bool tree, uint64_t mask, int i, int j)
   return static_cast<uint32_t>(j < 0) | (tree ? bit : static_cast<uint32_t>(j <= i));
 }
 
+// A row's maximum may be exceeded by this much (in powers of two) before its
+// sums are scaled again: weights of up to 2^8 lose nothing in fp32 or bf16.
+constexpr float kSlack = 8.f;
+
 __device__ __forceinline__ float xor_max(float x, int lane) {
   x = fmaxf(x, __uint_as_float(lane_xor<16>(__float_as_uint(x), lane)));
   return fmaxf(x, __uint_as_float(lane_xor<32>(__float_as_uint(x), lane)));
@@ -297,8 +303,12 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, const Rows& r, int 
   put_row<DT>(a.out, o * D + c0, sum, l);
 }
 
+// What sums are scaled by when the maximum grows from m to M; not 0, times which
+// an infinite sum would be NaN.
+__device__ __forceinline__ float grown(float m, float M) { return M == -INFINITY ? 1.f : fmaxf(__builtin_amdgcn_exp2f(m - M), 1e-37f); }
+
 // Weight of a part whose maximum is m among parts whose largest is M.
-__device__ __forceinline__ float part_weight(float m, float l, float M) { return l == 0.f ? 0.f : __builtin_amdgcn_exp2f(m - M); }
+__device__ __forceinline__ float part_weight(float m, float l, float M) { return l == 0.f ? 0.f : grown(m, M); }
 
 // ---------------------------------------------------------------------------
 // Few rows: a block takes 16 RT rows of a key head and a run of its keys, its
@@ -344,6 +354,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_few(AttnArgs a) {
   const int rows = r.n * a.each;
   const int row0 = r.tile * 16 * RT;
   const bool tree = a.tree != nullptr;
+  const int clear = r.prefix + (tree ? 0 : row0 / a.each + 1);   // keys that all rows see
 
   // this lane's row of each of the RT tiles
   bf16x8 Q[RT][KS];
@@ -358,7 +369,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_few(AttnArgs a) {
     mask[t] = tree ? a.tree[token] : 0;
     const uint16_t* q = static_cast<const uint16_t*>(a.q) + (token * a.nq + r.h * a.each + rr % a.each) * D;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) Q[t][s] = __builtin_bit_cast(bf16x8, load16(q + 32 * s + 8 * g));
+    for (int s = 0; s < KS; ++s) Q[t][s] = __builtin_bit_cast(bf16x8, load16(q + 32 * s + 8 * g) ^ a.flip);
   }
   f32x4 O[RT][DT];
   float m[RT], l[RT];
@@ -440,7 +451,22 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_few(AttnArgs a) {
     look(kt + kStep);
   }
   for (; kt < kend; kt += kStep) {
-    const uint8_t* vt = part + stage * L::kV;
+    uint8_t* vt = part + stage * L::kV;
+    const auto value = [&](int d) {          // rows 4 g + r, then 16 + 4 g + r (or again); this lane names row (n16 / 4), columns 4 (n16 % 4) ..
+      bf16x8 V;
+#pragma unroll
+      for (int x = 0; x < X; ++x) {
+        const int row = 16 * x + 4 * g + (n16 >> 2);
+        const int col = 2 * d + ((n16 & 3) >> 1);
+        const bf16x4 v = read_tr(vt + row * D * 2 + ((col ^ turn(row)) << 4) + (n16 & 1) * 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          V[4 * x + i] = v[i];
+          if constexpr (X == 1) V[4 + i] = v[i];
+        }
+      }
+      return V;
+    };
     wait_loads();
     f32x4 S[RT][X];
 #pragma unroll
@@ -461,8 +487,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_few(AttnArgs a) {
     }
 
     // keys that some row of the tile does not see, or that are not there
-    const bool careful = !WHOLE || none != 0 || kt + kKeys > kend || kt + kKeys > r.prefix;
-    bool bad = false;                        // such a tile holds a value that is not finite
+    const bool careful = !WHOLE || none != 0 || kt + kKeys > kend || kt + kKeys > clear;
     uint32_t seen[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) seen[t] = 0xffu;
@@ -495,7 +520,24 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_few(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) big = __builtin_elementwise_max(big, __builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu));
       }
-      bad = __ballot(big[0] >= 0x7f80u || big[1] >= 0x7f80u) != 0;
+      if (__ballot(big[0] >= 0x7f80u || big[1] >= 0x7f80u)) {
+        // values that are not finite: counted by the rows that see them, then taken out of the tile
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            f32x4 c = {0.f, 0.f, 0.f, 0.f};
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd_part(value(d)), bits_bf16(seen[t]), c, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) O[t][d][i] += odd_sum(c[i]);
+          }
+        wave_sync_lds();
+        for (int j = 0; j < VL; ++j) {
+          u32x4* w = reinterpret_cast<u32x4*>(vt + j * 1024 + lane * 16);
+          *w = __builtin_bit_cast(u32x4, finite_part(__builtin_bit_cast(bf16x8, *w)));
+        }
+        wave_sync_lds();
+      }
     }
     // P in two bf16 parts: one alone would add an error as large as the output's
     // own rounding.  With 16 keys a step both go into one product, V twice.
@@ -507,14 +549,13 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_few(AttnArgs a) {
       for (int x = 0; x < X; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          S[t][x][i] *= a.scale2;
           if (careful) S[t][x][i] = ((seen[t] >> (4 * x + i)) & 1u) ? S[t][x][i] : -INFINITY;
           mx = fmaxf(mx, S[t][x][i]);
         }
-      mx = xor_max(mx, lane);
-      if (__ballot(mx > m[t])) {             // some row's maximum grows
+      mx = xor_max(mx, lane) * a.scale2;
+      if (__ballot(mx > m[t] + kSlack)) {    // some row's maximum grows
         const float mn = fmaxf(m[t], mx);
-        const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[t] - mn);
+        const float f = grown(m[t], mn);
         m[t] = mn;
         l[t] *= f;
 #pragma unroll
@@ -526,7 +567,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_few(AttnArgs a) {
       for (int x = 0; x < X; ++x)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float p = __builtin_amdgcn_exp2f(S[t][x][i] - mu);
+          const float p = __builtin_amdgcn_exp2f(fmaf(S[t][x][i], a.scale2, -mu));
           add += p;
           const __bf16 hi = static_cast<__bf16>(p), lo = static_cast<__bf16>(p - static_cast<float>(hi));
           P[t][4 * x + i] = hi;
@@ -537,29 +578,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_few(AttnArgs a) {
     }
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
-      // rows 4 g + r, then 16 + 4 g + r; this lane names row (n16 / 4), columns 4 (n16 % 4) ..
-      bf16x8 V;
-#pragma unroll
-      for (int x = 0; x < X; ++x) {
-        const int row = 16 * x + 4 * g + (n16 >> 2);
-        const int col = 2 * d + ((n16 & 3) >> 1);
-        const bf16x4 v = read_tr(vt + row * D * 2 + ((col ^ turn(row)) << 4) + (n16 & 1) * 8);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          V[4 * x + i] = v[i];
-          if constexpr (X == 1) V[4 + i] = v[i];
-        }
-      }
-      if (bad) {
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          f32x4 c = {0.f, 0.f, 0.f, 0.f};
-          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(odd_part(V), bits_bf16(seen[t]), c, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) O[t][d][i] += odd_sum(c[i]);
-        }
-        V = finite_part(V);
-      }
+      const bf16x8 V = value(d);
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         if constexpr (X == 2) O[t][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(V, Plo[t], O[t][d], 0, 0, 0);
@@ -656,6 +675,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_tile(AttnArgs a)
   const int rows = r.n * a.each;
   const int row0 = r.tile * 128;
   const bool tree = a.tree != nullptr;
+  const int clear = r.prefix + (tree ? 0 : row0 / a.each + 1);   // keys that all rows see
 
   const int row = row0 + 32 * wave + n32;
   const int rr = row < rows ? row : rows - 1;
@@ -667,8 +687,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_tile(AttnArgs a)
   {
     const uint16_t* q = static_cast<const uint16_t*>(a.q) + (token * a.nq + r.h * a.each + rr % a.each) * D;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) Q[s] = __builtin_bit_cast(bf16x8, load16(q + 16 * s + 8 * g));
+    for (int s = 0; s < KS; ++s) Q[s] = __builtin_bit_cast(bf16x8, load16(q + 16 * s + 8 * g) ^ a.flip);
   }
+  // 256 dims: Q in accumulation registers, so that O, which is scaled, stays in the others
+  if constexpr (D == 256)
+#pragma unroll
+    for (int s = 0; s < KS; ++s) asm volatile("" : "+a"(Q[s]));
   f32x16 O[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d)
@@ -747,10 +771,33 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_tile(AttnArgs a)
       gone = missing();
       look(kt + 128);
     }
-    if (idle) continue;
-    const bool careful = !WHOLE || none != 0 || kt + 64 > kend || kt + 64 > r.prefix;
-    bool bad = false;                        // such a tile holds a value that is not finite
+    const bool careful = !WHOLE || none != 0 || kt + 64 > kend || kt + 64 > clear;
+    uint32_t seen[2] = {0xffffu, 0xffffu};   // of 32 keys each, bit i: key 8 (i / 4) + 4 g + i % 4
+    const auto value = [&](int key0, int d) {    // keys key0 + 8 y + 4 g + 0 .. 3, dims 32 d + 16 (lane / 16 % 2) ..
+      bf16x8 V;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int key = key0 + 8 * y + 4 * g + ((lane & 15) >> 2);
+        const int col = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+        const bf16x4 v = read_tr(Vt + key * D * 2 + ((col ^ v_turn<D>(key)) << 4) + (lane & 1) * 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) V[4 * y + i] = v[i];
+      }
+      return V;
+    };
     if (careful) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        seen[x] = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int at = kt + 32 * x + 8 * (i >> 2) + 4 * g + (i & 3);
+          uint32_t in = static_cast<uint32_t>(at < kend);
+          if constexpr (WHOLE) in &= ~(none >> ((32 * x + 8 * (i >> 2)) / kRun));
+          else in &= static_cast<uint32_t>(there(a, page_at(a, r.b, at < kend ? at : kend - 1)));
+          seen[x] |= (in & sees(tree, mask, itok, at - r.prefix)) << i;
+        }
+      }
       typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
       u16x2 big = {0, 0};
       for (int i = lane; i < 64 * kPer; i += kWave) {
@@ -758,8 +805,31 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_tile(AttnArgs a)
 #pragma unroll
         for (int j = 0; j < 4; ++j) big = __builtin_elementwise_max(big, __builtin_bit_cast(u16x2, w[j] & 0x7fff7fffu));
       }
-      bad = __ballot(big[0] >= 0x7f80u || big[1] >= 0x7f80u) != 0;
+      if (__ballot(big[0] >= 0x7f80u || big[1] >= 0x7f80u)) {
+        // values that are not finite (all four waves see them): counted by the
+        // rows that see them, then taken out of the tile
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            f32x16 c;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) c[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(odd_part(value(32 * x + 16 * j, d)), bits_bf16(seen[x] >> (8 * j)), c, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) O[d][i] += odd_sum(c[i]);
+          }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 64 * kPer; i += 256) {
+          u32x4* w = reinterpret_cast<u32x4*>(const_cast<uint8_t*>(Vt) + i * 16);
+          *w = __builtin_bit_cast(u32x4, finite_part(__builtin_bit_cast(bf16x8, *w)));
+        }
+        __syncthreads();
+      }
     }
+    if (idle) continue;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {            // 32 keys each
       f32x16 S;
@@ -772,29 +842,17 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_tile(AttnArgs a)
         S = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kv), Q[s], S, 0, 0, 0);
       }
       __builtin_amdgcn_sched_barrier(0);     // or the reads of V are moved up until registers run out
-      uint32_t seen = 0xffffu;               // bit i: key 32 x + 8 (i / 4) + 4 g + i % 4
       if (careful) {
-        seen = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int at = kt + 32 * x + 8 * (i >> 2) + 4 * g + (i & 3);
-          uint32_t in = static_cast<uint32_t>(at < kend);
-          if constexpr (WHOLE) in &= ~(none >> ((32 * x + 8 * (i >> 2)) / kRun));
-          else in &= static_cast<uint32_t>(there(a, page_at(a, r.b, at < kend ? at : kend - 1)));
-          seen |= (in & sees(tree, mask, itok, at - r.prefix)) << i;
-        }
+        for (int i = 0; i < 16; ++i) S[i] = ((seen[x] >> i) & 1u) ? S[i] : -INFINITY;
       }
       float mx = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        S[i] *= a.scale2;
-        if (careful) S[i] = ((seen >> i) & 1u) ? S[i] : -INFINITY;
-        mx = fmaxf(mx, S[i]);
-      }
-      mx = fmaxf(mx, __uint_as_float(lane_xor<32>(__float_as_uint(mx), lane)));
-      if (__ballot(mx > m)) {
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, S[i]);
+      mx = fmaxf(mx, __uint_as_float(lane_xor<32>(__float_as_uint(mx), lane))) * a.scale2;
+      if (__ballot(mx > m + kSlack)) {
         const float mn = fmaxf(m, mx);
-        const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+        const float f = grown(m, mn);
         m = mn;
         l *= f;
 #pragma unroll
@@ -804,45 +862,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_tile(AttnArgs a)
       bf16x8 P[2];                           // 16 keys each, in the order of the lane's S
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float p = __builtin_amdgcn_exp2f(S[i] - mu);
+        const float p = __builtin_amdgcn_exp2f(fmaf(S[i], a.scale2, -mu));
         l += p;
         P[i >> 3][i & 7] = static_cast<__bf16>(p);
       }
-      const auto value = [&](int d, int j) { // keys 32 x + 16 j + 8 y + 4 g + 0 .. 3, dims 32 d + 16 (lane / 16 % 2) ..
-        bf16x8 V;
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int key = 32 * x + 16 * j + 8 * y + 4 * g + ((lane & 15) >> 2);
-          const int col = 4 * d + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-          const bf16x4 v = read_tr(Vt + key * D * 2 + ((col ^ v_turn<D>(key)) << 4) + (lane & 1) * 8);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) V[4 * y + i] = v[i];
-        }
-        return V;
-      };
       __builtin_amdgcn_sched_barrier(0);
-      if (bad) {
-        // O d by d, with little held at once: this is rare
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          f32x16 c;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) c[i] = 0.f;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(odd_part(value(d, j)), bits_bf16(seen >> (8 * j)), c, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) O[d][i] += odd_sum(c[i]);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          bf16x8 V = value(d, j);
-          if (bad) V = finite_part(V);
-          O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(V, P[j], O[d], 0, 0, 0);
-        }
+        for (int j = 0; j < 2; ++j) O[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(value(32 * x + 16 * j, d), P[j], O[d], 0, 0, 0);
     }
   }
   l += __uint_as_float(lane_xor<32>(__float_as_uint(l), lane));
@@ -882,6 +910,7 @@ __global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
   const int rows = r.n * a.each;
   const int row0 = r.tile * 16 * RT;
   const bool tree = a.tree != nullptr;
+  const int clear = r.prefix + (tree ? 0 : row0 / a.each + 1);   // keys that all rows see
 
   f32x4 Q[RT][KS];
   int itok[RT];
@@ -895,7 +924,7 @@ __global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
     mask[t] = tree ? a.tree[token] : 0;
     const float* q = static_cast<const float*>(a.q) + (token * a.nq + r.h * a.each + rr % a.each) * D;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) Q[t][s] = *reinterpret_cast<const f32x4*>(q + 16 * s + 4 * g);
+    for (int s = 0; s < KS; ++s) Q[t][s] = __builtin_bit_cast(f32x4, load16(q + 16 * s + 4 * g) ^ a.flip);
   }
   f32x4 O[RT][DQ][4];                        // tile (q, i): dims 64 q + 4 m + i
   float m[RT], l[RT];
@@ -928,7 +957,7 @@ __global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
 #pragma unroll
       for (int d = 0; d < DQ; ++d) V[i][d] = *reinterpret_cast<const f32x4*>(vp + 64 * d + 4 * n16);
     }
-    const bool careful = there != 0xffffu || kt + 16 > kend || kt + 16 > r.prefix;
+    const bool careful = there != 0xffffu || kt + 16 > kend || kt + 16 > clear;
     bool bad = false;
     if (careful) {
       uint32_t big = 0;
@@ -963,13 +992,13 @@ __global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
       float mx = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        S[i] = (seen >> i) & 1u ? S[i] * a.scale2 : -INFINITY;
+        if (careful) S[i] = (seen >> i) & 1u ? S[i] : -INFINITY;
         mx = fmaxf(mx, S[i]);
       }
-      mx = xor_max(mx, lane);
-      if (__ballot(mx > m[t])) {
+      mx = xor_max(mx, lane) * a.scale2;
+      if (__ballot(mx > m[t] + kSlack)) {
         const float mn = fmaxf(m[t], mx);
-        const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[t] - mn);
+        const float f = grown(m[t], mn);
         m[t] = mn;
         l[t] *= f;
 #pragma unroll
@@ -981,7 +1010,7 @@ __global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
       f32x4 p;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(S[i] - mu);
+        p[i] = __builtin_amdgcn_exp2f(fmaf(S[i], a.scale2, -mu));
         l[t] += p[i];
       }
 #pragma unroll
@@ -1296,7 +1325,9 @@ extern "C" int attn_forward(const attn_desc* d, int32_t B, int32_t N, int32_t ne
   a.len_max = len_max;
   a.tiles = p.tiles;
   a.blocks = static_cast<int>(p.blocks);
-  a.scale2 = d->scale * 1.4426950408889634f;
+  // a positive factor, so that the largest product is the largest score: q takes the sign
+  a.scale2 = fmaxf(fabsf(d->scale) * 1.4426950408889634f, FLT_MIN);
+  a.flip = d->scale < 0.f ? (d->dtype == MOE_F32 ? 0x80000000u : 0x80008000u) : 0u;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool sent = d->head_dim == 64    ? launch_attn_d<64>(a, p, d->dtype, s)
                     : d->head_dim == 128 ? launch_attn_d<128>(a, p, d->dtype, s)
