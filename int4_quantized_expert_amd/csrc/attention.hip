@@ -898,7 +898,7 @@ struct F32Lds {
 };
 
 template <int D, int RT, bool EVEN>
-__global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
+__global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_f32(AttnArgs a) {
   using L = F32Lds<D, RT>;
   constexpr int KS = D / 16;                 // 16-byte pieces of a row for a lane's quarter
   constexpr int DQ = D / 64;                 // groups of 64 dims
@@ -948,6 +948,16 @@ __global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
     f32x4 K[KS];
 #pragma unroll
     for (int s = 0; s < KS; ++s) K[s] = *reinterpret_cast<const f32x4*>(kp + 16 * s + 4 * g);
+    f32x4 S[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(K[s][i], Q[t][s][i], S[t], 0, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);       // V takes the registers of K: a second block on the CU hides more than an earlier request
     f32x4 V[4][DQ];                          // keys 4 g + r, dims 64 q + 4 n16 ..
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -974,11 +984,6 @@ __global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
     }
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      f32x4 S = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) S = __builtin_amdgcn_mfma_f32_16x16x4f32(K[s][i], Q[t][s][i], S, 0, 0, 0);
       uint32_t seen = 0xfu;
       if (careful) {
         seen = 0;
@@ -992,8 +997,8 @@ __global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
       float mx = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (careful) S[i] = (seen >> i) & 1u ? S[i] : -INFINITY;
-        mx = fmaxf(mx, S[i]);
+        if (careful) S[t][i] = (seen >> i) & 1u ? S[t][i] : -INFINITY;
+        mx = fmaxf(mx, S[t][i]);
       }
       mx = xor_max(mx, lane) * a.scale2;
       if (__ballot(mx > m[t] + kSlack)) {
@@ -1010,7 +1015,7 @@ __global__ __launch_bounds__(256) void k_attn_f32(AttnArgs a) {
       f32x4 p;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(fmaf(S[i], a.scale2, -mu));
+        p[i] = __builtin_amdgcn_exp2f(fmaf(S[t][i], a.scale2, -mu));
         l[t] += p[i];
       }
 #pragma unroll
@@ -1183,8 +1188,8 @@ int attn_plan(const attn_desc* d, int32_t B, int32_t N, int32_t new_max, int32_t
   // registers and LDS.  64 contexts of 100 to 32768 tokens, 16 heads of 256: half as
   // many blocks 176 us, these 151, twice as many 155; a block for each (sequence, key
   // head) with its keys cut in runs of 2048 181.
-  const int fit = f32 ? (D == 64 ? (p->rt == 1 ? 3 : 2) : (D == 128 && p->rt == 1 ? 2 : 1))
-                      : (p->rt == 1 ? (D == 64 ? 4 : 2) : (D == 256 || (D == 128 && p->rt == 2) ? 1 : 2));
+  const int fit = f32 ? (p->rt == 1 ? (D == 64 ? 4 : (D == 128 ? 3 : 2)) : (D == 64 ? 2 : 1))
+                      : (D == 64 && p->rt < 8 ? 5 - p->rt : (D == 256 && p->rt == 8 ? 1 : 2));
   const int64_t slots = 256 * fit;
   const int64_t units = static_cast<int64_t>(B) * d->n_kv_heads * p->tiles;
   const int64_t steps = (static_cast<int64_t>(len_max) + step - 1) / step;
