@@ -9,10 +9,17 @@
 //   X = V - diag(e) K S^T,  O = diag(f) Q S^T + (O-matrix) X,
 //   Zt = (Z-matrix) X,      S <- g_C S + Zt^T K
 // with K and Q as they are stored (their norms are in the factors).
+//
+// Single precision on the bf16 matrix units.  An fp32 value is the sum of three
+// bf16 (8 bits each, 24 together); K and Q are bf16 as they come.  So K S^T takes
+// three products, and (Z-matrix) X the six whose terms are above 2^-24: 1 1, 1 2,
+// 2 1, 1 3, 2 2, 3 1.  That is 5 to 10 times the rate of the fp32 instruction,
+// which fp32 activations run on.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
 #include <cstdio>
+#include <type_traits>
 
 #include "device_common.h"
 #include "gdn_chunk.h"
@@ -27,10 +34,16 @@ constexpr int kRowsS = 16;                    // state rows a block
 constexpr int64_t kPassBytes = int64_t(256) << 20;   // workspace a pass may take
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// One chunk and value head in the workspace.
-constexpr int kSlotMat = kC * kC;             // floats of each matrix
-constexpr int kSlotVec = 4 * kC;              // e, f, then g_C and whether the chunk runs token by token
-constexpr int kSlotFloats = 2 * kSlotMat + kSlotVec;
+// One chunk and value head in the workspace: the row factors e, f, then g_C and
+// whether the chunk runs token by token; the two matrices.  For fp32 activations
+// they are rows of fp32; for bf16 three planes of bf16 as the matrix unit's
+// operand has them, 16 rows by 32 columns a kilobyte, those that lie above the
+// diagonal left out.
+constexpr int kVec = 4 * kC;                  // floats
+constexpr int kPieces = 6;                    // (rows 0, 16, 32, 48 by columns 0; 32, 48 by 32)
+constexpr int kMatF32 = kC * kC * 4, kMatBf16 = 3 * kPieces * 1024;
+constexpr int slot_bytes(int act) { return kVec * 4 + 2 * (act == kF32 ? kMatF32 : kMatBf16); }
+__host__ __device__ constexpr int piece_of(int tile, int step) { return tile < 2 ? tile : 2 * tile - 2 + step; }
 
 struct GdcArgs {
   const int32_t* cu;
@@ -42,7 +55,7 @@ struct GdcArgs {
   const float* state_in;
   float* state_out;
   void* out;
-  float* ws;
+  uint8_t* ws;
   int B, N, T_max;
   int nk, nv, dv;
   int first;            // first chunk of this pass in every sequence
@@ -76,26 +89,51 @@ __device__ __forceinline__ f32x4 load4(const void* base, int64_t c) {
   }
 }
 
-__device__ __forceinline__ float xor16_add(float x, int lane) {
-  x = x + __uint_as_float(lane_xor<16>(__float_as_uint(x), lane));
-  return x + __uint_as_float(lane_xor<32>(__float_as_uint(x), lane));
-}
-
 __device__ __forceinline__ bool finite4(const f32x4& v) {
   return isfinite(v[0]) && isfinite(v[1]) && isfinite(v[2]) && isfinite(v[3]);
 }
 
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// x as the sum of three bf16.
+__device__ __forceinline__ void split3(float x, __bf16& a, __bf16& b, __bf16& c) {
+  a = static_cast<__bf16>(x);
+  const float r = x - static_cast<float>(a);
+  b = static_cast<__bf16>(r);
+  c = static_cast<__bf16>(r - static_cast<float>(b));
+}
+
+// The part of a row of K or Q that a lane feeds to a product over 32 (bf16) or
+// 16 (fp32) dims, from LDS.
+template <int ACT>
+using Operand = std::conditional_t<ACT == kF32, f32x4, bf16x8>;
+
+__device__ __forceinline__ f32x4 dot_step(f32x4 a, f32x4 b, f32x4 c) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+  return c;
+}
+__device__ __forceinline__ f32x4 dot_step(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
 template <int DK, int ACT>
 __global__ __launch_bounds__(256) void k_gdc_prep(GdcArgs a) {
-  constexpr int KS = DK / 16;
+  constexpr int kSize = ACT == kF32 ? 4 : 2;
+  constexpr int kRow = DK * kSize + 16;          // bytes of a row of K or Q in LDS
+  constexpr int kPer = DK * kSize / 16;          // 16-byte pieces a row: the lanes that load it
+  constexpr int KS = DK * kSize / 64;            // steps of 64 bytes
   constexpr int kLd = kC + 4;
+  // K and Q, then in their place P and T
+  constexpr int kKq = 2 * kC * kRow, kMats = 2 * kC * kLd * 4;
+  __shared__ __align__(16) uint8_t kq[kKq > kMats ? kKq : kMats];
   __shared__ __align__(16) float As[kC * kLd];
-  __shared__ __align__(16) float Ts[kC * kLd];   // its blocks on and below the diagonal
-  __shared__ __align__(16) float Ps[kC * kLd];
   __shared__ float rk[kC], rq[kC], be[kC];
   __shared__ double Lg[kC];
   __shared__ int odd;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), w = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int n16 = lane & 15, g = lane >> 4;
   const int slot = blockIdx.x / a.nv, h = blockIdx.x % a.nv, kh = h / (a.nv / a.nk);
 
@@ -107,11 +145,12 @@ __global__ __launch_bounds__(256) void k_gdc_prep(GdcArgs a) {
     int cnt = 0;
     for (int i = 0; i < a.B; i += kWave) {
       const int j = i + lane;
-      cnt += __popcll(__ballot(j < a.B && a.cu[j] / kC + j <= slot));
+      cnt += __popcll(__ballot(j < a.B && a.cu[j < a.B ? j : 0] / kC + j <= slot));
     }
     b = cnt - 1;
   }
   if (b < 0 || b >= a.B) return;
+  b = __builtin_amdgcn_readfirstlane(b);
   int begin, n;
   sequence(a, b, begin, n);
   const int c = a.per_pass ? a.first + slot % a.per_pass : slot - begin / kC - b;
@@ -122,11 +161,12 @@ __global__ __launch_bounds__(256) void k_gdc_prep(GdcArgs a) {
 
   if (tid == 0) odd = 0;
   __syncthreads();
+  bool fine = true;
   if (w == 0) {                                // gates: logarithms summed in double precision
     const bool in = lane < len;
     const float al = in ? a.alpha[(row0 + lane) * a.nv + h] : 1.f;
     const float bt = in ? a.beta[(row0 + lane) * a.nv + h] : 0.f;
-    if (!(al >= 9.5367431640625e-7f && al <= 1.f && bt >= 0.f && bt <= 2.f)) odd = 1;
+    if (!(al >= 9.5367431640625e-7f && al <= 1.f && bt >= 0.f && bt <= 2.f)) fine = false;
     double s = static_cast<double>(log2f(al));
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
@@ -136,81 +176,106 @@ __global__ __launch_bounds__(256) void k_gdc_prep(GdcArgs a) {
     Lg[lane] = s;
     be[lane] = bt;
   }
-
-  // K K^T and Q K^T, the lower blocks; rows of tile w, columns of tiles up to w
+  // K and Q into LDS, and the norms of their rows over the lanes that load one
   const int64_t st = static_cast<int64_t>(a.nk) * DK;
-  const bool live = 16 * w + n16 < len;
-  const int64_t mine = (row0 + (live ? 16 * w + n16 : 0)) * st + static_cast<int64_t>(kh) * DK;
-  f32x4 Ka[KS], Qa[KS];
-  float sk = 0.f, sq = 0.f;
-  bool fine = true;
 #pragma unroll
-  for (int s = 0; s < KS; ++s) {
-    Ka[s] = load4<ACT>(a.k, mine + 16 * s + 4 * g);
-    Qa[s] = load4<ACT>(a.q, mine + 16 * s + 4 * g);
-    if (!live) Ka[s] = Qa[s] = f32x4{0.f, 0.f, 0.f, 0.f};
-    fine = fine && finite4(Ka[s]) && finite4(Qa[s]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sk = fmaf(Ka[s][i], Ka[s][i], sk);
-      sq = fmaf(Qa[s][i], Qa[s][i], sq);
+  for (int i = tid; i < kC * kPer; i += 256) {
+    const int r = i / kPer, at = (i % kPer) * 16;
+    u32x4 kv = {0, 0, 0, 0}, qv = kv;
+    if (r < len) {
+      const int64_t off = ((row0 + r) * st + static_cast<int64_t>(kh) * DK) * kSize + at;
+      kv = load16(static_cast<const uint8_t*>(a.k) + off);
+      qv = load16(static_cast<const uint8_t*>(a.q) + off);
     }
-  }
-  for (int i = tid; i < len * (a.dv / 4); i += 256) {
-    const f32x4 v = load4<ACT>(a.v, ((row0 + i / (a.dv / 4)) * a.nv + h) * static_cast<int64_t>(a.dv) + (i % (a.dv / 4)) * 4);
-    fine = fine && finite4(v);
-  }
-  sk = xor16_add(sk, lane);
-  sq = xor16_add(sq, lane);
-  const float rkv = 1.0f / sqrtf(sk + a.eps), rqv = a.scale / sqrtf(sq + a.eps);
-  if (!fine || (live && !(isfinite(rkv) && isfinite(rqv) && isfinite(sk) && isfinite(sq)))) odd = 1;
-  if (g == 0) {
-    rk[16 * w + n16] = live ? rkv : 0.f;
-    rq[16 * w + n16] = live ? rqv : 0.f;
-  }
-  f32x4 G[4], H[4];
+    *reinterpret_cast<u32x4*>(kq + r * kRow + at) = kv;
+    *reinterpret_cast<u32x4*>(kq + kC * kRow + r * kRow + at) = qv;
+    float sk = 0.f, sq = 0.f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    G[j] = H[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (j > w) continue;
-    const bool lj = 16 * j + n16 < len;
-    const int64_t at = (row0 + (lj ? 16 * j + n16 : 0)) * st + static_cast<int64_t>(kh) * DK;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      f32x4 Kb = load4<ACT>(a.k, at + 16 * s + 4 * g);
-      if (!lj) Kb = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        G[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(Ka[s][i], Kb[i], G[j], 0, 0, 0);
-        H[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(Qa[s][i], Kb[i], H[j], 0, 0, 0);
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (ACT == kF32) {
+        sk = fmaf(__uint_as_float(kv[j]), __uint_as_float(kv[j]), sk);
+        sq = fmaf(__uint_as_float(qv[j]), __uint_as_float(qv[j]), sq);
+      } else {
+        const float k0 = __uint_as_float(kv[j] << 16), k1 = __uint_as_float(kv[j] & 0xffff0000u);
+        const float q0 = __uint_as_float(qv[j] << 16), q1 = __uint_as_float(qv[j] & 0xffff0000u);
+        sk = fmaf(k1, k1, fmaf(k0, k0, sk));
+        sq = fmaf(q1, q1, fmaf(q0, q0, sq));
       }
     }
+#pragma unroll
+    for (int d = 1; d < kPer; d <<= 1) {
+      sk += __shfl_xor(sk, d);
+      sq += __shfl_xor(sq, d);
+    }
+    const float rkv = 1.0f / sqrtf(sk + a.eps), rqv = a.scale / sqrtf(sq + a.eps);
+    // a row that is not finite has a norm that is not
+    fine = fine && (r >= len || (isfinite(sk) && isfinite(sq) && isfinite(rkv) && isfinite(rqv)));
+    if (i % kPer == 0) {
+      rk[r] = r < len ? rkv : 0.f;
+      rq[r] = r < len ? rqv : 0.f;
+    }
   }
+  for (int i = tid; i < len * (a.dv / 8); i += 256) {
+    const int64_t at = ((row0 + i / (a.dv / 8)) * a.nv + h) * static_cast<int64_t>(a.dv) + (i % (a.dv / 8)) * 8;
+    fine = fine && finite4(load4<ACT>(a.v, at)) && finite4(load4<ACT>(a.v, at + 4));
+  }
+  if (!fine) odd = 1;
   __syncthreads();
-  float* slot_p = a.ws + (static_cast<int64_t>(slot) * a.nv + h) * kSlotFloats;
+  uint8_t* const out = a.ws + (static_cast<int64_t>(slot) * a.nv + h) * slot_bytes(ACT);
+  float* const vec = reinterpret_cast<float*>(out);
   if (odd) {
-    if (tid == 0) slot_p[2 * kSlotMat + 2 * kC + 1] = 1.f;
+    if (tid == 0) vec[2 * kC + 1] = 1.f;
     return;
   }
+  // K K^T and Q K^T: the ten blocks (i, j) of 16 x 16 on and below the diagonal
+  constexpr int I[12] = {0, 1, 2, 3, 1, 2, 3, 2, 3, 3, 0, 0}, J[12] = {0, 1, 2, 3, 0, 1, 2, 0, 1, 0, 0, 0};
+  f32x4 H[3];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int x = 0; x < 3; ++x) {
+    const int p = w + 4 * x;
+    if (p >= 10) continue;
+    const int bi = I[p], bj = J[p];
+    f32x4 G = {0.f, 0.f, 0.f, 0.f};
+    H[x] = G;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const auto Ka = *reinterpret_cast<const Operand<ACT>*>(kq + (16 * bi + n16) * kRow + 64 * s + 16 * g);
+      const auto Qa = *reinterpret_cast<const Operand<ACT>*>(kq + kC * kRow + (16 * bi + n16) * kRow + 64 * s + 16 * g);
+      const auto Kb = *reinterpret_cast<const Operand<ACT>*>(kq + (16 * bj + n16) * kRow + 64 * s + 16 * g);
+      G = dot_step(Ka, Kb, G);
+      H[x] = dot_step(Qa, Kb, H[x]);
+    }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int i = 16 * w + 4 * g + r, jj = 16 * j + n16;
-      const float D = i >= jj ? exp2f(static_cast<float>(Lg[i] - Lg[jj])) : 0.f;
-      As[i * kLd + jj] = i > jj ? be[i] * D * rk[i] * rk[jj] * G[j][r] : 0.f;
-      Ps[i * kLd + jj] = D * rq[i] * rk[jj] * H[j][r];
+      const int i = 16 * bi + 4 * g + r, j = 16 * bj + n16;
+      const float D = i >= j ? exp2f(static_cast<float>(Lg[i] - Lg[j])) * rk[j] : 0.f;
+      As[i * kLd + j] = i > j ? be[i] * D * rk[i] * G[r] : 0.f;
+      H[x][r] *= D * rq[i];
     }
-  __syncthreads();
+  }
+  __syncthreads();                               // K and Q have been read
+  float* const Ps = reinterpret_cast<float*>(kq);
+  float* const Ts = Ps + kC * kLd;
+  float* const PT = As;                          // A has done its part by then
+#pragma unroll
+  for (int x = 0; x < 3; ++x) {
+    const int p = w + 4 * x;
+    if (p < 10)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) Ps[(16 * I[p] + 4 * g + r) * kLd + 16 * J[p] + n16] = H[x][r];
+  }
   // T = (I + A)^-1: the diagonal blocks by substitution, a column a lane ...
   {
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float s = i == n16 ? 1.f : 0.f;
+      float s0 = i == n16 ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
-      for (int l = 0; l < i; ++l) s = fmaf(-As[(16 * w + i) * kLd + 16 * w + l], x[l], s);
-      x[i] = s;
+      for (int l = 0; l < i; ++l) {
+        float& s = l & 1 ? s1 : s0;
+        s = fmaf(-As[(16 * w + i) * kLd + 16 * w + l], x[l], s);
+      }
+      x[i] = s0 + s1;
     }
     if (g == 0)
 #pragma unroll
@@ -222,49 +287,409 @@ __global__ __launch_bounds__(256) void k_gdc_prep(GdcArgs a) {
     const int bj = w - d;
     if (bj >= 0) {
       f32x4 s = {0.f, 0.f, 0.f, 0.f}, o = {0.f, 0.f, 0.f, 0.f};
-      for (int l = bj; l < w; ++l)
+      for (int l = bj; l < w; ++l) {
+        const f32x4 Al = *reinterpret_cast<const f32x4*>(As + (16 * w + n16) * kLd + 16 * l + 4 * g);
 #pragma unroll
         for (int i = 0; i < 4; ++i)          // k = 4 g + i of block l
-          s = __builtin_amdgcn_mfma_f32_16x16x4f32(As[(16 * w + n16) * kLd + 16 * l + 4 * g + i],
-                                                   Ts[(16 * l + 4 * g + i) * kLd + 16 * bj + n16], s, 0, 0, 0);
+          s = __builtin_amdgcn_mfma_f32_16x16x4f32(Al[i], Ts[(16 * l + 4 * g + i) * kLd + 16 * bj + n16], s, 0, 0, 0);
+      }
+      const f32x4 Tw = *reinterpret_cast<const f32x4*>(Ts + (16 * w + n16) * kLd + 16 * w + 4 * g);
 #pragma unroll
       for (int i = 0; i < 4; ++i)            // s[i] is row 4 g + i: the operand's k
-        o = __builtin_amdgcn_mfma_f32_16x16x4f32(Ts[(16 * w + n16) * kLd + 16 * w + 4 * g + i], s[i], o, 0, 0, 0);
+        o = __builtin_amdgcn_mfma_f32_16x16x4f32(Tw[i], s[i], o, 0, 0, 0);
 #pragma unroll
       for (int r = 0; r < 4; ++r) Ts[(16 * w + 4 * g + r) * kLd + 16 * bj + n16] = -o[r];
     }
     __syncthreads();
   }
-  // P T, and both matrices out
+  // P T, block by block; entry (i, j) takes i - j + 1 products, and each wave five
+  constexpr int PI[12] = {3, 2, 3, 3, 0, 1, 2, 1, 0, 0, 0, 2}, PJ[12] = {0, 0, 1, 2, 0, 0, 1, 1, 0, 0, 0, 2};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int x = 0; x < 4; ++x) {
+    // wave 3 has (3, 2), (1, 1), (2, 2), (3, 3); the others two blocks
+    int bi, bj;
+    if (x < 2) {
+      bi = PI[w + 4 * x];
+      bj = PJ[w + 4 * x];
+    } else {
+      if (w != 3) continue;
+      bi = bj = x;
+    }
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
-    for (int l = j; l <= w; ++l)
+    for (int l = bj; l <= bi; ++l) {
+      const f32x4 Pl = *reinterpret_cast<const f32x4*>(Ps + (16 * bi + n16) * kLd + 16 * l + 4 * g);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        o = __builtin_amdgcn_mfma_f32_16x16x4f32(Ps[(16 * w + n16) * kLd + 16 * l + 4 * g + i],
-                                                 Ts[(16 * l + 4 * g + i) * kLd + 16 * j + n16], o, 0, 0, 0);
+        o = __builtin_amdgcn_mfma_f32_16x16x4f32(Pl[i], Ts[(16 * l + 4 * g + i) * kLd + 16 * bj + n16], o, 0, 0, 0);
+    }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = 16 * w + 4 * g + r, jj = 16 * j + n16;
-      const float wi = exp2f(static_cast<float>(Lg[kC - 1] - Lg[i])) * rk[i];
-      slot_p[i * kC + jj] = j <= w ? wi * Ts[i * kLd + jj] * be[jj] : 0.f;
-      slot_p[kSlotMat + i * kC + jj] = o[r] * be[jj];
+    for (int r = 0; r < 4; ++r) PT[(16 * bi + 4 * g + r) * kLd + 16 * bj + n16] = o[r];
+  }
+  __syncthreads();
+  // both matrices out, row tile w, scaled by w_i and beta_j
+  {
+    const int i = 16 * w + n16;
+    const float wi = exp2f(static_cast<float>(Lg[kC - 1] - Lg[i])) * rk[i];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (ACT == kBF16 && s > w / 2) continue;
+      float tz[8], to[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const int j = 32 * s + 8 * g + x;
+        const bool in = j <= i;
+        tz[x] = in ? wi * Ts[i * kLd + j] * be[j] : 0.f;
+        to[x] = in ? PT[i * kLd + j] * be[j] : 0.f;
+      }
+      if constexpr (ACT == kF32) {
+        float* m = vec + kVec + i * kC + 32 * s + 8 * g;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          *reinterpret_cast<f32x4*>(m + 4 * x) = f32x4{tz[4 * x], tz[4 * x + 1], tz[4 * x + 2], tz[4 * x + 3]};
+          *reinterpret_cast<f32x4*>(m + kC * kC + 4 * x) = f32x4{to[4 * x], to[4 * x + 1], to[4 * x + 2], to[4 * x + 3]};
+        }
+      } else {
+        bf16x8 z[3], o[3];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          __bf16 p0, p1, p2;
+          split3(tz[x], p0, p1, p2);
+          z[0][x] = p0; z[1][x] = p1; z[2][x] = p2;
+          split3(to[x], p0, p1, p2);
+          o[0][x] = p0; o[1][x] = p1; o[2][x] = p2;
+        }
+        uint8_t* m = out + kVec * 4 + piece_of(w, s) * 3 * 1024 + lane * 16;
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+          *reinterpret_cast<bf16x8*>(m + x * 1024) = z[x];
+          *reinterpret_cast<bf16x8*>(m + kMatBf16 + x * 1024) = o[x];
+        }
+      }
     }
   }
   if (tid < kC) {
     const float gi = exp2f(static_cast<float>(Lg[tid]));
-    slot_p[2 * kSlotMat + tid] = gi * rk[tid];
-    slot_p[2 * kSlotMat + kC + tid] = gi * rq[tid];
+    vec[tid] = gi * rk[tid];
+    vec[kC + tid] = gi * rq[tid];
     if (tid == kC - 1) {
-      slot_p[2 * kSlotMat + 2 * kC] = gi;
-      slot_p[2 * kSlotMat + 2 * kC + 1] = 0.f;
+      vec[2 * kC] = gi;
+      vec[2 * kC + 1] = 0.f;
     }
   }
 }
 
+// A chunk token by token, 16 lanes a row of the 16 of the state in LDS (S, rows
+// kLs apart), every wave four of them.
 template <int DK, int ACT, int OUT>
-__global__ __launch_bounds__(256) void k_gdc_scan(GdcArgs a) {
+__device__ __forceinline__ void chunk_by_token(const GdcArgs& a, float* Ss, int kLs, int64_t row0, int len, int h, int kh, int dv0, int lane, int w) {
+  constexpr int NC = DK / 16;
+  const int n16 = lane & 15, r = 4 * w + (lane >> 4);
+  const int64_t st = static_cast<int64_t>(a.nk) * DK;
+  float S[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) S[i] = Ss[r * kLs + n16 * NC + i];
+  const auto sum16 = [&](float x) {
+    x += __shfl_xor(x, 1);
+    x += __shfl_xor(x, 2);
+    x += __shfl_xor(x, 4);
+    return x + __shfl_xor(x, 8);
+  };
+  for (int t = 0; t < len; ++t) {
+    const int64_t at = (row0 + t) * st + static_cast<int64_t>(kh) * DK + n16 * NC;
+    float kv[NC], qv[NC], sk = 0.f, sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      kv[i] = load_scalar<ACT>(a.k, at + i);
+      qv[i] = load_scalar<ACT>(a.q, at + i);
+      sk = fmaf(kv[i], kv[i], sk);
+      sq = fmaf(qv[i], qv[i], sq);
+    }
+    const float fk = 1.0f / sqrtf(sum16(sk) + a.eps), fq = a.scale / sqrtf(sum16(sq) + a.eps);
+    const float al = a.alpha[(row0 + t) * a.nv + h], bt = a.beta[(row0 + t) * a.nv + h];
+    const int64_t vo = ((row0 + t) * a.nv + h) * static_cast<int64_t>(a.dv) + dv0 + r;
+    float x = 0.f, o = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      kv[i] *= fk;
+      qv[i] *= fq;
+      x = fmaf(S[i], kv[i], x);
+    }
+    const float u = bt * (load_scalar<ACT>(a.v, vo) - al * sum16(x));
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      S[i] = fmaf(u, kv[i], al * S[i]);
+      o = fmaf(S[i], qv[i], o);
+    }
+    o = sum16(o);
+    if (n16 == 0) {
+      if constexpr (OUT == kF32) static_cast<float*>(a.out)[vo] = o;
+      else static_cast<uint16_t*>(a.out)[vo] = f32_to_bf16(o);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NC; ++i) Ss[r * kLs + n16 * NC + i] = S[i];
+}
+
+// What a block of a scan works on: head h of sequence b, state rows from dv0 on.
+struct Scan {
+  int h, kh, b, dv0, begin, n, c0, c1;
+  int64_t state;        // offset of its rows in the states
+};
+
+// The blocks of a head, which read the same matrices, go to one XCD (blocks
+// are dealt out in turns over eight).
+__device__ __forceinline__ bool find_scan(const GdcArgs& a, int dk, Scan& s) {
+  const int nz = a.dv / kRowsS;
+  const int q = blockIdx.x / 8;
+  const int bh = (q / nz) * 8 + blockIdx.x % 8;
+  if (bh >= a.B * a.nv) return false;
+  s.dv0 = (q % nz) * kRowsS;
+  s.h = bh % a.nv;
+  s.b = bh / a.nv;
+  s.kh = s.h / (a.nv / a.nk);
+  sequence(a, s.b, s.begin, s.n);
+  s.state = (static_cast<int64_t>(s.b) * a.nv + s.h) * a.dv * static_cast<int64_t>(dk) + static_cast<int64_t>(s.dv0) * dk;
+  s.c0 = a.first;
+  s.c1 = (s.n + kC - 1) / kC;
+  if (a.per_pass && s.c1 > s.c0 + a.per_pass) s.c1 = s.c0 + a.per_pass;
+  return s.c0 == 0 || s.c0 < s.c1;             // else done in an earlier pass
+}
+
+// bf16 activations.  Wave w has tokens 16 w .. 16 w + 15 of a chunk in the first
+// two products and state columns DK / 4 w .. in the third; S, X and Zt pass from
+// one to the next through LDS, split in three.  What a product takes of the next
+// chunk is requested as soon as it is done with this one's.
+template <int DK, int OUT>
+__global__ __launch_bounds__(256, 2) void k_gdc_scan_bf16(GdcArgs a) {
+  constexpr int KS = DK / 32;                  // steps of 32 state columns
+  constexpr int NT = DK / 64;                  // tiles of 16 state columns a wave
+  constexpr int kLs = DK + 4;
+  constexpr int kPer = DK / 8;                 // 16-byte pieces of a row of K
+  constexpr int kKl = kC * kPer / 256;         // of them a thread
+  constexpr int kPlaneS = kRowsS * DK * 2, kPlaneX = kRowsS * kC * 2;
+  __shared__ __align__(16) uint8_t Sp[3 * kPlaneS];        // S, X and Zt: [plane][state row][column or token]
+  __shared__ __align__(16) uint8_t Xp[3 * kPlaneX];
+  __shared__ __align__(16) uint8_t Zp[3 * kPlaneX];
+  __shared__ __align__(16) uint8_t Kp[2][kC * DK * 2];
+  const int lane = threadIdx.x & (kWave - 1), w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int n16 = lane & 15, g = lane >> 4;
+  Scan sc;
+  if (!find_scan(a, DK, sc)) return;
+  // Pieces of 16 bytes turned by their row against bank conflicts: rows of S
+  // (256 or 128 bytes), of X and Zt (128), and of K (read by rows and, four rows of
+  // 32 bytes at once, transposed).
+  const auto s_at = [&](int row, int col) { return row * DK * 2 + (((col >> 3) ^ (row & (kPer - 1))) << 4) + (col & 7) * 2; };
+  const auto x_at = [&](int row, int tok) { return row * kC * 2 + (((tok >> 3) ^ (row & 7)) << 4) + (tok & 7) * 2; };
+  const auto k_at = [&](int tok, int piece) { return tok * DK * 2 + ((piece ^ (((tok & 3) + ((tok >> 1) & 4)) * (DK == 128 ? 2 : 1))) << 4); };
+
+  // this wave's columns of S^T: tile t, lane: state row n16, columns 16 (NT w + t) + 4 g ..
+  f32x4 S[NT];
+  const float* src = sc.c0 > 0 ? a.state_out : a.state_in;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+    S[t] = src ? *reinterpret_cast<const f32x4*>(src + sc.state + n16 * DK + 16 * (NT * w + t) + 4 * g) : f32x4{0.f, 0.f, 0.f, 0.f};
+  const auto put_s = [&]() {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      bf16x4 p[3];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        __bf16 x, y, z;
+        split3(S[t][i], x, y, z);
+        p[0][i] = x; p[1][i] = y; p[2][i] = z;
+      }
+#pragma unroll
+      for (int x = 0; x < 3; ++x) *reinterpret_cast<bf16x4*>(Sp + x * kPlaneS + s_at(n16, 16 * (NT * w + t) + 4 * g)) = p[x];
+    }
+  };
+  const auto put_x = [&](uint8_t* to, const f32x4& v) {
+    bf16x4 p[3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __bf16 x, y, z;
+      split3(v[i], x, y, z);
+      p[0][i] = x; p[1][i] = y; p[2][i] = z;
+    }
+#pragma unroll
+    for (int x = 0; x < 3; ++x) *reinterpret_cast<bf16x4*>(to + x * kPlaneX + x_at(n16, 16 * w + 4 * g)) = p[x];
+  };
+
+  const int64_t st = static_cast<int64_t>(a.nk) * DK;
+  const uint16_t* const kb = static_cast<const uint16_t*>(a.k) + static_cast<int64_t>(sc.kh) * DK;
+  const uint16_t* const qb = static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(sc.kh) * DK;
+  const uint16_t* const vb = static_cast<const uint16_t*>(a.v) + static_cast<int64_t>(sc.h) * a.dv + sc.dv0 + n16;
+  const int64_t vst = static_cast<int64_t>(a.nv) * a.dv;
+  // Tokens behind the last one: rows of it again, whose Zt and matrix columns are 0.
+  const auto row_of = [&](int c, int t) {
+    const int at = c * kC + t;
+    return static_cast<int64_t>(sc.begin) + (at < sc.n ? at : sc.n - 1);
+  };
+  u32x4 Kn[kKl];
+  bf16x8 Q[KS], Tz[2][3], To[2][3];
+  uint32_t V[4];                               // as stored: converted where it is used, or the load would be waited for here
+  f32x4 e, f;
+  float2 gc;                                   // g_C, and whether the chunk runs token by token
+  const auto slot = [&](int c) { return a.ws + (slot_of(a, sc.b, sc.begin, c) * a.nv + sc.h) * slot_bytes(kBF16); };
+  const auto ask_k = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < kKl; ++i) {
+      const int p = threadIdx.x + 256 * i;
+      Kn[i] = load16(kb + row_of(c, p / kPer) * st + (p % kPer) * 8);
+    }
+  };
+  const auto put_k = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < kKl; ++i) {
+      const int p = threadIdx.x + 256 * i;
+      *reinterpret_cast<u32x4*>(Kp[c & 1] + k_at(p / kPer, p % kPer)) = Kn[i];
+    }
+  };
+  const auto ask_first = [&](int c) {          // for the first product
+    const uint16_t* q = qb + row_of(c, 16 * w + n16) * st + 8 * g;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) Q[s] = __builtin_bit_cast(bf16x8, load16(q + 32 * s));
+#pragma unroll
+    for (int r = 0; r < 4; ++r) V[r] = vb[row_of(c, 16 * w + 4 * g + r) * vst];
+    const float* vec = reinterpret_cast<const float*>(slot(c));
+    e = *reinterpret_cast<const f32x4*>(vec + 16 * w + 4 * g);
+    f = *reinterpret_cast<const f32x4*>(vec + kC + 16 * w + 4 * g);
+    gc = *reinterpret_cast<const float2*>(vec + 2 * kC);
+  };
+  const auto ask_second = [&](int c) {         // for the second
+    const uint8_t* m = slot(c) + kVec * 4 + lane * 16;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (s <= w / 2)
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+          Tz[s][x] = __builtin_bit_cast(bf16x8, load16(m + (piece_of(w, s) * 3 + x) * 1024));
+          To[s][x] = __builtin_bit_cast(bf16x8, load16(m + kMatBf16 + (piece_of(w, s) * 3 + x) * 1024));
+        }
+  };
+  put_s();
+  if (sc.c0 < sc.c1) {
+    ask_k(sc.c0);
+    ask_first(sc.c0);
+    ask_second(sc.c0);
+    put_k(sc.c0);
+  }
+  __syncthreads();
+  for (int c = sc.c0; c < sc.c1; ++c) {
+    const int64_t row0 = static_cast<int64_t>(sc.begin) + c * kC;
+    const int len = sc.n - c * kC < kC ? sc.n - c * kC : kC;
+    // requests without a condition (the last chunk asks for itself again), so that no copy of a register waits for one
+    const int next = c + 1 < sc.c1 ? c + 1 : c;
+    const uint8_t* K = Kp[c & 1];
+    ask_k(next);
+    const float gC = gc.x;
+    const bool by_token = __builtin_amdgcn_readfirstlane(__float_as_int(gc.y)) != 0;
+    f32x4 qs = {0.f, 0.f, 0.f, 0.f};
+    if (by_token) {
+      // in fp32 through the place of S
+      static_assert(3 * kPlaneS >= kRowsS * kLs * 4, "room for the state");
+      float* Ss = reinterpret_cast<float*>(Sp);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) *reinterpret_cast<f32x4*>(Ss + n16 * kLs + 16 * (NT * w + t) + 4 * g) = S[t];
+      __syncthreads();
+      chunk_by_token<DK, kBF16, OUT>(a, Ss, kLs, row0, len, sc.h, sc.kh, sc.dv0, lane, w);
+      __syncthreads();
+#pragma unroll
+      for (int t = 0; t < NT; ++t) S[t] = *reinterpret_cast<const f32x4*>(Ss + n16 * kLs + 16 * (NT * w + t) + 4 * g);
+    } else {
+      // K S^T and Q S^T
+      f32x4 ks = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const bf16x8 Ka = *reinterpret_cast<const bf16x8*>(K + k_at(16 * w + n16, 4 * s + g));
+#pragma unroll
+        for (int x = 2; x >= 0; --x) {
+          const bf16x8 Sb = *reinterpret_cast<const bf16x8*>(Sp + x * kPlaneS + s_at(n16, 32 * s + 8 * g));
+          ks = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Ka, Sb, ks, 0, 0, 0);
+          qs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Q[s], Sb, qs, 0, 0, 0);
+        }
+      }
+      f32x4 x;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        x[r] = __uint_as_float(V[r] << 16) - e[r] * ks[r];
+        qs[r] *= f[r];
+      }
+      put_x(Xp, x);
+    }
+    ask_first(next);
+    __syncthreads();
+    if (!by_token) {
+      // (Z-matrix) X and (O-matrix) X
+      f32x4 zt = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (s <= w / 2) {
+          bf16x8 Xb[3];
+#pragma unroll
+          for (int y = 0; y < 3; ++y) Xb[y] = *reinterpret_cast<const bf16x8*>(Xp + y * kPlaneX + x_at(n16, 32 * s + 8 * g));
+#pragma unroll
+          for (int y = 2; y >= 0; --y)         // the smallest terms first
+#pragma unroll
+            for (int z = 2 - y; z >= 0; --z) {
+              zt = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Tz[s][z], Xb[y], zt, 0, 0, 0);
+              qs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(To[s][z], Xb[y], qs, 0, 0, 0);
+            }
+        }
+      put_x(Zp, zt);
+    }
+    ask_second(next);
+    __syncthreads();
+    if (!by_token) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 16 * w + 4 * g + r;
+        if (i < len) {
+          const int64_t oi = ((row0 + i) * a.nv + sc.h) * static_cast<int64_t>(a.dv) + sc.dv0 + n16;
+          if constexpr (OUT == kF32) static_cast<float*>(a.out)[oi] = qs[r];
+          else static_cast<uint16_t*>(a.out)[oi] = f32_to_bf16(qs[r]);
+        }
+      }
+      // S^T, the columns of this wave
+      bf16x8 Zb[2][3];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int y = 0; y < 3; ++y) Zb[s][y] = *reinterpret_cast<const bf16x8*>(Zp + y * kPlaneX + x_at(n16, 32 * s + 8 * g));
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int piece = 2 * (NT * w + t) + ((n16 & 3) >> 1);
+        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          bf16x8 Ka;                           // column n16 of the tile, tokens 32 s + 8 g + 0 .. 7
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+            const int tok = 32 * s + 8 * g + 4 * y + (n16 >> 2);
+            const bf16x4 v = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(K + k_at(tok, piece) + (n16 & 1) * 8)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) Ka[4 * y + i] = v[i];
+          }
+#pragma unroll
+          for (int y = 2; y >= 0; --y) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Ka, Zb[s][y], d, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[t][i] = fmaf(gC, S[t][i], d[i]);
+      }
+    }
+    put_s();
+    put_k(c + 1);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+    *reinterpret_cast<f32x4*>(a.state_out + sc.state + n16 * DK + 16 * (NT * w + t) + 4 * g) = S[t];
+}
+
+// fp32 activations, on the fp32 matrix instruction.
+template <int DK, int OUT>
+__global__ __launch_bounds__(256) void k_gdc_scan_f32(GdcArgs a) {
+  constexpr int ACT = kF32;
   constexpr int KS = DK / 16;
   constexpr int NT = DK / 64;                  // tiles of 16 state columns a wave
   constexpr int kLs = DK + 4, kLx = kC + 4;
@@ -274,18 +699,10 @@ __global__ __launch_bounds__(256) void k_gdc_scan(GdcArgs a) {
   __shared__ __align__(16) float Zs[kRowsS * kLx];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave;
   const int n16 = lane & 15, g = lane >> 4;
-  const int nz = a.dv / kRowsS;
-  const int z = blockIdx.x % nz;
-  const int bh = blockIdx.x / nz;
-  const int h = bh % a.nv, b = bh / a.nv, kh = h / (a.nv / a.nk);
-  int begin, n;
-  sequence(a, b, begin, n);
-  const int dv0 = z * kRowsS;
-  const int64_t so = (static_cast<int64_t>(b) * a.nv + h) * a.dv * static_cast<int64_t>(DK) + static_cast<int64_t>(dv0) * DK;
-  const int c0 = a.first;
-  int c1 = (n + kC - 1) / kC;
-  if (a.per_pass && c1 > c0 + a.per_pass) c1 = c0 + a.per_pass;
-  if (c0 > 0 && c0 >= c1) return;              // done in an earlier pass
+  Scan sc;
+  if (!find_scan(a, DK, sc)) return;
+  const int h = sc.h, kh = sc.kh, b = sc.b, begin = sc.begin, n = sc.n, c0 = sc.c0, c1 = sc.c1, dv0 = sc.dv0;
+  const int64_t so = sc.state;
   const float* src = c0 > 0 ? a.state_out : a.state_in;
   for (int i = tid; i < kRowsS * (DK / 4); i += 256) {
     const int r = i / (DK / 4), cc = (i % (DK / 4)) * 4;
@@ -298,53 +715,10 @@ __global__ __launch_bounds__(256) void k_gdc_scan(GdcArgs a) {
     const int t0 = c * kC;
     const int len = n - t0 < kC ? n - t0 : kC;
     const int64_t row0 = static_cast<int64_t>(begin) + t0;
-    const float* slot_p = a.ws + (slot_of(a, b, begin, c) * a.nv + h) * kSlotFloats;
-    if (slot_p[2 * kSlotMat + 2 * kC + 1] != 0.f) {
-      // token by token, 16 lanes a row of the state
-      const int r = 4 * w + g;
-      float S[DK / 16];
-#pragma unroll
-      for (int i = 0; i < DK / 16; ++i) S[i] = Ss[r * kLs + n16 * (DK / 16) + i];
-      for (int t = 0; t < len; ++t) {
-        const int64_t at = (row0 + t) * st + static_cast<int64_t>(kh) * DK + n16 * (DK / 16);
-        float kv[DK / 16], qv[DK / 16], sk = 0.f, sq = 0.f;
-#pragma unroll
-        for (int i = 0; i < DK / 16; ++i) {
-          kv[i] = load_scalar<ACT>(a.k, at + i);
-          qv[i] = load_scalar<ACT>(a.q, at + i);
-          sk = fmaf(kv[i], kv[i], sk);
-          sq = fmaf(qv[i], qv[i], sq);
-        }
-        const auto sum16 = [&](float x) {
-          x += __shfl_xor(x, 1);
-          x += __shfl_xor(x, 2);
-          x += __shfl_xor(x, 4);
-          return x + __shfl_xor(x, 8);
-        };
-        const float fk = 1.0f / sqrtf(sum16(sk) + a.eps), fq = a.scale / sqrtf(sum16(sq) + a.eps);
-        const float al = a.alpha[(row0 + t) * a.nv + h], bt = a.beta[(row0 + t) * a.nv + h];
-        const int64_t vo = ((row0 + t) * a.nv + h) * static_cast<int64_t>(a.dv) + dv0 + r;
-        float x = 0.f, o = 0.f;
-#pragma unroll
-        for (int i = 0; i < DK / 16; ++i) {
-          kv[i] *= fk;
-          qv[i] *= fq;
-          x = fmaf(S[i], kv[i], x);
-        }
-        const float u = bt * (load_scalar<ACT>(a.v, vo) - al * sum16(x));
-#pragma unroll
-        for (int i = 0; i < DK / 16; ++i) {
-          S[i] = fmaf(u, kv[i], al * S[i]);
-          o = fmaf(S[i], qv[i], o);
-        }
-        o = sum16(o);
-        if (n16 == 0) {
-          if constexpr (OUT == kF32) static_cast<float*>(a.out)[vo] = o;
-          else static_cast<uint16_t*>(a.out)[vo] = f32_to_bf16(o);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < DK / 16; ++i) Ss[r * kLs + n16 * (DK / 16) + i] = S[i];
+    const float* vec = reinterpret_cast<const float*>(a.ws + (slot_of(a, b, begin, c) * a.nv + h) * slot_bytes(kF32));
+    const float* slot_p = vec + kVec;
+    if (vec[2 * kC + 1] != 0.f) {
+      chunk_by_token<DK, ACT, OUT>(a, Ss, kLs, row0, len, h, kh, dv0, lane, w);
       __syncthreads();
       continue;
     }
@@ -369,15 +743,15 @@ __global__ __launch_bounds__(256) void k_gdc_scan(GdcArgs a) {
     for (int r = 0; r < 4; ++r) {
       const int i = 16 * w + 4 * g + r;
       const float v = i < len ? load_scalar<ACT>(a.v, ((row0 + i) * a.nv + h) * static_cast<int64_t>(a.dv) + dv0 + n16) : 0.f;
-      x[r] = v - slot_p[2 * kSlotMat + i] * ks[r];
-      qs[r] *= slot_p[2 * kSlotMat + kC + i];
+      x[r] = v - vec[i] * ks[r];
+      qs[r] *= vec[kC + i];
     }
     *reinterpret_cast<f32x4*>(Xs + n16 * kLx + 16 * w + 4 * g) = x;
     __syncthreads();
     f32x4 zt = {0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s <= w; ++s) {
       const f32x4 Tz = *reinterpret_cast<const f32x4*>(slot_p + (16 * w + n16) * kC + 16 * s + 4 * g);
-      const f32x4 To = *reinterpret_cast<const f32x4*>(slot_p + kSlotMat + (16 * w + n16) * kC + 16 * s + 4 * g);
+      const f32x4 To = *reinterpret_cast<const f32x4*>(slot_p + kC * kC + (16 * w + n16) * kC + 16 * s + 4 * g);
       const f32x4 Xb = *reinterpret_cast<const f32x4*>(Xs + n16 * kLx + 16 * s + 4 * g);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -397,7 +771,7 @@ __global__ __launch_bounds__(256) void k_gdc_scan(GdcArgs a) {
     }
     __syncthreads();
     // S^T, the columns of this wave
-    const float gc = slot_p[2 * kSlotMat + 2 * kC];
+    const float gc = vec[2 * kC];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int d0 = 16 * (NT * w + t);
@@ -457,7 +831,7 @@ struct GdcPlan {
 
 GdcPlan plan(const gdn_desc* d, int32_t B, int32_t N) {
   GdcPlan p;
-  const int64_t each = static_cast<int64_t>(d->n_v_heads) * kSlotFloats * 4;
+  const int64_t each = static_cast<int64_t>(d->n_v_heads) * slot_bytes(d->act_dtype);
   const int64_t all = static_cast<int64_t>(N) / kC + B;
   if (all * each <= kPassBytes || all <= B) {
     p.per_pass = 0;
@@ -472,11 +846,17 @@ GdcPlan plan(const gdn_desc* d, int32_t B, int32_t N) {
   return p;
 }
 
-template <int DK, int ACT>
-void launch(const GdcArgs& a, int out, uint32_t prep, uint32_t scan, hipStream_t s) {
-  if (prep > 0) launch_kernel(k_gdc_prep<DK, ACT>, dim3(prep), dim3(256), 0, s, a);
-  if (out == MOE_F32) launch_kernel(k_gdc_scan<DK, ACT, kF32>, dim3(scan), dim3(256), 0, s, a);
-  else launch_kernel(k_gdc_scan<DK, ACT, kBF16>, dim3(scan), dim3(256), 0, s, a);
+template <int DK>
+void launch(const GdcArgs& a, const gdn_desc* d, uint32_t prep, uint32_t scan, hipStream_t s) {
+  if (d->act_dtype == MOE_F32) {
+    if (prep > 0) launch_kernel(k_gdc_prep<DK, kF32>, dim3(prep), dim3(256), 0, s, a);
+    if (d->out_dtype == MOE_F32) launch_kernel(k_gdc_scan_f32<DK, kF32>, dim3(scan), dim3(256), 0, s, a);
+    else launch_kernel(k_gdc_scan_f32<DK, kBF16>, dim3(scan), dim3(256), 0, s, a);
+  } else {
+    if (prep > 0) launch_kernel(k_gdc_prep<DK, kBF16>, dim3(prep), dim3(256), 0, s, a);
+    if (d->out_dtype == MOE_F32) launch_kernel(k_gdc_scan_bf16<DK, kF32>, dim3(scan), dim3(256), 0, s, a);
+    else launch_kernel(k_gdc_scan_bf16<DK, kBF16>, dim3(scan), dim3(256), 0, s, a);
+  }
 }
 
 }  // namespace
@@ -532,25 +912,20 @@ extern "C" int gdn_chunk_forward(const gdn_desc* d, int32_t B, int32_t N, int32_
   a.cu = cu;
   a.q = q; a.k = k; a.v = v; a.alpha = alpha; a.beta = beta;
   a.state_in = state_in; a.state_out = state_out; a.out = out;
-  a.ws = static_cast<float*>(workspace);
+  a.ws = static_cast<uint8_t*>(workspace);
   a.B = B; a.N = N; a.T_max = T_max < N ? T_max : N;
   a.nk = d->n_k_heads; a.nv = d->n_v_heads; a.dv = d->d_v;
   a.scale = d->scale; a.eps = d->eps;
   a.per_pass = p.per_pass;
   a.slots = p.slots;
-  const int64_t scan = static_cast<int64_t>(B) * d->n_v_heads * (d->d_v / kRowsS), prep = static_cast<int64_t>(p.slots) * d->n_v_heads;
+  const int64_t scan = (static_cast<int64_t>(B) * d->n_v_heads + 7) / 8 * 8 * (d->d_v / kRowsS), prep = static_cast<int64_t>(p.slots) * d->n_v_heads;
   if (scan >= (1 << 24) || prep >= (1 << 24)) return bad("B=%lld sequences of N=%lld tokens are too many blocks for one launch", B, N);
   const int chunks = (a.T_max + kC - 1) / kC;
   hipStream_t s = static_cast<hipStream_t>(stream);
   for (a.first = 0; a.first == 0 || a.first < chunks; a.first += a.per_pass) {
     const uint32_t np = chunks > 0 ? static_cast<uint32_t>(prep) : 0u, nb = static_cast<uint32_t>(scan);
-    if (d->d_k == 128) {
-      if (d->act_dtype == MOE_F32) launch<128, kF32>(a, d->out_dtype, np, nb, s);
-      else launch<128, kBF16>(a, d->out_dtype, np, nb, s);
-    } else {
-      if (d->act_dtype == MOE_F32) launch<64, kF32>(a, d->out_dtype, np, nb, s);
-      else launch<64, kBF16>(a, d->out_dtype, np, nb, s);
-    }
+    if (d->d_k == 128) launch<128>(a, d, np, nb, s);
+    else launch<64>(a, d, np, nb, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) {
       char buf[256];
