@@ -29,7 +29,7 @@ HIP_FLAGS = [
 
 # Kernels whose sums are both products' results and scaled in between: kept in the
 # ordinary registers (the accumulation registers cost a move each way per value).
-FILE_FLAGS = {"attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+FILE_FLAGS = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for f in ("attention.hip", "gdn_chunk.hip")}
 
 
 def hipcc() -> str:

@@ -371,6 +371,11 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_few(AttnArgs a) {
 #pragma unroll
     for (int s = 0; s < KS; ++s) Q[t][s] = __builtin_bit_cast(bf16x8, load16(q + 32 * s + 8 * g) ^ a.flip);
   }
+  // waited for here: a wait in the loop would be for the direct loads as well
+#pragma unroll
+  for (int t = 0; t < RT; ++t)
+#pragma unroll
+    for (int s = 0; s < KS; ++s) asm volatile("" : "+v"(Q[t][s]));
   f32x4 O[RT][DT];
   float m[RT], l[RT];
 #pragma unroll
@@ -689,10 +694,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_tile(AttnArgs a)
 #pragma unroll
     for (int s = 0; s < KS; ++s) Q[s] = __builtin_bit_cast(bf16x8, load16(q + 16 * s + 8 * g) ^ a.flip);
   }
-  // 256 dims: Q in accumulation registers, so that O, which is scaled, stays in the others
-  if constexpr (D == 256)
+  // Q is waited for here: a wait in the loop would be for the direct loads as well.
+  // 256 dims: in accumulation registers, so that O, which is scaled, stays in the others.
 #pragma unroll
-    for (int s = 0; s < KS; ++s) asm volatile("" : "+a"(Q[s]));
+  for (int s = 0; s < KS; ++s) {
+    if constexpr (D == 256) asm volatile("" : "+a"(Q[s]));
+    else asm volatile("" : "+v"(Q[s]));
+  }
   f32x16 O[DT];
 #pragma unroll
   for (int d = 0; d < DT; ++d)

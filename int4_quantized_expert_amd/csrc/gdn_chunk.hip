@@ -17,6 +17,8 @@
 // which fp32 activations run on.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <type_traits>
@@ -31,18 +33,24 @@ namespace {
 
 constexpr int kC = 64;                        // tokens a chunk
 constexpr int kRowsS = 16;                    // state rows a block
-constexpr int64_t kPassBytes = int64_t(256) << 20;   // workspace a pass may take
+constexpr int64_t kPassBytes = int64_t(512) << 20;   // workspace a pass may take
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // One chunk and value head in the workspace: the row factors e, f, then g_C and
 // whether the chunk runs token by token; the two matrices.  For fp32 activations
-// they are rows of fp32; for bf16 three planes of bf16 as the matrix unit's
+// they are rows of fp32; for bf16 planes of bf16 as the matrix unit's
 // operand has them, 16 rows by 32 columns a kilobyte, those that lie above the
-// diagonal left out.
+// diagonal left out (rows in the order of token_of).
 constexpr int kVec = 4 * kC;                  // floats
-constexpr int kPieces = 6;                    // (rows 0, 16, 32, 48 by columns 0; 32, 48 by 32)
-constexpr int kMatF32 = kC * kC * 4, kMatBf16 = 3 * kPieces * 1024;
-constexpr int slot_bytes(int act) { return kVec * 4 + 2 * (act == kF32 ? kMatF32 : kMatBf16); }
+constexpr int kPieces = 6;                    // (tiles 0 .. 3 by columns 0; 2, 3 by 32)
+constexpr int kMatF32 = kC * kC * 4, kMatBf16 = kPieces * 1024;   // of one plane
+// Planes of the O-matrix, and of S in Q S^T: outputs in bf16 keep 8 bits, so two.
+constexpr int o_planes(int out) { return out == kF32 ? 3 : 2; }
+constexpr int slot_bytes(int act, int out) { return kVec * 4 + (act == kF32 ? 2 * kMatF32 : (3 + o_planes(out)) * kMatBf16); }
+// Row m of tile i is this token of the chunk: the eight values that a lane holds
+// of the results of two tiles are then eight tokens in a row, which is the
+// operand of the next product as it stands.
+__host__ __device__ constexpr int token_of(int tile, int m) { return 32 * (tile >> 1) + 8 * (m >> 2) + 4 * (tile & 1) + (m & 3); }
 __host__ __device__ constexpr int piece_of(int tile, int step) { return tile < 2 ? tile : 2 * tile - 2 + step; }
 
 struct GdcArgs {
@@ -97,12 +105,34 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// x as the sum of three bf16.
-__device__ __forceinline__ void split3(float x, __bf16& a, __bf16& b, __bf16& c) {
-  a = static_cast<__bf16>(x);
-  const float r = x - static_cast<float>(a);
-  b = static_cast<__bf16>(r);
-  c = static_cast<__bf16>(r - static_cast<float>(b));
+// Two values as the sums of three bf16 each, a word a plane.
+__device__ __forceinline__ void split3(float x, float y, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const auto step = [&]() {
+    const uint32_t p = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x, y}), bf16x2));
+    x -= __uint_as_float(p << 16);
+    y -= __uint_as_float(p & 0xffff0000u);
+    return p;
+  };
+  p0 = step();
+  p1 = step();
+  p2 = step();
+}
+
+// Eight values, four of each argument, as an operand in three planes.
+__device__ __forceinline__ void split3(const f32x4& lo, const f32x4& hi, bf16x8 (&p)[3]) {
+  u32x4 w[3];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t a0, a1, a2;
+    split3(lo[2 * i], lo[2 * i + 1], a0, a1, a2);
+    w[0][i] = a0; w[1][i] = a1; w[2][i] = a2;
+    split3(hi[2 * i], hi[2 * i + 1], a0, a1, a2);
+    w[0][2 + i] = a0; w[1][2 + i] = a1; w[2][2 + i] = a2;
+  }
+#pragma unroll
+  for (int x = 0; x < 3; ++x) p[x] = __builtin_bit_cast(bf16x8, w[x]);
 }
 
 // The part of a row of K or Q that a lane feeds to a product over 32 (bf16) or
@@ -119,7 +149,7 @@ __device__ __forceinline__ f32x4 dot_step(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-template <int DK, int ACT>
+template <int DK, int ACT, int OUT>
 __global__ __launch_bounds__(256) void k_gdc_prep(GdcArgs a) {
   constexpr int kSize = ACT == kF32 ? 4 : 2;
   constexpr int kRow = DK * kSize + 16;          // bytes of a row of K or Q in LDS
@@ -221,7 +251,7 @@ __global__ __launch_bounds__(256) void k_gdc_prep(GdcArgs a) {
   }
   if (!fine) odd = 1;
   __syncthreads();
-  uint8_t* const out = a.ws + (static_cast<int64_t>(slot) * a.nv + h) * slot_bytes(ACT);
+  uint8_t* const out = a.ws + (static_cast<int64_t>(slot) * a.nv + h) * slot_bytes(ACT, OUT);
   float* const vec = reinterpret_cast<float*>(out);
   if (odd) {
     if (tid == 0) vec[2 * kC + 1] = 1.f;
@@ -326,43 +356,37 @@ __global__ __launch_bounds__(256) void k_gdc_prep(GdcArgs a) {
     for (int r = 0; r < 4; ++r) PT[(16 * bi + 4 * g + r) * kLd + 16 * bj + n16] = o[r];
   }
   __syncthreads();
-  // both matrices out, row tile w, scaled by w_i and beta_j
+  // both matrices out, 16 rows a wave, scaled by w_i and beta_j
   {
-    const int i = 16 * w + n16;
+    const int i = ACT == kF32 ? 16 * w + n16 : token_of(w, n16);
     const float wi = exp2f(static_cast<float>(Lg[kC - 1] - Lg[i])) * rk[i];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       if (ACT == kBF16 && s > w / 2) continue;
-      float tz[8], to[8];
+      f32x4 tz[2], to[2];
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
         const int j = 32 * s + 8 * g + x;
         const bool in = j <= i;
-        tz[x] = in ? wi * Ts[i * kLd + j] * be[j] : 0.f;
-        to[x] = in ? PT[i * kLd + j] * be[j] : 0.f;
+        tz[x / 4][x % 4] = in ? wi * Ts[i * kLd + j] * be[j] : 0.f;
+        to[x / 4][x % 4] = in ? PT[i * kLd + j] * be[j] : 0.f;
       }
       if constexpr (ACT == kF32) {
         float* m = vec + kVec + i * kC + 32 * s + 8 * g;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          *reinterpret_cast<f32x4*>(m + 4 * x) = f32x4{tz[4 * x], tz[4 * x + 1], tz[4 * x + 2], tz[4 * x + 3]};
-          *reinterpret_cast<f32x4*>(m + kC * kC + 4 * x) = f32x4{to[4 * x], to[4 * x + 1], to[4 * x + 2], to[4 * x + 3]};
+          *reinterpret_cast<f32x4*>(m + 4 * x) = tz[x];
+          *reinterpret_cast<f32x4*>(m + kC * kC + 4 * x) = to[x];
         }
       } else {
         bf16x8 z[3], o[3];
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          __bf16 p0, p1, p2;
-          split3(tz[x], p0, p1, p2);
-          z[0][x] = p0; z[1][x] = p1; z[2][x] = p2;
-          split3(to[x], p0, p1, p2);
-          o[0][x] = p0; o[1][x] = p1; o[2][x] = p2;
-        }
-        uint8_t* m = out + kVec * 4 + piece_of(w, s) * 3 * 1024 + lane * 16;
+        split3(tz[0], tz[1], z);
+        split3(to[0], to[1], o);
+        uint8_t* m = out + kVec * 4 + piece_of(w, s) * 1024 + lane * 16;   // [plane][piece]
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
-          *reinterpret_cast<bf16x8*>(m + x * 1024) = z[x];
-          *reinterpret_cast<bf16x8*>(m + kMatBf16 + x * 1024) = o[x];
+          *reinterpret_cast<bf16x8*>(m + x * kMatBf16) = z[x];
+          if (x < o_planes(OUT)) *reinterpret_cast<bf16x8*>(m + (3 + x) * kMatBf16) = o[x];
         }
       }
     }
@@ -438,14 +462,27 @@ struct Scan {
 
 // The blocks of a head, which read the same matrices, go to one XCD (blocks
 // are dealt out in turns over eight).
+template <int WIDTH>
 __device__ __forceinline__ bool find_scan(const GdcArgs& a, int dk, Scan& s) {
-  const int nz = a.dv / kRowsS;
+  const int nz = (a.dv + WIDTH - 1) / WIDTH;
   const int q = blockIdx.x / 8;
   const int bh = (q / nz) * 8 + blockIdx.x % 8;
   if (bh >= a.B * a.nv) return false;
-  s.dv0 = (q % nz) * kRowsS;
+  s.dv0 = (q % nz) * WIDTH;
   s.h = bh % a.nv;
   s.b = bh / a.nv;
+  // the longest sequences first, where a wave holds all of them: theirs are the last to end
+  if (a.B > 1 && a.B <= kWave) {
+    const int lane = threadIdx.x & (kWave - 1);
+    int begin, n = -1, rank = 0;
+    if (lane < a.B) sequence(a, lane, begin, n);
+    for (int j = 0; j < a.B; ++j) {
+      const int o = __builtin_amdgcn_readlane(n, j);
+      rank += o > n || (o == n && j < lane);
+    }
+    const uint64_t hit = __ballot(lane < a.B && rank == s.b);
+    s.b = __builtin_ctzll(hit);
+  }
   s.kh = s.h / (a.nv / a.nk);
   sequence(a, s.b, s.begin, s.n);
   s.state = (static_cast<int64_t>(s.b) * a.nv + s.h) * a.dv * static_cast<int64_t>(dk) + static_cast<int64_t>(s.dv0) * dk;
@@ -455,12 +492,13 @@ __device__ __forceinline__ bool find_scan(const GdcArgs& a, int dk, Scan& s) {
   return s.c0 == 0 || s.c0 < s.c1;             // else done in an earlier pass
 }
 
-// bf16 activations.  Wave w has tokens 16 w .. 16 w + 15 of a chunk in the first
-// two products and state columns DK / 4 w .. in the third; S, X and Zt pass from
-// one to the next through LDS, split in three.  What a product takes of the next
-// chunk is requested as soon as it is done with this one's.
+// bf16 activations, few heads: four waves share 16 rows of a state.  Wave w has
+// the tokens of tile w of a chunk in the first two products and state columns
+// DK / 4 w .. in the third; S, X and Zt pass from one to the next through LDS, split
+// in three.  What a product takes of the next chunk is requested a chunk ahead.
 template <int DK, int OUT>
-__global__ __launch_bounds__(256, 2) void k_gdc_scan_bf16(GdcArgs a) {
+__global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
+  constexpr int OP = o_planes(OUT);
   constexpr int KS = DK / 32;                  // steps of 32 state columns
   constexpr int NT = DK / 64;                  // tiles of 16 state columns a wave
   constexpr int kLs = DK + 4;
@@ -474,7 +512,7 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_bf16(GdcArgs a) {
   const int lane = threadIdx.x & (kWave - 1), w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int n16 = lane & 15, g = lane >> 4;
   Scan sc;
-  if (!find_scan(a, DK, sc)) return;
+  if (!find_scan<kRowsS>(a, DK, sc)) return;
   // Pieces of 16 bytes turned by their row against bank conflicts: rows of S
   // (256 or 128 bytes), of X and Zt (128), and of K (read by rows and, four rows of
   // 32 bytes at once, transposed).
@@ -491,27 +529,20 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_bf16(GdcArgs a) {
   const auto put_s = [&]() {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      bf16x4 p[3];
+      uint32_t p[3], q[3];
+      split3(S[t][0], S[t][1], p[0], p[1], p[2]);
+      split3(S[t][2], S[t][3], q[0], q[1], q[2]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        __bf16 x, y, z;
-        split3(S[t][i], x, y, z);
-        p[0][i] = x; p[1][i] = y; p[2][i] = z;
-      }
-#pragma unroll
-      for (int x = 0; x < 3; ++x) *reinterpret_cast<bf16x4*>(Sp + x * kPlaneS + s_at(n16, 16 * (NT * w + t) + 4 * g)) = p[x];
+      for (int x = 0; x < 3; ++x) *reinterpret_cast<uint2*>(Sp + x * kPlaneS + s_at(n16, 16 * (NT * w + t) + 4 * g)) = uint2{p[x], q[x]};
     }
   };
+  const int t4 = token_of(w, 4 * g);           // this lane's four tokens of a result
   const auto put_x = [&](uint8_t* to, const f32x4& v) {
-    bf16x4 p[3];
+    uint32_t p[3], q[3];
+    split3(v[0], v[1], p[0], p[1], p[2]);
+    split3(v[2], v[3], q[0], q[1], q[2]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      __bf16 x, y, z;
-      split3(v[i], x, y, z);
-      p[0][i] = x; p[1][i] = y; p[2][i] = z;
-    }
-#pragma unroll
-    for (int x = 0; x < 3; ++x) *reinterpret_cast<bf16x4*>(to + x * kPlaneX + x_at(n16, 16 * w + 4 * g)) = p[x];
+    for (int x = 0; x < 3; ++x) *reinterpret_cast<uint2*>(to + x * kPlaneX + x_at(n16, t4)) = uint2{p[x], q[x]};
   };
 
   const int64_t st = static_cast<int64_t>(a.nk) * DK;
@@ -525,11 +556,15 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_bf16(GdcArgs a) {
     return static_cast<int64_t>(sc.begin) + (at < sc.n ? at : sc.n - 1);
   };
   u32x4 Kn[kKl];
-  bf16x8 Q[KS], Tz[2][3], To[2][3];
-  uint32_t V[4];                               // as stored: converted where it is used, or the load would be waited for here
-  f32x4 e, f;
-  float2 gc;                                   // g_C, and whether the chunk runs token by token
-  const auto slot = [&](int c) { return a.ws + (slot_of(a, sc.b, sc.begin, c) * a.nv + sc.h) * slot_bytes(kBF16); };
+  bf16x8 Tz[2][3], To[2][OP];
+  struct First {                               // what the first product takes
+    bf16x8 Q[KS];
+    uint32_t V[4];                             // as stored: converted where it is used, or the load would be waited for here
+    f32x4 e, f;
+    float2 gc;                                 // g_C, and whether the chunk runs token by token
+  };
+  First even, odd;                             // by the chunk's number
+  const auto slot = [&](int c) { return a.ws + (slot_of(a, sc.b, sc.begin, c) * a.nv + sc.h) * slot_bytes(kBF16, OUT); };
   const auto ask_k = [&](int c) {
 #pragma unroll
     for (int i = 0; i < kKl; ++i) {
@@ -537,23 +572,23 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_bf16(GdcArgs a) {
       Kn[i] = load16(kb + row_of(c, p / kPer) * st + (p % kPer) * 8);
     }
   };
-  const auto put_k = [&](int c) {
+  const auto put_k = [&](int half) {
 #pragma unroll
     for (int i = 0; i < kKl; ++i) {
       const int p = threadIdx.x + 256 * i;
-      *reinterpret_cast<u32x4*>(Kp[c & 1] + k_at(p / kPer, p % kPer)) = Kn[i];
+      *reinterpret_cast<u32x4*>(Kp[half] + k_at(p / kPer, p % kPer)) = Kn[i];
     }
   };
-  const auto ask_first = [&](int c) {          // for the first product
-    const uint16_t* q = qb + row_of(c, 16 * w + n16) * st + 8 * g;
+  const auto ask_first = [&](int c, First& o) {
+    const uint16_t* q = qb + row_of(c, token_of(w, n16)) * st + 8 * g;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) Q[s] = __builtin_bit_cast(bf16x8, load16(q + 32 * s));
+    for (int s = 0; s < KS; ++s) o.Q[s] = __builtin_bit_cast(bf16x8, load16(q + 32 * s));
 #pragma unroll
-    for (int r = 0; r < 4; ++r) V[r] = vb[row_of(c, 16 * w + 4 * g + r) * vst];
+    for (int r = 0; r < 4; ++r) o.V[r] = vb[row_of(c, t4 + r) * vst];
     const float* vec = reinterpret_cast<const float*>(slot(c));
-    e = *reinterpret_cast<const f32x4*>(vec + 16 * w + 4 * g);
-    f = *reinterpret_cast<const f32x4*>(vec + kC + 16 * w + 4 * g);
-    gc = *reinterpret_cast<const float2*>(vec + 2 * kC);
+    o.e = *reinterpret_cast<const f32x4*>(vec + t4);
+    o.f = *reinterpret_cast<const f32x4*>(vec + kC + t4);
+    o.gc = *reinterpret_cast<const float2*>(vec + 2 * kC);
   };
   const auto ask_second = [&](int c) {         // for the second
     const uint8_t* m = slot(c) + kVec * 4 + lane * 16;
@@ -562,27 +597,29 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_bf16(GdcArgs a) {
       if (s <= w / 2)
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
-          Tz[s][x] = __builtin_bit_cast(bf16x8, load16(m + (piece_of(w, s) * 3 + x) * 1024));
-          To[s][x] = __builtin_bit_cast(bf16x8, load16(m + kMatBf16 + (piece_of(w, s) * 3 + x) * 1024));
+          Tz[s][x] = __builtin_bit_cast(bf16x8, load16(m + x * kMatBf16 + piece_of(w, s) * 1024));
+          if (x < OP) To[s][x] = __builtin_bit_cast(bf16x8, load16(m + (3 + x) * kMatBf16 + piece_of(w, s) * 1024));
         }
   };
   put_s();
   if (sc.c0 < sc.c1) {
     ask_k(sc.c0);
-    ask_first(sc.c0);
+    ask_first(sc.c0, even);
     ask_second(sc.c0);
-    put_k(sc.c0);
+    put_k(0);
   }
   __syncthreads();
-  for (int c = sc.c0; c < sc.c1; ++c) {
+  // chunk c, whose rows of K lie in stage `half`
+  const auto chunk = [&](int c, int half, const First& one, First& then) {
     const int64_t row0 = static_cast<int64_t>(sc.begin) + c * kC;
     const int len = sc.n - c * kC < kC ? sc.n - c * kC : kC;
     // requests without a condition (the last chunk asks for itself again), so that no copy of a register waits for one
     const int next = c + 1 < sc.c1 ? c + 1 : c;
-    const uint8_t* K = Kp[c & 1];
+    const uint8_t* K = Kp[half];
     ask_k(next);
-    const float gC = gc.x;
-    const bool by_token = __builtin_amdgcn_readfirstlane(__float_as_int(gc.y)) != 0;
+    ask_first(next, then);
+    const float gC = one.gc.x;
+    const bool by_token = __builtin_amdgcn_readfirstlane(__float_as_int(one.gc.y)) != 0;
     f32x4 qs = {0.f, 0.f, 0.f, 0.f};
     if (by_token) {
       // in fp32 through the place of S
@@ -600,23 +637,22 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_bf16(GdcArgs a) {
       f32x4 ks = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        const bf16x8 Ka = *reinterpret_cast<const bf16x8*>(K + k_at(16 * w + n16, 4 * s + g));
+        const bf16x8 Ka = *reinterpret_cast<const bf16x8*>(K + k_at(token_of(w, n16), 4 * s + g));
 #pragma unroll
         for (int x = 2; x >= 0; --x) {
           const bf16x8 Sb = *reinterpret_cast<const bf16x8*>(Sp + x * kPlaneS + s_at(n16, 32 * s + 8 * g));
           ks = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Ka, Sb, ks, 0, 0, 0);
-          qs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Q[s], Sb, qs, 0, 0, 0);
+          if (x < OP) qs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(one.Q[s], Sb, qs, 0, 0, 0);
         }
       }
       f32x4 x;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        x[r] = __uint_as_float(V[r] << 16) - e[r] * ks[r];
-        qs[r] *= f[r];
+        x[r] = __uint_as_float(one.V[r] << 16) - one.e[r] * ks[r];
+        qs[r] *= one.f[r];
       }
       put_x(Xp, x);
     }
-    ask_first(next);
     __syncthreads();
     if (!by_token) {
       // (Z-matrix) X and (O-matrix) X
@@ -632,7 +668,7 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_bf16(GdcArgs a) {
 #pragma unroll
             for (int z = 2 - y; z >= 0; --z) {
               zt = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Tz[s][z], Xb[y], zt, 0, 0, 0);
-              qs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(To[s][z], Xb[y], qs, 0, 0, 0);
+              if (z + y < OP) qs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(To[s][z], Xb[y], qs, 0, 0, 0);
             }
         }
       put_x(Zp, zt);
@@ -642,7 +678,7 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_bf16(GdcArgs a) {
     if (!by_token) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = 16 * w + 4 * g + r;
+        const int i = t4 + r;
         if (i < len) {
           const int64_t oi = ((row0 + i) * a.nv + sc.h) * static_cast<int64_t>(a.dv) + sc.dv0 + n16;
           if constexpr (OUT == kF32) static_cast<float*>(a.out)[oi] = qs[r];
@@ -678,12 +714,271 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_bf16(GdcArgs a) {
       }
     }
     put_s();
-    put_k(c + 1);
+    put_k(half ^ 1);
     __syncthreads();
+  };
+  for (int c = sc.c0; c < sc.c1; c += 2) {
+    chunk(c, 0, even, odd);
+    if (c + 1 < sc.c1) chunk(c + 1, 1, odd, even);
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t)
     *reinterpret_cast<f32x4*>(a.state_out + sc.state + n16 * DK + 16 * (NT * w + t) + 4 * g) = S[t];
+}
+
+// bf16 activations, many heads.  A wave walks the chunks with 16 rows of the state to itself,
+// all in registers: a product's result, four tokens (or columns) of a state row
+// a lane and tile, is split in three and is the next one's operand as it
+// stands, by the order of tokens and columns within two tiles (token_of).  The four
+// waves of a block, 64 rows of one head, share K, Q, V, the factors and the
+// matrices in LDS, where the next chunk's arrive by direct loads meanwhile: one
+// barrier a chunk.
+//
+// 216 products of 16 x 16 x 32 a chunk, 18 to 20 cycles each with their operands
+// from LDS, bound it; four waves that shared the tokens of 16 rows instead, passing
+// S, X and Zt through LDS with three barriers, took 1.5 times as long for one
+// sequence and 4 times for many.
+template <int DK, int OUT, int NW>
+struct ScanLds {
+  static constexpr int kK = 0, kQ = kC * DK * 2, kV = 2 * kC * DK * 2, kF = kV + kC * 16 * NW * 2, kM = kF + kVec * 4;
+  static constexpr int kStage = kM + (3 + o_planes(OUT)) * kMatBf16, kBytes = 2 * kStage;
+};
+
+template <int DK, int OUT, int NW>
+__global__ __launch_bounds__(64 * NW, NW / 4) void k_gdc_scan_bf16(GdcArgs a) {
+  using L = ScanLds<DK, OUT, NW>;
+  constexpr int OP = o_planes(OUT);
+  constexpr int KS = DK / 32;                  // steps of 32 state columns
+  constexpr int kPer = DK / 8;                 // 16-byte pieces of a row of K
+  constexpr int kRpl = 64 / kPer;              // rows a direct load
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & (kWave - 1), w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int n16 = lane & 15, g = lane >> 4;
+  Scan sc;
+  if (!find_scan<16 * NW>(a, DK, sc)) return;
+  const int dv0 = sc.dv0 + 16 * w;             // this wave's state rows
+  const bool idle = dv0 >= a.dv;               // none: it only fetches
+  // Pieces of K and Q are turned by their row, so that the 16 rows of a tile, and
+  // eight of the sixteen of a transposing read, fall into different banks.
+  const auto turn = [](int tok) { return DK == 128 ? (tok & 3) | ((tok >> 1) & 12) : (tok & 3) | ((tok >> 1) & 4); };
+
+  // this wave's rows of S^T: tile pair s, lane: row n16, columns 32 s + 8 g + 0 .. 3, then + 4 .. 7
+  f32x4 S[2 * KS];
+  const float* src = sc.c0 > 0 ? a.state_out : a.state_in;
+  const int64_t so = sc.state + static_cast<int64_t>(16 * w + n16) * DK;
+#pragma unroll
+  for (int t = 0; t < 2 * KS; ++t)
+    S[t] = src && !idle ? *reinterpret_cast<const f32x4*>(src + so + 32 * (t >> 1) + 8 * g + 4 * (t & 1)) : f32x4{0.f, 0.f, 0.f, 0.f};
+  // waited for here: a wait in the loop would be for the direct loads as well
+#pragma unroll
+  for (int t = 0; t < 2 * KS; ++t) asm volatile("" : "+v"(S[t]));
+
+  const int64_t st = static_cast<int64_t>(a.nk) * DK, vst = static_cast<int64_t>(a.nv) * a.dv;
+  const uint16_t* const kb = static_cast<const uint16_t*>(a.k) + static_cast<int64_t>(sc.begin) * st + static_cast<int64_t>(sc.kh) * DK;
+  const uint16_t* const qb = static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(sc.begin) * st + static_cast<int64_t>(sc.kh) * DK;
+  const uint16_t* const vb = static_cast<const uint16_t*>(a.v) + static_cast<int64_t>(sc.begin) * vst + static_cast<int64_t>(sc.h) * a.dv + sc.dv0;
+  const int vcols = a.dv - sc.dv0 < 16 * NW ? a.dv - sc.dv0 : 16 * NW;
+  // Load i of a wave is kilobyte NW i + w: of K and Q kRpl rows each, of V kRpv.
+  constexpr int kKq = kC / kRpl / NW, kRpv = 1024 / (32 * NW), kVl = kC / kRpv / NW, kMl = 1 + (3 + OP) * kPieces;
+  uint32_t koff[kKq], voff[kVl];
+#pragma unroll
+  for (int i = 0; i < kKq; ++i) {
+    const int row = (NW * i + w) * kRpl + lane / kPer;
+    koff[i] = static_cast<uint32_t>(row) * static_cast<uint32_t>(st) * 2u + (((lane % kPer) ^ turn(row)) << 4);
+  }
+#pragma unroll
+  for (int i = 0; i < kVl; ++i)
+    voff[i] = static_cast<uint32_t>((NW * i + w) * kRpv + lane / (2 * NW)) * static_cast<uint32_t>(vst) * 2u + (lane % (2 * NW)) * 16;
+  const auto length = [&](int c) { return sc.n - c * kC < kC ? sc.n - c * kC : kC; };
+  // The requests for a chunk, in parts: the memory unit takes 64 bytes a cycle, so
+  // all at once would hold the wave up.  The descriptors end with the last token:
+  // rows behind it arrive as zeros.
+  constexpr int kParts = 4;
+  const auto request = [&](int c, uint8_t* to, int part) {
+    const int len = length(c);
+    const int64_t r = static_cast<int64_t>(c) * kC;
+    if (part == 0) {
+      const u32x4 rk = raw_rsrc(kb + r * st, ((len - 1) * st + DK) * 2);
+#pragma unroll
+      for (int i = 0; i < kKq; ++i) lds_load<16>(rk, to + L::kK + (NW * i + w) * 1024, koff[i], 0);
+    } else if (part == 1) {
+      const u32x4 rq = raw_rsrc(qb + r * st, ((len - 1) * st + DK) * 2), rv = raw_rsrc(vb + r * vst, ((len - 1) * vst + vcols) * 2);
+#pragma unroll
+      for (int i = 0; i < kKq; ++i) lds_load<16>(rq, to + L::kQ + (NW * i + w) * 1024, koff[i], 0);
+#pragma unroll
+      for (int i = 0; i < kVl; ++i) lds_load<16>(rv, to + L::kV + (NW * i + w) * 1024, voff[i], 0);
+    } else {
+      // the factors and the matrices lie as they do in the slot
+      const u32x4 rm = raw_rsrc(a.ws + (slot_of(a, sc.b, sc.begin, c) * a.nv + sc.h) * slot_bytes(kBF16, OUT), slot_bytes(kBF16, OUT));
+      constexpr int kEach = (kMl + NW - 1) / NW, kHalf = kEach / 2;
+#pragma unroll
+      for (int i = part == 2 ? 0 : kHalf; i < (part == 2 ? kHalf : kEach); ++i)
+        if (NW * i + w < kMl) lds_load<16>(rm, to + L::kF + (NW * i + w) * 1024, lane * 16, (NW * i + w) * 1024);
+    }
+  };
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  const auto transposed = [&](const uint8_t* p) { return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p)); };
+
+  int stage = 0, c = sc.c0;
+  if (c < sc.c1)
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) request(c, smem, i);
+  uint8_t* in = smem;
+  // waits for chunk c; whether it runs token by token
+  const auto arrive = [&]() {
+    in = smem + stage * L::kStage;
+    stage ^= 1;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();                           // the chunk is there, and nobody reads the other stage any more
+    return __builtin_amdgcn_readfirstlane(__float_as_int(reinterpret_cast<const float*>(in + L::kF)[2 * kC + 1])) != 0;
+  };
+  const uint32_t ooff = (static_cast<uint32_t>(8 * g) * static_cast<uint32_t>(vst) + n16) * (OUT == kF32 ? 4u : 2u);
+  for (; c < sc.c1; ++c) {
+    // chunk after chunk as matrix products ...
+    bool by_token = false;
+    for (; c < sc.c1; ++c) {
+    by_token = arrive();
+    if (by_token) break;
+    const bool more = c + 1 < sc.c1;
+    uint8_t* const other = smem + stage * L::kStage;
+    if (idle) {
+      if (more)
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) request(c + 1, other, i);
+      continue;
+    }
+    const float* const vec = reinterpret_cast<const float*>(in + L::kF);
+    const int len = length(c);
+    // K S^T and Q S^T
+    bf16x8 Sp[KS][3];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) split3(S[2 * s], S[2 * s + 1], Sp[s]);
+    f32x4 ks[4], o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ks[i] = o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const int tok = token_of(i, n16);
+      if (more) request(c + 1, other, i);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const int off = tok * DK * 2 + (((4 * s + g) ^ turn(tok)) << 4);
+        const bf16x8 Ka = *reinterpret_cast<const bf16x8*>(in + L::kK + off), Qa = *reinterpret_cast<const bf16x8*>(in + L::kQ + off);
+#pragma unroll
+        for (int x = 2; x >= 0; --x) {
+          ks[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Ka, Sp[s][x], ks[i], 0, 0, 0);
+          if (x < OP) o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Qa, Sp[s][x], o[i], 0, 0, 0);
+        }
+      }
+    }
+    // X: tokens 8 g + 0 .. 3 and 4 .. 7 of each half of the chunk
+    bf16x8 Xp[2][3];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      f32x4 x[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int tok = 32 * s + 8 * g + 4 * y;
+        const bf16x4 v = transposed(in + L::kV + (tok + (n16 >> 2)) * 32 * NW + (16 * w + 4 * (n16 & 3)) * 2);
+        const f32x4 e = *reinterpret_cast<const f32x4*>(vec + tok), f = *reinterpret_cast<const f32x4*>(vec + kC + tok);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[y][r] = static_cast<float>(v[r]) - e[r] * ks[2 * s + y][r];
+        o[2 * s + y] *= f;
+      }
+      split3(x[0], x[1], Xp[s]);
+    }
+    // (Z-matrix) X and (O-matrix) X, the smallest terms first
+    f32x4 z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      z[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s <= i / 2; ++s) {
+        const uint8_t* m = in + L::kM + piece_of(i, s) * 1024 + lane * 16;
+        bf16x8 Tz[3], To[OP];
+#pragma unroll
+        for (int x = 0; x < 3; ++x) Tz[x] = *reinterpret_cast<const bf16x8*>(m + x * kMatBf16);
+#pragma unroll
+        for (int x = 0; x < OP; ++x) To[x] = *reinterpret_cast<const bf16x8*>(m + (3 + x) * kMatBf16);
+#pragma unroll
+        for (int y = 2; y >= 0; --y)
+#pragma unroll
+          for (int x = 2 - y; x >= 0; --x) {
+            z[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Tz[x], Xp[s][y], z[i], 0, 0, 0);
+            if (x + y < OP) o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(To[x], Xp[s][y], o[i], 0, 0, 0);
+          }
+      }
+    }
+    {
+      // rows 32 s + 8 g + 4 y + r: a base for each (s, y, r), one offset for all
+      const int64_t osz = OUT == kF32 ? 4 : 2;
+      uint8_t* const ob = static_cast<uint8_t*>(a.out) +
+                          ((static_cast<int64_t>(sc.begin) + static_cast<int64_t>(c) * kC) * vst + static_cast<int64_t>(sc.h) * a.dv + dv0) * osz;
+      const auto store = [&](int i, int r) {
+        uint8_t* p = ob + (32 * (i >> 1) + 4 * (i & 1) + r) * vst * osz + ooff;
+        if constexpr (OUT == kF32) *reinterpret_cast<float*>(p) = o[i][r];
+        else *reinterpret_cast<uint16_t*>(p) = f32_to_bf16(o[i][r]);
+      };
+      if (len == kC) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) store(i, r);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (token_of(i, 4 * g + r) < len) store(i, r);
+      }
+    }
+    // S^T
+    bf16x8 Zp[2][3];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) split3(z[2 * s], z[2 * s + 1], Zp[s]);
+    const float gC = vec[2 * kC];
+#pragma unroll
+    for (int t = 0; t < 2 * KS; ++t) {
+      f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        bf16x8 Ka;                             // row m of the tile is column 32 (t / 2) + 8 (m / 4) + 4 (t % 2) + m % 4; tokens 32 s + 8 g ..
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int tok = 32 * s + 8 * g + 4 * y + (n16 >> 2);
+          const bf16x4 v = transposed(in + L::kK + tok * DK * 2 + (((4 * (t >> 1) + (n16 & 3)) ^ turn(tok)) << 4) + 8 * (t & 1));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) Ka[4 * y + i] = v[i];
+        }
+#pragma unroll
+        for (int x = 2; x >= 0; --x) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Ka, Zp[s][x], d, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[t][i] = fmaf(gC, S[t][i], d[i]);
+    }
+    }
+    if (!by_token) break;
+    // ... and one token by token, the state through its place in LDS
+    constexpr int kLs = DK + 4;
+    static_assert(NW * kRowsS * kLs * 4 <= L::kStage, "room for the states");
+    if (c + 1 < sc.c1)
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) request(c + 1, smem + stage * L::kStage, i);
+    __syncthreads();                           // every wave has seen the flag
+    float* Ss = reinterpret_cast<float*>(in) + w * kRowsS * kLs;
+    if (!idle) {
+#pragma unroll
+      for (int t = 0; t < 2 * KS; ++t) *reinterpret_cast<f32x4*>(Ss + n16 * kLs + 32 * (t >> 1) + 8 * g + 4 * (t & 1)) = S[t];
+      wave_sync_lds();
+      const int64_t row0 = static_cast<int64_t>(sc.begin) + static_cast<int64_t>(c) * kC;
+      for (int x = 0; x < 4; ++x) chunk_by_token<DK, kBF16, OUT>(a, Ss, kLs, row0, length(c), sc.h, sc.kh, dv0, lane, x);
+      wave_sync_lds();
+#pragma unroll
+      for (int t = 0; t < 2 * KS; ++t) S[t] = *reinterpret_cast<const f32x4*>(Ss + n16 * kLs + 32 * (t >> 1) + 8 * g + 4 * (t & 1));
+    }
+  }
+  if (!idle)
+#pragma unroll
+    for (int t = 0; t < 2 * KS; ++t) *reinterpret_cast<f32x4*>(a.state_out + so + 32 * (t >> 1) + 8 * g + 4 * (t & 1)) = S[t];
 }
 
 // fp32 activations, on the fp32 matrix instruction.
@@ -700,7 +995,7 @@ __global__ __launch_bounds__(256) void k_gdc_scan_f32(GdcArgs a) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave;
   const int n16 = lane & 15, g = lane >> 4;
   Scan sc;
-  if (!find_scan(a, DK, sc)) return;
+  if (!find_scan<kRowsS>(a, DK, sc)) return;
   const int h = sc.h, kh = sc.kh, b = sc.b, begin = sc.begin, n = sc.n, c0 = sc.c0, c1 = sc.c1, dv0 = sc.dv0;
   const int64_t so = sc.state;
   const float* src = c0 > 0 ? a.state_out : a.state_in;
@@ -715,7 +1010,7 @@ __global__ __launch_bounds__(256) void k_gdc_scan_f32(GdcArgs a) {
     const int t0 = c * kC;
     const int len = n - t0 < kC ? n - t0 : kC;
     const int64_t row0 = static_cast<int64_t>(begin) + t0;
-    const float* vec = reinterpret_cast<const float*>(a.ws + (slot_of(a, b, begin, c) * a.nv + h) * slot_bytes(kF32));
+    const float* vec = reinterpret_cast<const float*>(a.ws + (slot_of(a, b, begin, c) * a.nv + h) * slot_bytes(kF32, OUT));
     const float* slot_p = vec + kVec;
     if (vec[2 * kC + 1] != 0.f) {
       chunk_by_token<DK, ACT, OUT>(a, Ss, kLs, row0, len, h, kh, dv0, lane, w);
@@ -831,7 +1126,7 @@ struct GdcPlan {
 
 GdcPlan plan(const gdn_desc* d, int32_t B, int32_t N) {
   GdcPlan p;
-  const int64_t each = static_cast<int64_t>(d->n_v_heads) * slot_bytes(d->act_dtype);
+  const int64_t each = static_cast<int64_t>(d->n_v_heads) * slot_bytes(d->act_dtype, d->out_dtype);
   const int64_t all = static_cast<int64_t>(N) / kC + B;
   if (all * each <= kPassBytes || all <= B) {
     p.per_pass = 0;
@@ -846,17 +1141,74 @@ GdcPlan plan(const gdn_desc* d, int32_t B, int32_t N) {
   return p;
 }
 
-template <int DK>
-void launch(const GdcArgs& a, const gdn_desc* d, uint32_t prep, uint32_t scan, hipStream_t s) {
-  if (d->act_dtype == MOE_F32) {
-    if (prep > 0) launch_kernel(k_gdc_prep<DK, kF32>, dim3(prep), dim3(256), 0, s, a);
-    if (d->out_dtype == MOE_F32) launch_kernel(k_gdc_scan_f32<DK, kF32>, dim3(scan), dim3(256), 0, s, a);
-    else launch_kernel(k_gdc_scan_f32<DK, kBF16>, dim3(scan), dim3(256), 0, s, a);
-  } else {
-    if (prep > 0) launch_kernel(k_gdc_prep<DK, kBF16>, dim3(prep), dim3(256), 0, s, a);
-    if (d->out_dtype == MOE_F32) launch_kernel(k_gdc_scan_bf16<DK, kF32>, dim3(scan), dim3(256), 0, s, a);
-    else launch_kernel(k_gdc_scan_bf16<DK, kBF16>, dim3(scan), dim3(256), 0, s, a);
+// Whether two stages of a block of eight waves fit the LDS of a CU.
+template <int DK, int OUT>
+constexpr bool kHasWide = ScanLds<DK, OUT, 8>::kBytes <= 160 * 1024;
+
+// Launch with dynamic LDS, whose size is set once per kernel and device.
+template <void (*KERNEL)(GdcArgs), int BYTES, int NW>
+bool launch_scan(const GdcArgs& a, uint32_t blocks, hipStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) return false;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!bit || !(done.load(std::memory_order_relaxed) & bit)) {
+    if (hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize, BYTES) != hipSuccess)
+      return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
   }
+  launch_kernel(KERNEL, dim3(blocks), dim3(64 * NW), BYTES, s, a);
+  return true;
+}
+
+// State rows a block of the scan takes.  A chunk takes a block of 16 rows 3.3 us
+// (two on a CU; 2.4 alone), one of 64 rows 4.3 and one of 128 rows 6.6 (128 x 128
+// states, one on a CU).  The longest sequence's chunks run one after the other, and
+// all of them share the chip: the larger of the two is what a width takes, and the
+// smallest wins.  1, 2, 3, 4 and 8 sequences of 1024 tokens by 32 heads: 16 rows 40,
+// 53, 99, 106 and 208 us; 64 rows 66, 67, 70, 72 and 140; 128 rows 105 each.
+int scan_width(const gdn_desc* d, int32_t B, int32_t N, int T_max) {
+  if (d->act_dtype == MOE_F32) return kRowsS;
+  const bool fits = d->d_k == 64 ? kHasWide<64, kF32> : (d->out_dtype == MOE_F32 ? kHasWide<128, kF32> : kHasWide<128, kBF16>);
+  const double chain = (T_max + kC - 1) / kC, mean = static_cast<double>(N) / kC / B + 0.5, heads = static_cast<double>(B) * d->n_v_heads;
+  int best = kRowsS;
+  double least = 1e300;
+  for (const int w : {16, 64, 128}) {
+    if (w == 128 && (!fits || d->d_v <= 64)) continue;
+    const double t = w == 16 ? 3.3 : (w == 64 ? 4.3 : 6.6), slots = w == 16 ? 512 : 256;
+    const double blocks = heads * ((d->d_v + w - 1) / w);
+    const double one = w == 16 && blocks <= 256 ? 2.4 : t;
+    const double took = std::max(chain * one, std::ceil(blocks / slots) * mean * t);
+    if (took < least) {
+      least = took;
+      best = w;
+    }
+  }
+  return best;
+}
+
+template <int DK, int OUT>
+bool launch_out(const GdcArgs& a, bool f32, int width, uint32_t prep, uint32_t scan, hipStream_t s) {
+  if (f32) {
+    if (prep > 0) launch_kernel(k_gdc_prep<DK, kF32, OUT>, dim3(prep), dim3(256), 0, s, a);
+    launch_kernel(k_gdc_scan_f32<DK, OUT>, dim3(scan), dim3(256), 0, s, a);
+    return true;
+  }
+  if (prep > 0) launch_kernel(k_gdc_prep<DK, kBF16, OUT>, dim3(prep), dim3(256), 0, s, a);
+  if (width == kRowsS) {
+    launch_kernel(k_gdc_scan_few<DK, OUT>, dim3(scan), dim3(256), 0, s, a);
+    return true;
+  }
+  if constexpr (kHasWide<DK, OUT>)
+    if (width == 128) return launch_scan<k_gdc_scan_bf16<DK, OUT, 8>, ScanLds<DK, OUT, 8>::kBytes, 8>(a, scan, s);
+  return launch_scan<k_gdc_scan_bf16<DK, OUT, 4>, ScanLds<DK, OUT, 4>::kBytes, 4>(a, scan, s);
+}
+
+bool launch(const GdcArgs& a, const gdn_desc* d, int width, uint32_t prep, uint32_t scan, hipStream_t s) {
+  const bool f32 = d->act_dtype == MOE_F32;
+  if (d->d_k == 128)
+    return d->out_dtype == MOE_F32 ? launch_out<128, kF32>(a, f32, width, prep, scan, s) : launch_out<128, kBF16>(a, f32, width, prep, scan, s);
+  return d->out_dtype == MOE_F32 ? launch_out<64, kF32>(a, f32, width, prep, scan, s) : launch_out<64, kBF16>(a, f32, width, prep, scan, s);
 }
 
 }  // namespace
@@ -918,16 +1270,17 @@ extern "C" int gdn_chunk_forward(const gdn_desc* d, int32_t B, int32_t N, int32_
   a.scale = d->scale; a.eps = d->eps;
   a.per_pass = p.per_pass;
   a.slots = p.slots;
-  const int64_t scan = (static_cast<int64_t>(B) * d->n_v_heads + 7) / 8 * 8 * (d->d_v / kRowsS), prep = static_cast<int64_t>(p.slots) * d->n_v_heads;
+  const int width = scan_width(d, B, N, a.T_max);
+  const int64_t heads = static_cast<int64_t>(B) * d->n_v_heads;
+  const int64_t scan = (heads + 7) / 8 * 8 * ((d->d_v + width - 1) / width), prep = static_cast<int64_t>(p.slots) * d->n_v_heads;
   if (scan >= (1 << 24) || prep >= (1 << 24)) return bad("B=%lld sequences of N=%lld tokens are too many blocks for one launch", B, N);
   const int chunks = (a.T_max + kC - 1) / kC;
   hipStream_t s = static_cast<hipStream_t>(stream);
   for (a.first = 0; a.first == 0 || a.first < chunks; a.first += a.per_pass) {
     const uint32_t np = chunks > 0 ? static_cast<uint32_t>(prep) : 0u, nb = static_cast<uint32_t>(scan);
-    if (d->d_k == 128) launch<128>(a, d, np, nb, s);
-    else launch<64>(a, d, np, nb, s);
+    const bool sent = launch(a, d, width, np, nb, s);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) {
+    if (e != hipSuccess || !sent) {
       char buf[256];
       snprintf(buf, sizeof(buf), "chunked delta rule launch failed: %s", hipGetErrorString(e));
       return api_fail(MOE_EHIP, buf);

@@ -298,7 +298,7 @@ def test_several_passes():
     """More chunks than the workspace holds at once: passes over parts of every sequence, the state carried between them.  The
     same chunks by themselves give the same bits."""
     show("passes")
-    lens = [1200, 0, 3000, 64, 70]
+    lens = [4000, 0, 6000, 64, 70]
     c = Case(lens, 16, 256, 64, 16, "bf16", "bf16", seed=15)
     d = c.desc
     full = M.gdn_chunk_workspace_bytes(d, 1, 64)
