@@ -97,8 +97,15 @@ __device__ __forceinline__ f32x4 load4(const void* base, int64_t c) {
   }
 }
 
-__device__ __forceinline__ bool finite4(const f32x4& v) {
-  return isfinite(v[0]) && isfinite(v[1]) && isfinite(v[2]) && isfinite(v[3]);
+// Sum over the L lanes that hold a row; every lane ends with it.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x, int lane) {
+  x += __uint_as_float(lane_xor<1>(__float_as_uint(x), lane));
+  x += __uint_as_float(lane_xor<2>(__float_as_uint(x), lane));
+  x += __uint_as_float(lane_xor<4>(__float_as_uint(x), lane));
+  if constexpr (L > 8) x += __uint_as_float(lane_xor<8>(__float_as_uint(x), lane));
+  if constexpr (L > 16) x += __uint_as_float(lane_xor<16>(__float_as_uint(x), lane));
+  return x;
 }
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -160,7 +167,8 @@ __global__ __launch_bounds__(256) void k_gdc_prep(GdcArgs a) {
   constexpr int kKq = 2 * kC * kRow, kMats = 2 * kC * kLd * 4;
   __shared__ __align__(16) uint8_t kq[kKq > kMats ? kKq : kMats];
   __shared__ __align__(16) float As[kC * kLd];
-  __shared__ float rk[kC], rq[kC], be[kC];
+  __shared__ float rk[kC], rq[kC];
+  __shared__ __align__(16) float be[kC];
   __shared__ double Lg[kC];
   __shared__ int odd;
   const int tid = threadIdx.x, lane = tid & (kWave - 1), w = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -190,12 +198,55 @@ __global__ __launch_bounds__(256) void k_gdc_prep(GdcArgs a) {
   const int64_t row0 = static_cast<int64_t>(begin) + t0;
 
   if (tid == 0) odd = 0;
+  // everything that is read, requested at once
+  constexpr int kLoads = kC * kPer / 256;
+  const int64_t st = static_cast<int64_t>(a.nk) * DK;
+  u32x4 kv[kLoads], qv[kLoads];
+#pragma unroll
+  for (int x = 0; x < kLoads; ++x) {
+    const int i = tid + 256 * x, r = i / kPer;
+    const int64_t off = ((row0 + (r < len ? r : len - 1)) * st + static_cast<int64_t>(kh) * DK) * kSize + (i % kPer) * 16;
+    kv[x] = load16(static_cast<const uint8_t*>(a.k) + off);
+    qv[x] = load16(static_cast<const uint8_t*>(a.q) + off);
+  }
+  float al = 1.f, bt = 0.f;
+  if (w == 0 && lane < len) {
+    al = a.alpha[(row0 + lane) * a.nv + h];
+    bt = a.beta[(row0 + lane) * a.nv + h];
+  }
   __syncthreads();
   bool fine = true;
+  // K and Q into LDS, and the norms of their rows over the lanes that load one
+#pragma unroll
+  for (int x = 0; x < kLoads; ++x) {
+    const int i = tid + 256 * x, r = i / kPer, at = (i % kPer) * 16;
+    if (r >= len) kv[x] = qv[x] = u32x4{0, 0, 0, 0};
+    *reinterpret_cast<u32x4*>(kq + r * kRow + at) = kv[x];
+    *reinterpret_cast<u32x4*>(kq + kC * kRow + r * kRow + at) = qv[x];
+    float sk = 0.f, sq = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (ACT == kF32) {
+        sk = fmaf(__uint_as_float(kv[x][j]), __uint_as_float(kv[x][j]), sk);
+        sq = fmaf(__uint_as_float(qv[x][j]), __uint_as_float(qv[x][j]), sq);
+      } else {
+        const float k0 = __uint_as_float(kv[x][j] << 16), k1 = __uint_as_float(kv[x][j] & 0xffff0000u);
+        const float q0 = __uint_as_float(qv[x][j] << 16), q1 = __uint_as_float(qv[x][j] & 0xffff0000u);
+        sk = fmaf(k1, k1, fmaf(k0, k0, sk));
+        sq = fmaf(q1, q1, fmaf(q0, q0, sq));
+      }
+    }
+    sk = lanes_sum<kPer>(sk, lane);
+    sq = lanes_sum<kPer>(sq, lane);
+    const float rkv = 1.0f / sqrtf(sk + a.eps), rqv = a.scale / sqrtf(sq + a.eps);
+    // a row that is not finite has a norm that is not
+    fine = fine && (r >= len || (isfinite(sk) && isfinite(sq) && isfinite(rkv) && isfinite(rqv)));
+    if (i % kPer == 0) {
+      rk[r] = r < len ? rkv : 0.f;
+      rq[r] = r < len ? rqv : 0.f;
+    }
+  }
   if (w == 0) {                                // gates: logarithms summed in double precision
-    const bool in = lane < len;
-    const float al = in ? a.alpha[(row0 + lane) * a.nv + h] : 1.f;
-    const float bt = in ? a.beta[(row0 + lane) * a.nv + h] : 0.f;
     if (!(al >= 9.5367431640625e-7f && al <= 1.f && bt >= 0.f && bt <= 2.f)) fine = false;
     double s = static_cast<double>(log2f(al));
 #pragma unroll
@@ -205,49 +256,6 @@ __global__ __launch_bounds__(256) void k_gdc_prep(GdcArgs a) {
     }
     Lg[lane] = s;
     be[lane] = bt;
-  }
-  // K and Q into LDS, and the norms of their rows over the lanes that load one
-  const int64_t st = static_cast<int64_t>(a.nk) * DK;
-#pragma unroll
-  for (int i = tid; i < kC * kPer; i += 256) {
-    const int r = i / kPer, at = (i % kPer) * 16;
-    u32x4 kv = {0, 0, 0, 0}, qv = kv;
-    if (r < len) {
-      const int64_t off = ((row0 + r) * st + static_cast<int64_t>(kh) * DK) * kSize + at;
-      kv = load16(static_cast<const uint8_t*>(a.k) + off);
-      qv = load16(static_cast<const uint8_t*>(a.q) + off);
-    }
-    *reinterpret_cast<u32x4*>(kq + r * kRow + at) = kv;
-    *reinterpret_cast<u32x4*>(kq + kC * kRow + r * kRow + at) = qv;
-    float sk = 0.f, sq = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (ACT == kF32) {
-        sk = fmaf(__uint_as_float(kv[j]), __uint_as_float(kv[j]), sk);
-        sq = fmaf(__uint_as_float(qv[j]), __uint_as_float(qv[j]), sq);
-      } else {
-        const float k0 = __uint_as_float(kv[j] << 16), k1 = __uint_as_float(kv[j] & 0xffff0000u);
-        const float q0 = __uint_as_float(qv[j] << 16), q1 = __uint_as_float(qv[j] & 0xffff0000u);
-        sk = fmaf(k1, k1, fmaf(k0, k0, sk));
-        sq = fmaf(q1, q1, fmaf(q0, q0, sq));
-      }
-    }
-#pragma unroll
-    for (int d = 1; d < kPer; d <<= 1) {
-      sk += __shfl_xor(sk, d);
-      sq += __shfl_xor(sq, d);
-    }
-    const float rkv = 1.0f / sqrtf(sk + a.eps), rqv = a.scale / sqrtf(sq + a.eps);
-    // a row that is not finite has a norm that is not
-    fine = fine && (r >= len || (isfinite(sk) && isfinite(sq) && isfinite(rkv) && isfinite(rqv)));
-    if (i % kPer == 0) {
-      rk[r] = r < len ? rkv : 0.f;
-      rq[r] = r < len ? rqv : 0.f;
-    }
-  }
-  for (int i = tid; i < len * (a.dv / 8); i += 256) {
-    const int64_t at = ((row0 + i / (a.dv / 8)) * a.nv + h) * static_cast<int64_t>(a.dv) + (i % (a.dv / 8)) * 8;
-    fine = fine && finite4(load4<ACT>(a.v, at)) && finite4(load4<ACT>(a.v, at + 4));
   }
   if (!fine) odd = 1;
   __syncthreads();
@@ -278,7 +286,7 @@ __global__ __launch_bounds__(256) void k_gdc_prep(GdcArgs a) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int i = 16 * bi + 4 * g + r, j = 16 * bj + n16;
-      const float D = i >= j ? exp2f(static_cast<float>(Lg[i] - Lg[j])) * rk[j] : 0.f;
+      const float D = i >= j ? __builtin_amdgcn_exp2f(static_cast<float>(Lg[i] - Lg[j])) * rk[j] : 0.f;
       As[i * kLd + j] = i > j ? be[i] * D * rk[i] * G[r] : 0.f;
       H[x][r] *= D * rq[i];
     }
@@ -365,11 +373,16 @@ __global__ __launch_bounds__(256) void k_gdc_prep(GdcArgs a) {
       if (ACT == kBF16 && s > w / 2) continue;
       f32x4 tz[2], to[2];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const int j = 32 * s + 8 * g + x;
-        const bool in = j <= i;
-        tz[x / 4][x % 4] = in ? wi * Ts[i * kLd + j] * be[j] : 0.f;
-        to[x / 4][x % 4] = in ? PT[i * kLd + j] * be[j] : 0.f;
+      for (int x = 0; x < 2; ++x) {
+        const int j0 = 32 * s + 8 * g + 4 * x;
+        const f32x4 t = *reinterpret_cast<const f32x4*>(Ts + i * kLd + j0), p = *reinterpret_cast<const f32x4*>(PT + i * kLd + j0);
+        const f32x4 b4 = *reinterpret_cast<const f32x4*>(be + j0);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const bool in = j0 + y <= i;
+          tz[x][y] = in ? wi * t[y] * b4[y] : 0.f;
+          to[x][y] = in ? p[y] * b4[y] : 0.f;
+        }
       }
       if constexpr (ACT == kF32) {
         float* m = vec + kVec + i * kC + 32 * s + 8 * g;
@@ -400,6 +413,15 @@ __global__ __launch_bounds__(256) void k_gdc_prep(GdcArgs a) {
       vec[2 * kC + 1] = 0.f;
     }
   }
+}
+
+// Whether one of the values is not finite, or so large (2^96) that the products
+// of a chunk could leave the range where those of single tokens do not.
+__device__ __forceinline__ bool far4(const f32x4& v) {
+  const uint32_t a = __float_as_uint(v[0]) & 0x7fffffffu, b = __float_as_uint(v[1]) & 0x7fffffffu;
+  const uint32_t c = __float_as_uint(v[2]) & 0x7fffffffu, d = __float_as_uint(v[3]) & 0x7fffffffu;
+  const uint32_t x = a > b ? a : b, y = c > d ? c : d;
+  return (x > y ? x : y) > 0x6f800000u;
 }
 
 // A chunk token by token, 16 lanes a row of the 16 of the state in LDS (S, rows
@@ -509,6 +531,7 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
   __shared__ __align__(16) uint8_t Xp[3 * kPlaneX];
   __shared__ __align__(16) uint8_t Zp[3 * kPlaneX];
   __shared__ __align__(16) uint8_t Kp[2][kC * DK * 2];
+  __shared__ int far[4];                       // whether a wave's part of X is out of range
   const int lane = threadIdx.x & (kWave - 1), w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int n16 = lane & 15, g = lane >> 4;
   Scan sc;
@@ -619,10 +642,9 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
     ask_k(next);
     ask_first(next, then);
     const float gC = one.gc.x;
-    const bool by_token = __builtin_amdgcn_readfirstlane(__float_as_int(one.gc.y)) != 0;
+    bool by_token = __builtin_amdgcn_readfirstlane(__float_as_int(one.gc.y)) != 0;
     f32x4 qs = {0.f, 0.f, 0.f, 0.f};
-    if (by_token) {
-      // in fp32 through the place of S
+    const auto run_tokens = [&]() {            // in fp32 through the place of S
       static_assert(3 * kPlaneS >= kRowsS * kLs * 4, "room for the state");
       float* Ss = reinterpret_cast<float*>(Sp);
 #pragma unroll
@@ -632,6 +654,10 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
       __syncthreads();
 #pragma unroll
       for (int t = 0; t < NT; ++t) S[t] = *reinterpret_cast<const f32x4*>(Ss + n16 * kLs + 16 * (NT * w + t) + 4 * g);
+      __syncthreads();
+    };
+    if (by_token) {
+      run_tokens();
     } else {
       // K S^T and Q S^T
       f32x4 ks = {0.f, 0.f, 0.f, 0.f};
@@ -652,8 +678,15 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
         qs[r] *= one.f[r];
       }
       put_x(Xp, x);
+      if (lane == 0) far[w] = 0;
+      if (far4(x)) far[w] = 1;
     }
     __syncthreads();
+    if (!by_token && (far[0] | far[1] | far[2] | far[3]) != 0) {
+      by_token = true;                         // out of range: S is as it was
+      __syncthreads();                         // before the next chunk's flags
+      run_tokens();
+    }
     if (!by_token) {
       // (Z-matrix) X and (O-matrix) X
       f32x4 zt = {0.f, 0.f, 0.f, 0.f};
@@ -819,28 +852,75 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_gdc_scan_bf16(GdcArgs a) {
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
   const auto transposed = [&](const uint8_t* p) { return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p)); };
 
-  int stage = 0, c = sc.c0;
-  if (c < sc.c1)
+  // A chunk token by token: a lane has a quarter of a row's columns.
+  const auto tokens = [&](int c, const uint8_t* in) {
+    const int64_t row0 = static_cast<int64_t>(sc.begin) + static_cast<int64_t>(c) * kC;
+    const auto sum4 = [&](float x) {
+      x += __uint_as_float(lane_xor<16>(__float_as_uint(x), lane));
+      return x + __uint_as_float(lane_xor<32>(__float_as_uint(x), lane));
+    };
+    const int len = length(c);
+#pragma unroll 1
+    for (int t = 0; t < len; ++t) {
+      u32x4 kr[KS], qr[KS];
+      float sk = 0.f, sq = 0.f;
+      const auto lo = [](uint32_t x) { return __uint_as_float(x << 16); };
+      const auto hi = [](uint32_t x) { return __uint_as_float(x & 0xffff0000u); };
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) request(c, smem, i);
-  uint8_t* in = smem;
-  // waits for chunk c; whether it runs token by token
-  const auto arrive = [&]() {
-    in = smem + stage * L::kStage;
+      for (int s = 0; s < KS; ++s) {
+        const int off = t * DK * 2 + (((4 * s + g) ^ turn(t)) << 4);
+        kr[s] = *reinterpret_cast<const u32x4*>(in + L::kK + off);
+        qr[s] = *reinterpret_cast<const u32x4*>(in + L::kQ + off);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sk = fmaf(hi(kr[s][i]), hi(kr[s][i]), fmaf(lo(kr[s][i]), lo(kr[s][i]), sk));
+          sq = fmaf(hi(qr[s][i]), hi(qr[s][i]), fmaf(lo(qr[s][i]), lo(qr[s][i]), sq));
+        }
+      }
+      const float fk = 1.0f / sqrtf(sum4(sk) + a.eps), fq = a.scale / sqrtf(sum4(sq) + a.eps);
+      const float al = a.alpha[(row0 + t) * a.nv + sc.h], bt = a.beta[(row0 + t) * a.nv + sc.h];
+      const float v = bf16_to_f32(*reinterpret_cast<const uint16_t*>(in + L::kV + t * 32 * NW + (16 * w + n16) * 2));
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x = fmaf(S[2 * s + i / 2][2 * (i % 2)], lo(kr[s][i]) * fk, x);
+          x = fmaf(S[2 * s + i / 2][2 * (i % 2) + 1], hi(kr[s][i]) * fk, x);
+        }
+      const float u = bt * (v - al * sum4(x));
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float s0 = fmaf(u, lo(kr[s][i]) * fk, al * S[2 * s + i / 2][2 * (i % 2)]);
+          const float s1 = fmaf(u, hi(kr[s][i]) * fk, al * S[2 * s + i / 2][2 * (i % 2) + 1]);
+          S[2 * s + i / 2][2 * (i % 2)] = s0;
+          S[2 * s + i / 2][2 * (i % 2) + 1] = s1;
+          y = fmaf(s0, lo(qr[s][i]) * fq, y);
+          y = fmaf(s1, hi(qr[s][i]) * fq, y);
+        }
+      y = sum4(y);
+      if (g == 0) {
+        const int64_t oi = ((row0 + t) * a.nv + sc.h) * static_cast<int64_t>(a.dv) + dv0 + n16;
+        if constexpr (OUT == kF32) static_cast<float*>(a.out)[oi] = y;
+        else static_cast<uint16_t*>(a.out)[oi] = f32_to_bf16(y);
+      }
+    }
+  };
+
+  int stage = 0;
+  if (sc.c0 < sc.c1)
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) request(sc.c0, smem, i);
+  const uint32_t ooff = (static_cast<uint32_t>(8 * g) * static_cast<uint32_t>(vst) + n16) * (OUT == kF32 ? 4u : 2u);
+  for (int c = sc.c0; c < sc.c1; ++c) {
+    uint8_t* const in = smem + stage * L::kStage;
     stage ^= 1;
+    uint8_t* const other = smem + stage * L::kStage;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();                           // the chunk is there, and nobody reads the other stage any more
-    return __builtin_amdgcn_readfirstlane(__float_as_int(reinterpret_cast<const float*>(in + L::kF)[2 * kC + 1])) != 0;
-  };
-  const uint32_t ooff = (static_cast<uint32_t>(8 * g) * static_cast<uint32_t>(vst) + n16) * (OUT == kF32 ? 4u : 2u);
-  for (; c < sc.c1; ++c) {
-    // chunk after chunk as matrix products ...
-    bool by_token = false;
-    for (; c < sc.c1; ++c) {
-    by_token = arrive();
-    if (by_token) break;
     const bool more = c + 1 < sc.c1;
-    uint8_t* const other = smem + stage * L::kStage;
     if (idle) {
       if (more)
 #pragma unroll
@@ -849,6 +929,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_gdc_scan_bf16(GdcArgs a) {
     }
     const float* const vec = reinterpret_cast<const float*>(in + L::kF);
     const int len = length(c);
+    bool by_token = __builtin_amdgcn_readfirstlane(__float_as_int(vec[2 * kC + 1])) != 0;
     // K S^T and Q S^T
     bf16x8 Sp[KS][3];
 #pragma unroll
@@ -872,6 +953,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_gdc_scan_bf16(GdcArgs a) {
     }
     // X: tokens 8 g + 0 .. 3 and 4 .. 7 of each half of the chunk
     bf16x8 Xp[2][3];
+    bool far = false;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       f32x4 x[2];
@@ -883,8 +965,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_gdc_scan_bf16(GdcArgs a) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) x[y][r] = static_cast<float>(v[r]) - e[r] * ks[2 * s + y][r];
         o[2 * s + y] *= f;
+        far |= far4(x[y]);
       }
       split3(x[0], x[1], Xp[s]);
+    }
+    if (by_token || __ballot(far)) {           // outside the range of the matrices, or not finite
+      tokens(c, in);
+      continue;
     }
     // (Z-matrix) X and (O-matrix) X, the smallest terms first
     f32x4 z[4];
@@ -955,26 +1042,6 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_gdc_scan_bf16(GdcArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) S[t][i] = fmaf(gC, S[t][i], d[i]);
     }
-    }
-    if (!by_token) break;
-    // ... and one token by token, the state through its place in LDS
-    constexpr int kLs = DK + 4;
-    static_assert(NW * kRowsS * kLs * 4 <= L::kStage, "room for the states");
-    if (c + 1 < sc.c1)
-#pragma unroll
-      for (int i = 0; i < kParts; ++i) request(c + 1, smem + stage * L::kStage, i);
-    __syncthreads();                           // every wave has seen the flag
-    float* Ss = reinterpret_cast<float*>(in) + w * kRowsS * kLs;
-    if (!idle) {
-#pragma unroll
-      for (int t = 0; t < 2 * KS; ++t) *reinterpret_cast<f32x4*>(Ss + n16 * kLs + 32 * (t >> 1) + 8 * g + 4 * (t & 1)) = S[t];
-      wave_sync_lds();
-      const int64_t row0 = static_cast<int64_t>(sc.begin) + static_cast<int64_t>(c) * kC;
-      for (int x = 0; x < 4; ++x) chunk_by_token<DK, kBF16, OUT>(a, Ss, kLs, row0, length(c), sc.h, sc.kh, dv0, lane, x);
-      wave_sync_lds();
-#pragma unroll
-      for (int t = 0; t < 2 * KS; ++t) S[t] = *reinterpret_cast<const f32x4*>(Ss + n16 * kLs + 32 * (t >> 1) + 8 * g + 4 * (t & 1));
-    }
   }
   if (!idle)
 #pragma unroll
@@ -992,6 +1059,7 @@ __global__ __launch_bounds__(256) void k_gdc_scan_f32(GdcArgs a) {
   __shared__ __align__(16) float Ks[kC * kLs];
   __shared__ __align__(16) float Xs[kRowsS * kLx];
   __shared__ __align__(16) float Zs[kRowsS * kLx];
+  __shared__ int far[4];                       // whether a wave's part of X is out of range
   const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave;
   const int n16 = lane & 15, g = lane >> 4;
   Scan sc;
@@ -1042,7 +1110,14 @@ __global__ __launch_bounds__(256) void k_gdc_scan_f32(GdcArgs a) {
       qs[r] *= vec[kC + i];
     }
     *reinterpret_cast<f32x4*>(Xs + n16 * kLx + 16 * w + 4 * g) = x;
+    if (lane == 0) far[w] = 0;
+    if (far4(x)) far[w] = 1;
     __syncthreads();
+    if ((far[0] | far[1] | far[2] | far[3]) != 0) {   // out of range: S is as it was
+      chunk_by_token<DK, ACT, OUT>(a, Ss, kLs, row0, len, h, kh, dv0, lane, w);
+      __syncthreads();
+      continue;
+    }
     f32x4 zt = {0.f, 0.f, 0.f, 0.f};
     for (int s = 0; s <= w; ++s) {
       const f32x4 Tz = *reinterpret_cast<const f32x4*>(slot_p + (16 * w + n16) * kC + 16 * s + 4 * g);
