@@ -2,14 +2,16 @@
 // v to the paged cache (include/attention.h), in one pass (gfx950).
 //
 // A head is 16 bytes a lane: L = head_dim * size / 16 lanes, so a wave takes
-// 64 / L heads of one token at once.  The norm is one sum of squares over L
-// lanes; the partner of a rotated pair is in the same lane (adjacent pairs) or
-// read again from the row, which the load before has brought to the cache.
-// Angles are formed once per lane and used for all heads that the wave takes.
+// 64 / L heads of one token at once, a group.  The norm is one sum of squares over
+// L lanes; the partner of a rotated pair is in the same lane (adjacent pairs) or
+// read again from the row, which the load before has brought to the cache.  The
+// angles of a token are formed once by the wave, a pair a lane, and handed out
+// through LDS; with the weights of the norm they make two factors a value.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
 #include <cstdio>
+#include <type_traits>
 
 #include "attn_internal.h"
 #include "moe_internal.h"
@@ -46,16 +48,32 @@ __device__ __forceinline__ float lanes_sum(float x, int lane) {
   return x;
 }
 
-// Number of entries of cu[0 .. B] that are at most t, less one: the last
-// sequence that begins at or before row t (-1: none).  All lanes, 64 entries a
-// step.
-__device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int t, int lane) {
-  int n = 0;
-  for (int i = 0; i <= B; i += kWave) {
-    const int j = i + lane;
-    n += __popcll(__ballot(j <= B && cu[j] <= t));
+// 1 / sqrt(x) by the instruction, within one unit in the last place; it takes
+// denormals for zero, so small x are brought up.
+__device__ __forceinline__ float inverse_root(float x) {
+  const bool small = x < 0x1p-96f;
+  return __builtin_amdgcn_rsqf(small ? x * 0x1p64f : x) * (small ? 0x1p32f : 1.f);
+}
+
+// The sequence of row t, with the number of the row's token in it; false if it
+// has none.  64 entries of cu a step, in equal distances until 64 are left.
+__device__ __forceinline__ bool find_sequence(const AttnBatch& at, int t, int lane, int& b, int64_t& number) {
+  int lo = 0, n = at.B;
+  while (n > kWave) {
+    const int step = (n + kWave - 1) / kWave, j = lane * step;
+    const int hits = __popcll(__ballot(j < n && at.cu[lo + (j < n ? j : 0)] <= t));
+    if (hits == 0) return false;
+    lo += (hits - 1) * step;
+    n = n - (hits - 1) * step < step ? n - (hits - 1) * step : step;
   }
-  return n - 1;
+  const int j = lo + (lane < n ? lane : n - 1);
+  const int begin = at.cu[j], end = at.cu[j + 1], len = at.lens[j];
+  const uint64_t hit = __ballot(lane < n && begin <= t && t < end);
+  if (hit == 0) return false;
+  const int first = __builtin_ctzll(hit);
+  b = lo + first;
+  number = static_cast<int64_t>(__builtin_amdgcn_readlane(len, first)) - __builtin_amdgcn_readlane(end, first) + t;
+  return true;
 }
 
 template <int DT, int V>
@@ -67,13 +85,16 @@ __device__ __forceinline__ void unpack(const u32x4& w, float (&x)[V]) {
   }
 }
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
 template <int DT, int V>
 __device__ __forceinline__ u32x4 pack(const float (&x)[V]) {
   u32x4 w;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (DT == kF32) w[i] = __float_as_uint(x[i]);
-    else w[i] = f32_to_bf16(x[2 * i]) | (static_cast<uint32_t>(f32_to_bf16(x[2 * i + 1])) << 16);
+    else w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{x[2 * i], x[2 * i + 1]}), bf16x2));
   }
   return w;
 }
@@ -82,115 +103,154 @@ template <int DT, int D>
 __global__ __launch_bounds__(256) void k_attn_append(AppendArgs a) {
   constexpr int V = DT == kF32 ? 4 : 8;      // values a lane
   constexpr int L = D / V;                   // lanes a head
-  constexpr int H = kWave / L;               // heads a wave takes at once
+  constexpr int H = kWave / L;               // heads a group
+  constexpr int G = 4;                       // groups requested at once
   constexpr int kSize = DT == kF32 ? 4 : 2;
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = threadIdx.x / kWave;
-  const int heads = (a.q ? a.nq : 0) + 2 * a.nkv;
-  const int groups = (heads + H - 1) / H;
+  __shared__ __align__(16) float turns[4][2][D];   // by wave: cosines and sines, the sign of the pair's first on the sine
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int nq = a.q ? a.nq : 0;
+  const int qgroups = (nq + H - 1) / H, groups = qgroups + (2 * a.nkv + H - 1) / H;
   const int waves = (groups + a.per_wave - 1) / a.per_wave;      // per token
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + wave;
+  const uint32_t w = blockIdx.x * 4 + wave;
   const int t = static_cast<int>(w / waves);
   if (t >= a.at.N) return;
-  const int first = static_cast<int>(w % waves) * a.per_wave;
+  const int first = static_cast<int>(w % waves) * a.per_wave, last = first + a.per_wave < groups ? first + a.per_wave : groups;
 
-  const int b = sequence_of(a.at.cu, a.at.B, t, lane);
-  if (b < 0 || b >= a.at.B) return;          // a row of no sequence
-  const int begin = a.at.cu[b], end = a.at.cu[b + 1];
-  const int64_t number = static_cast<int64_t>(a.at.lens[b]) - end + t;
+  const int sub = lane / L, e0 = (lane % L) * V;                 // this lane's values of a head
+  const int half = a.R / 2;
+  const bool turned = e0 < a.R, apart = turned && !a.adjacent;
+  u32x4 raw[G], other[G];
+  const uint8_t* src[G];
+  // Groups g0 .. of those up to `to`: heads of q, or of k and then v.
+  const auto request = [&](auto kind, int g0, int to) {
+    constexpr bool IS_Q = decltype(kind)::value;
+    const int base = IS_Q ? 0 : qgroups, heads = IS_Q ? nq : 2 * a.nkv;
+#pragma unroll
+    for (int y = 0; y < G; ++y) {
+      int head = (g0 + y < to ? g0 + y - base : to - 1 - base) * H + sub;
+      head = head < heads ? head : heads - 1;
+      const bool is_v = !IS_Q && head >= a.nkv;
+      const int64_t row = static_cast<int64_t>(t) * (IS_Q ? a.qs : (is_v ? a.vs : a.ks));
+      src[y] = static_cast<const uint8_t*>(IS_Q ? a.q : (is_v ? a.v : a.k)) + (row + static_cast<int64_t>(is_v ? head - a.nkv : head) * D) * kSize;
+      raw[y] = load16(src[y] + e0 * kSize);
+      if (apart && half % V == 0) other[y] = load16(src[y] + (e0 < half ? e0 + half : e0 - half) * kSize);
+    }
+  };
+  if (first < qgroups) request(std::true_type{}, first, last < qgroups ? last : qgroups);
+  else request(std::false_type{}, first, last);
+
+  int b;
+  int64_t number;
+  if (!find_sequence(a.at, t, lane, b, number)) return;
   int64_t page = -1;
   if (number >= 0 && (number >> a.at.shift) < a.at.max_pages)
     page = a.at.table[static_cast<int64_t>(b) * a.at.max_pages + (number >> a.at.shift)];
   const bool kept = page >= 0 && page < a.at.n_pages;
   const int64_t place = number & ((1 << a.at.shift) - 1);
 
-  const int sub = lane / L;
-  const int e0 = (lane % L) * V;             // this lane's values of a head
-  const bool turned = e0 < a.R;
-  float cs[V], sn[V];
-  if (turned) {
-    const double pos = a.positions[t];
-    const int half = a.R / 2;
+  float* const cosines = turns[wave][0];
+  float* const sines = turns[wave][1];
+  for (int p = lane; p < half; p += kWave) {
+    // turns, reduced to [-1/2, 1/2] before the step down to fp32
+    const double whole = static_cast<double>(a.positions[t]) * (static_cast<double>(a.inv_freq[p]) * 0.15915494309189535);
+    float sn, cs;
+    sincospif(2.f * static_cast<float>(whole - rint(whole)), &sn, &cs);
+    const int i = a.adjacent ? 2 * p : p, j = a.adjacent ? 2 * p + 1 : p + half;
+    cosines[i] = cosines[j] = cs;
+    sines[i] = -sn;                          // first of a pair: x cos - partner sin; second: x cos + partner sin
+    sines[j] = sn;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  const auto partner = [&](int e) { return a.adjacent ? e ^ 1 : (e < half ? e + half : e - half); };
+
+  const auto take = [&](auto kind, int from, int to) {
+    constexpr bool IS_Q = decltype(kind)::value;
+    const int base = IS_Q ? 0 : qgroups, heads = IS_Q ? nq : 2 * a.nkv;
+    const float* const wt = IS_Q ? a.qw : a.kw;
+    float c[V], s[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = e0 + i;
-      const int pair = a.adjacent ? e / 2 : (e < half ? e : e - half);
-      const bool second = a.adjacent ? (i & 1) != 0 : e >= half;
-      float c = 1.f, s = 0.f;
-      if (a.adjacent && second) {
-        c = cs[i - 1];
-        s = -sn[i - 1];
-      } else if (e < a.R) {
-        // turns, reduced to [-1/2, 1/2] before the step down to fp32
-        const double turns = pos * (static_cast<double>(a.inv_freq[pair]) * 0.15915494309189535);
-        sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
-      }
-      cs[i] = c;
-      sn[i] = second ? s : -s;               // first of a pair: x cos - partner sin; second: x cos + partner sin
-    }
-  }
-
-  for (int gidx = first; gidx < first + a.per_wave && gidx < groups; ++gidx) {
-    const int head = gidx * H + sub;         // queries, then keys, then values
-    if (head >= heads) continue;
-    const int nq = heads - 2 * a.nkv;
-    const bool is_q = head < nq, is_v = head >= nq + a.nkv;
-    const int h = is_q ? head : (is_v ? head - nq - a.nkv : head - nq);
-    const uint8_t* src = static_cast<const uint8_t*>(is_q ? a.q : (is_v ? a.v : a.k)) +
-                         (static_cast<int64_t>(t) * (is_q ? a.qs : (is_v ? a.vs : a.ks)) + static_cast<int64_t>(h) * D) * kSize;
-    u32x4 raw = *reinterpret_cast<const u32x4*>(src + e0 * kSize);
-    if (!is_v) {
-      float x[V], y[V];
-      unpack<DT, V>(raw, x);
-      const bool apart = turned && !a.adjacent;
-      const int half = a.R / 2;
-      if (apart) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int e = e0 + i;
-          const int p = e < half ? e + half : (e < a.R ? e - half : e);
-          y[i] = load_scalar<DT>(src, p);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) y[i] = x[i ^ 1];
-      }
-      const float* wt = is_q ? a.qw : a.kw;
+      c[i] = e < a.R ? cosines[e] : 1.f;
+      s[i] = e < a.R ? sines[e] : 0.f;
       if (wt) {
-        float ss = 0.f;
+        c[i] *= a.offset + wt[e];
+        if (e < a.R) s[i] *= a.offset + wt[partner(e)];
+      }
+    }
+    for (int g0 = from; g0 < to; g0 += G) {
+      if (g0 > first) request(kind, g0, to);
 #pragma unroll
-        for (int i = 0; i < V; ++i) ss = fmaf(x[i], x[i], ss);
-        ss = lanes_sum<L>(ss, lane);
-        const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
+      for (int y = 0; y < G; ++y) {
+        const int head = (g0 + y - base) * H + sub;
+        if (g0 + y >= to || head >= heads) continue;
+        const bool is_v = !IS_Q && head >= a.nkv;
+        if (!is_v && (wt || turned)) {
+          float x[V], z[V], r = 1.f;
+          unpack<DT, V>(raw[y], x);
+          if (wt) {
+            float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int e = e0 + i;
-          const int p = apart ? (e < half ? e + half : (e < a.R ? e - half : e)) : (e0 + (i ^ 1));
-          x[i] = x[i] * r * (a.offset + wt[e]);
-          y[i] = y[i] * r * (a.offset + wt[p]);
+            for (int i = 0; i < V; ++i) ss = fmaf(x[i], x[i], ss);
+            ss = lanes_sum<L>(ss, lane);
+            r = inverse_root(fmaf(ss, 1.0f / D, a.eps));
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] *= r;
+          }
+          if (turned) {
+            if (!apart) {
+#pragma unroll
+              for (int i = 0; i < V; ++i) z[i] = x[i ^ 1];
+            } else {
+              if (half % V == 0) {
+                unpack<DT, V>(other[y], z);
+              } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) z[i] = load_scalar<DT>(src[y], e0 + i < a.R ? partner(e0 + i) : e0 + i);
+              }
+#pragma unroll
+              for (int i = 0; i < V; ++i) z[i] *= r;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            x[i] *= c[i];
+            if (e0 + i < a.R) x[i] = fmaf(z[i], s[i], x[i]);
+          }
+          raw[y] = pack<DT, V>(x);
         }
+        uint8_t* to_row;
+        if (IS_Q) {
+          to_row = static_cast<uint8_t*>(a.q_out) + (static_cast<int64_t>(t) * nq + head) * D * kSize;
+        } else {
+          if (!kept) continue;
+          to_row = static_cast<uint8_t*>(a.pages) + (page * a.at.page_elems + (is_v ? a.at.half_elems : 0) +
+                   ((static_cast<int64_t>(is_v ? head - a.nkv : head) << a.at.shift) + place) * D) * kSize;
+        }
+        *reinterpret_cast<u32x4*>(to_row + e0 * kSize) = raw[y];
       }
-      if (turned) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (e0 + i < a.R) x[i] = fmaf(x[i], cs[i], y[i] * sn[i]);
-      }
-      raw = pack<DT, V>(x);
     }
-    if (is_q) {
-      *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.q_out) + ((static_cast<int64_t>(t) * a.nq + h) * D + e0) * kSize) = raw;
-    } else if (kept) {
-      const int64_t o = page * a.at.page_elems + (is_v ? a.at.half_elems : 0) +
-                        ((static_cast<int64_t>(h) << a.at.shift) + place) * D + e0;
-      *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.pages) + o * kSize) = raw;
-    }
-  }
+  };
+  if (first < qgroups) take(std::true_type{}, first, last < qgroups ? last : qgroups);
+  if (last > qgroups) take(std::false_type{}, first > qgroups ? first : qgroups, last);
+}
+
+// Groups that a wave takes: one for few tokens, so that as many loads as can be
+// are under way at once, and with more of them as many as leave ten waves a CU,
+// so that a token's place and angles are formed less often.  Microseconds with
+// 1, 2, 5 and 10 groups a wave, 16 + 2 heads of 256: a token 4.8, 5.3, 9.0, 12.0;
+// 512 tokens 12.8, 9.0, 10.4, 13.4; 1024 21, 14.6, 12.9, 14.1; 4096 73, 43, 34, 27.
+int append_per_wave(int groups, int N) {
+  const int64_t v = (static_cast<int64_t>(groups) * N + 2559) / 2560;
+  return v < groups ? static_cast<int>(v) : groups;
 }
 
 template <int DT>
-void launch_append(const AppendArgs& a, int D, hipStream_t s) {
+void launch_append(AppendArgs a, int D, hipStream_t s) {
   const int V = DT == kF32 ? 4 : 8, H = kWave / (D / V);
-  const int heads = (a.q ? a.nq : 0) + 2 * a.nkv, groups = (heads + H - 1) / H;
+  const int groups = ((a.q ? a.nq : 0) + H - 1) / H + (2 * a.nkv + H - 1) / H;
+  a.per_wave = append_per_wave(groups, a.at.N);
   const int64_t waves = static_cast<int64_t>((groups + a.per_wave - 1) / a.per_wave) * a.at.N;
   const dim3 grid(static_cast<uint32_t>((waves + 3) / 4));
   if (D == 64) launch_kernel(k_attn_append<DT, 64>, grid, dim3(256), 0, s, a);
@@ -286,11 +346,6 @@ extern "C" int attn_append(const attn_desc* d, int32_t B, int32_t N, const int32
   a.adjacent = d->rotary_pairs == ATTN_ROTARY_ADJACENT;
   a.eps = d->eps;
   a.offset = d->norm_offset;
-  // one group of heads a wave: the most waves for few tokens; more where a
-  // launch would need 2^32 threads
-  const int per_group = kWave / static_cast<int>(D * sz / 16), heads = (q ? d->n_q_heads : 0) + 2 * d->n_kv_heads;
-  const int64_t groups = (heads + per_group - 1) / per_group;
-  a.per_wave = static_cast<int>((groups * N + (1 << 25) - 1) >> 25);
   if (d->dtype == MOE_F32) launch_append<kF32>(a, d->head_dim, static_cast<hipStream_t>(stream));
   else launch_append<kBF16>(a, d->head_dim, static_cast<hipStream_t>(stream));
   const hipError_t e = hipGetLastError();
