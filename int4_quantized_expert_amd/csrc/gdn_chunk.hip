@@ -569,31 +569,42 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
   };
 
   const int64_t st = static_cast<int64_t>(a.nk) * DK;
-  const uint16_t* const kb = static_cast<const uint16_t*>(a.k) + static_cast<int64_t>(sc.kh) * DK;
-  const uint16_t* const qb = static_cast<const uint16_t*>(a.q) + static_cast<int64_t>(sc.kh) * DK;
-  const uint16_t* const vb = static_cast<const uint16_t*>(a.v) + static_cast<int64_t>(sc.h) * a.dv + sc.dv0 + n16;
   const int64_t vst = static_cast<int64_t>(a.nv) * a.dv;
-  // Tokens behind the last one: rows of it again, whose Zt and matrix columns are 0.
-  const auto row_of = [&](int c, int t) {
-    const int at = c * kC + t;
-    return static_cast<int64_t>(sc.begin) + (at < sc.n ? at : sc.n - 1);
+  constexpr int kOut = OUT == kF32 ? 4 : 2;
+  const uint16_t* const kb = static_cast<const uint16_t*>(a.k) + sc.begin * st + static_cast<int64_t>(sc.kh) * DK;
+  const uint16_t* const qb = static_cast<const uint16_t*>(a.q) + sc.begin * st + static_cast<int64_t>(sc.kh) * DK;
+  const uint16_t* const vb = static_cast<const uint16_t*>(a.v) + sc.begin * vst + static_cast<int64_t>(sc.h) * a.dv + sc.dv0;
+  uint8_t* const ob = static_cast<uint8_t*>(a.out) + (sc.begin * vst + static_cast<int64_t>(sc.h) * a.dv + sc.dv0) * kOut;
+  // Offsets within a chunk.  The descriptors end with the last token: rows behind
+  // it arrive as zeros, and are not written.
+  uint32_t koff[kKl], voff[4];
+#pragma unroll
+  for (int i = 0; i < kKl; ++i) {
+    const int p = threadIdx.x + 256 * i;
+    koff[i] = (p / kPer) * static_cast<uint32_t>(st) * 2u + (p % kPer) * 16;
+  }
+  const uint32_t qoff = token_of(w, n16) * static_cast<uint32_t>(st) * 2u + g * 16;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) voff[r] = (t4 + r) * static_cast<uint32_t>(vst) * 2u + n16 * 2;
+  const auto length = [&](int c) { return sc.n - c * kC < kC ? sc.n - c * kC : kC; };
+  const auto buffer = [](const void* base, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(bytes), 0x00020000);
   };
+  const auto load = [](auto rs, uint32_t off, int at) { return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, at, 0)); };
   u32x4 Kn[kKl];
   bf16x8 Tz[2][3], To[2][OP];
   struct First {                               // what the first product takes
     bf16x8 Q[KS];
-    uint32_t V[4];                             // as stored: converted where it is used, or the load would be waited for here
+    uint16_t V[4];                             // as stored: converted where it is used, or the load would be waited for here
     f32x4 e, f;
     float2 gc;                                 // g_C, and whether the chunk runs token by token
   };
   First even, odd;                             // by the chunk's number
   const auto slot = [&](int c) { return a.ws + (slot_of(a, sc.b, sc.begin, c) * a.nv + sc.h) * slot_bytes(kBF16, OUT); };
   const auto ask_k = [&](int c) {
+    const auto rs = buffer(kb + static_cast<int64_t>(c) * kC * st, ((length(c) - 1) * st + DK) * 2);
 #pragma unroll
-    for (int i = 0; i < kKl; ++i) {
-      const int p = threadIdx.x + 256 * i;
-      Kn[i] = load16(kb + row_of(c, p / kPer) * st + (p % kPer) * 8);
-    }
+    for (int i = 0; i < kKl; ++i) Kn[i] = load(rs, koff[i], 0);
   };
   const auto put_k = [&](int half) {
 #pragma unroll
@@ -602,34 +613,40 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
       *reinterpret_cast<u32x4*>(Kp[half] + k_at(p / kPer, p % kPer)) = Kn[i];
     }
   };
-  const auto ask_first = [&](int c, First& o) {
-    const uint16_t* q = qb + row_of(c, token_of(w, n16)) * st + 8 * g;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) o.Q[s] = __builtin_bit_cast(bf16x8, load16(q + 32 * s));
-#pragma unroll
-    for (int r = 0; r < 4; ++r) o.V[r] = vb[row_of(c, t4 + r) * vst];
-    const float* vec = reinterpret_cast<const float*>(slot(c));
-    o.e = *reinterpret_cast<const f32x4*>(vec + t4);
-    o.f = *reinterpret_cast<const f32x4*>(vec + kC + t4);
-    o.gc = *reinterpret_cast<const float2*>(vec + 2 * kC);
+  const auto ask_q = [&](int c, First& o, int s) {
+    const auto rq = buffer(qb + static_cast<int64_t>(c) * kC * st, ((length(c) - 1) * st + DK) * 2);
+    o.Q[s] = __builtin_bit_cast(bf16x8, load(rq, qoff + 64 * s, 0));
   };
-  const auto ask_second = [&](int c) {         // for the second
-    const uint8_t* m = slot(c) + kVec * 4 + lane * 16;
+  const auto ask_rest = [&](int c, First& o) {
+    const auto rv = buffer(vb + static_cast<int64_t>(c) * kC * vst, ((length(c) - 1) * vst + kRowsS) * 2);
+    const auto rf = buffer(slot(c), kVec * 4);
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-      if (s <= w / 2)
+    for (int r = 0; r < 4; ++r) o.V[r] = __builtin_amdgcn_raw_buffer_load_b16(rv, voff[r], 0, 0);
+    o.e = __builtin_bit_cast(f32x4, load(rf, t4 * 4, 0));
+    o.f = __builtin_bit_cast(f32x4, load(rf, t4 * 4, kC * 4));
+    o.gc = __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(rf, 0, 2 * kC * 4, 0));
+  };
+  const auto ask_second = [&](int c, int s) {  // for the second, 32 columns of the matrices
+    const auto rm = buffer(slot(c), slot_bytes(kBF16, OUT));
+    if (s <= w / 2)
 #pragma unroll
-        for (int x = 0; x < 3; ++x) {
-          Tz[s][x] = __builtin_bit_cast(bf16x8, load16(m + x * kMatBf16 + piece_of(w, s) * 1024));
-          if (x < OP) To[s][x] = __builtin_bit_cast(bf16x8, load16(m + (3 + x) * kMatBf16 + piece_of(w, s) * 1024));
-        }
+      for (int x = 0; x < 3; ++x) {
+        Tz[s][x] = __builtin_bit_cast(bf16x8, load(rm, lane * 16, kVec * 4 + x * kMatBf16 + piece_of(w, s) * 1024));
+        if (x < OP) To[s][x] = __builtin_bit_cast(bf16x8, load(rm, lane * 16, kVec * 4 + (3 + x) * kMatBf16 + piece_of(w, s) * 1024));
+      }
   };
   put_s();
   if (sc.c0 < sc.c1) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      ask_q(sc.c0, even, s);
+    }
     ask_k(sc.c0);
-    ask_first(sc.c0, even);
-    ask_second(sc.c0);
+    ask_rest(sc.c0, even);
+    ask_second(sc.c0, 0);
+    ask_second(sc.c0, 1);
     put_k(0);
+    ask_k(sc.c0 + 1 < sc.c1 ? sc.c0 + 1 : sc.c0);
   }
   __syncthreads();
   // chunk c, whose rows of K lie in stage `half`
@@ -639,8 +656,6 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
     // requests without a condition (the last chunk asks for itself again), so that no copy of a register waits for one
     const int next = c + 1 < sc.c1 ? c + 1 : c;
     const uint8_t* K = Kp[half];
-    ask_k(next);
-    ask_first(next, then);
     const float gC = one.gc.x;
     bool by_token = __builtin_amdgcn_readfirstlane(__float_as_int(one.gc.y)) != 0;
     f32x4 qs = {0.f, 0.f, 0.f, 0.f};
@@ -658,26 +673,36 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
     };
     if (by_token) {
       run_tokens();
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        ask_q(next, then, s);
+      }
+      ask_rest(next, then);
     } else {
       // K S^T and Q S^T
-      f32x4 ks = {0.f, 0.f, 0.f, 0.f};
+      f32x4 ks = {0.f, 0.f, 0.f, 0.f}, ks2 = ks, qs2 = ks;   // two chains each: a product waits for the one before it
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const bf16x8 Ka = *reinterpret_cast<const bf16x8*>(K + k_at(token_of(w, n16), 4 * s + g));
+        ask_q(next, then, s);
 #pragma unroll
         for (int x = 2; x >= 0; --x) {
           const bf16x8 Sb = *reinterpret_cast<const bf16x8*>(Sp + x * kPlaneS + s_at(n16, 32 * s + 8 * g));
-          ks = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Ka, Sb, ks, 0, 0, 0);
-          if (x < OP) qs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(one.Q[s], Sb, qs, 0, 0, 0);
+          f32x4& kd = s & 1 ? ks2 : ks;
+          f32x4& qd = s & 1 ? qs2 : qs;
+          kd = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Ka, Sb, kd, 0, 0, 0);
+          if (x < OP) qd = __builtin_amdgcn_mfma_f32_16x16x32_bf16(one.Q[s], Sb, qd, 0, 0, 0);
         }
+        __builtin_amdgcn_sched_barrier(0);     // requests between the products: the memory unit takes 64 bytes a cycle
       }
       f32x4 x;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        x[r] = __uint_as_float(one.V[r] << 16) - one.e[r] * ks[r];
-        qs[r] *= one.f[r];
+        x[r] = bf16_to_f32(one.V[r]) - one.e[r] * (ks[r] + ks2[r]);
+        qs[r] = (qs[r] + qs2[r]) * one.f[r];
       }
       put_x(Xp, x);
+      ask_rest(next, then);
       if (lane == 0) far[w] = 0;
       if (far4(x)) far[w] = 1;
     }
@@ -689,7 +714,7 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
     }
     if (!by_token) {
       // (Z-matrix) X and (O-matrix) X
-      f32x4 zt = {0.f, 0.f, 0.f, 0.f};
+      f32x4 zt = {0.f, 0.f, 0.f, 0.f}, zt2 = zt;
 #pragma unroll
       for (int s = 0; s < 2; ++s)
         if (s <= w / 2) {
@@ -700,23 +725,21 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
           for (int y = 2; y >= 0; --y)         // the smallest terms first
 #pragma unroll
             for (int z = 2 - y; z >= 0; --z) {
-              zt = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Tz[s][z], Xb[y], zt, 0, 0, 0);
+              f32x4& zd = z & 1 ? zt2 : zt;
+              zd = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Tz[s][z], Xb[y], zd, 0, 0, 0);
               if (z + y < OP) qs = __builtin_amdgcn_mfma_f32_16x16x32_bf16(To[s][z], Xb[y], qs, 0, 0, 0);
             }
         }
-      put_x(Zp, zt);
+      put_x(Zp, zt + zt2);
     }
-    ask_second(next);
+    ask_second(next, 0);
     __syncthreads();
     if (!by_token) {
+      const auto ro = buffer(ob + static_cast<int64_t>(c) * kC * vst * kOut, ((len - 1) * vst + kRowsS) * kOut);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = t4 + r;
-        if (i < len) {
-          const int64_t oi = ((row0 + i) * a.nv + sc.h) * static_cast<int64_t>(a.dv) + sc.dv0 + n16;
-          if constexpr (OUT == kF32) static_cast<float*>(a.out)[oi] = qs[r];
-          else static_cast<uint16_t*>(a.out)[oi] = f32_to_bf16(qs[r]);
-        }
+        if constexpr (OUT == kF32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(qs[r]), ro, voff[r] * 2, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(qs[r]), ro, voff[r], 0, 0);
       }
       // S^T, the columns of this wave
       bf16x8 Zb[2][3];
@@ -727,7 +750,8 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int piece = 2 * (NT * w + t) + ((n16 & 3) >> 1);
-        f32x4 d = {0.f, 0.f, 0.f, 0.f};
+        f32x4 d[2] = {};
+        if (t == 0) ask_second(next, 1);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           bf16x8 Ka;                           // column n16 of the tile, tokens 32 s + 8 g + 0 .. 7
@@ -740,14 +764,17 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
             for (int i = 0; i < 4; ++i) Ka[4 * y + i] = v[i];
           }
 #pragma unroll
-          for (int y = 2; y >= 0; --y) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Ka, Zb[s][y], d, 0, 0, 0);
+          for (int y = 2; y >= 0; --y) d[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Ka, Zb[s][y], d[s], 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) S[t][i] = fmaf(gC, S[t][i], d[i]);
+        for (int i = 0; i < 4; ++i) S[t][i] = fmaf(gC, S[t][i], d[0][i] + d[1][i]);
       }
+    } else {
+      ask_second(next, 1);
     }
     put_s();
     put_k(half ^ 1);
+    ask_k(c + 2 < sc.c1 ? c + 2 : sc.c1 - 1);  // a chunk ahead: what has to come from HBM takes half of one
     __syncthreads();
   };
   for (int c = sc.c0; c < sc.c1; c += 2) {
