@@ -314,7 +314,9 @@ __device__ __forceinline__ float part_weight(float m, float l, float M) { return
 // Few rows: a block takes 16 RT rows of a key head and a run of its keys, its
 // four waves in turn 16 X keys each; they join at the end.
 //
-// The reads of K and V bound it.  K goes from memory straight into the operand
+// The reads of K and V bound it (64 contexts of 100 to 32768 tokens, 16 query and 2 key
+// heads of 256: 763 MB in 142 us, 5.4 TB/s; 256 of 2000 tokens, 8 key heads of 128:
+// 5.8 TB/s; a pure read reaches 6.4).  K goes from memory straight into the operand
 // of S^T (a lane reads 16 bytes of one key), V by direct loads into the wave's
 // own part of LDS, where the transposing read gives four keys of a dim; the
 // next keys are under way while the current ones are worked on.  Pieces of
@@ -644,7 +646,8 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_few(AttnArgs a) {
 // tile's 32 keys of one row, its partner (lane ^ 32) the others.
 //
 // The matrix units and the reads of LDS bound it alike (each wave reads the
-// whole tile for its 32 rows).  Pieces of 16 bytes lie turned by their row so
+// whole tile for its 32 rows): 8192 tokens behind 809, 16 heads of 256, 1150 us,
+// 570 TF/s; 4096 tokens, 32 heads of 128, 187 us, 735 TF/s.  Pieces of 16 bytes lie turned by their row so
 // that the 16 rows, or the four rows of a transposing read, that are read at
 // once fall into different banks.
 //
@@ -897,7 +900,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_tile(AttnArgs a)
 // fp32: the same split of the work on the fp32 matrix instruction (16x16x4).
 // Everything goes from memory to its operand: of the four dims of a 16-byte
 // piece of a key, one for each of four products; V likewise, four dims of one
-// key for four tiles.
+// key for four tiles.  Few rows are bound by the reads of K and V (64 tokens behind
+// 4000, 2 key heads of 256: 200 us, 5.2 TB/s), prompts by the instruction's rate and the
+// loads that each wave repeats (2048 tokens, 16 heads of 128: 222 us, 77 TF/s).
 template <int D, int RT>
 struct F32Lds {
   static constexpr int kCut = RT == 2 ? 32 : 64;
@@ -1103,7 +1108,9 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_f32(AttnArgs a) {
 // ---------------------------------------------------------------------------
 // The parts of a row joined, where blocks shared its keys, and zeros for rows
 // without any.  A wave takes 64 dims of a row, 16 lanes a part (four parts at
-// once, four loads each on the way); WIDE: the block's four waves share them.
+// once, four loads each on the way); WIDE: the block's four waves share them.  Bound
+// by the parts' reads, and by the launch where there are few (1 token of 16 heads
+// 4.0 us; 248 tokens of 32 heads, 32 MB of parts, 14).
 template <int DT, int D, int ROWS, int STEP, bool WIDE>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   constexpr int kSlices = D / 64;

@@ -123,7 +123,7 @@ def head(c, q, k, v, al, be, S):
         for t0 in range(0, n, 64):
             s = slice(t0, min(t0 + 64, n))
             K, Q, V, a, b = kn[s], qn[s], v[s], al[s], be[s]
-            fine = all(np.all(np.isfinite(x)) for x in (K, Q, V, a, b))
+            fine = all(np.all(np.isfinite(x)) for x in (K, Q, a, b))
             whole = fine and np.all((a >= 2.0 ** -20) & (a <= 1)) and np.all((b >= 0) & (b <= 2))
             Sin, Ein = S.copy(), E.copy()
             for t in range(s.start, s.stop):             # the rule itself, and its bound token by token
@@ -154,11 +154,14 @@ def head(c, q, k, v, al, be, S):
             dX0 = b[:, None] * (2 * U * np.abs(V) + e * gi * (np.abs(K) @ np.abs(Sin).T))
             dU = aT @ dX0 + dT @ np.abs(X) + 2 * g(64) * (aT @ np.abs(X))
             TX = aT @ np.abs(X)
+            by_token, E_token = bound[s].copy(), E
             bound[s] = (e * gi * (np.abs(Q) @ np.abs(Sin).T) + np.abs(Pm) @ dU + e * (Pb @ TX) + 4 * g(64) * (np.abs(Pm) @ TX)
                         + gi * np.linalg.norm(Q, axis=1)[:, None] * Ein)
             w = D[-1][:, None]
             dS = 4 * U * gi[-1] * np.abs(Sin) + (w * (dU + (e_k + eD + 2 * g(68)) * TX)).T @ np.abs(K)
             E = gi[-1, 0] * Ein + np.linalg.norm(dS, axis=1)
+            if not np.all(np.abs(X) <= 2.0 ** 96):       # such rows, and those in their block, run token by token
+                bound[s], E = np.fmax(bound[s], by_token), np.fmax(E, E_token)
     return out, S, bound, E
 
 
@@ -256,6 +259,40 @@ def test_values_that_are_not_finite_reach_no_earlier_token(act, what):
     assert np.array_equal(out[100:], clean[0][100:]) and np.array_equal(state[1], clean[1][1])
     assert np.isnan(out[80:100]).any()
     c.check()
+
+
+# Sequences enough for blocks of 64 and of 128 state rows (where that many fit) by 32 heads.
+SOME = [130, 64, 7, 0, 90, 33, 65, 20]
+MANY = [64 + 5 * i for i in range(16)]
+
+
+@pytest.mark.parametrize("lens,dk,dv,out", [(SOME, 128, 128, "bf16"), (SOME, 128, 64, "f32"), (SOME, 64, 48, "bf16"), (MANY, 64, 128, "f32"),
+                                            (MANY, 128, 112, "bf16"), (MANY, 128, 128, "f32")])
+def test_many_heads(lens, dk, dv, out):
+    show("heads", len(lens), dk, dv, out)
+    Case(lens, 8, 32, dk, dv, "bf16", out, seed=dk + dv, first=3, behind=70).check()
+
+
+@pytest.mark.parametrize("lens,dk,dv", [([130, 64, 7], 128, 32), (SOME, 128, 64), (MANY, 64, 128)])
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_values_and_states_out_of_range(lens, dk, dv, act):
+    """One row each of three heads: a value that is NaN, one too large for a chunk's products, and an infinite state; and a gate
+    of a fourth head.  No other row is touched."""
+    show("rows", len(lens), dk, dv, act)
+    nv = 4 if len(lens) == 3 else 32
+    c = Case(lens, nv // 4, nv, dk, dv, act, seed=15)
+    clean, clean_state = c.run()
+    set_v = lambda t, h, r, x: c.v.__setitem__((t, h, r), np.float32(x) if act == "f32" else np.float32(x).view(np.uint32) >> 16)
+    set_v(70, 0, 5, np.nan)
+    set_v(3, 1, 30, 2.0 ** 100)
+    c.state[1, 2, 17, 9] = np.inf
+    c.alpha[100, 3] = 0.0
+    out, state = c.check()
+    assert np.isnan(out[70:130, 0, 5]).all() and np.isfinite(out[:70, 0, 5]).all()
+    others = np.ones(dv, dtype=bool)
+    others[[5, 30, 17]] = False
+    assert np.isfinite(out[:, :3][..., others]).all() and np.isfinite(state[:, :3][:, :, others]).all()
+    assert np.array_equal(out[:, 4:], clean[:, 4:]) and np.array_equal(state[:, 4:], clean_state[:, 4:])
 
 
 def test_against_the_recurrence():
