@@ -10,9 +10,12 @@
  *   O = diag(g) Q' S^T + P U,                      P_ij = D_ij q'_i . k'_j         (j <= i)
  *   S <- g_C S + sum_j D_Cj u_j k'_j^T
  * which is the recurrence rearranged: the same results up to rounding, in
- * single precision or better throughout.  Chunks whose inputs are not finite,
- * whose gates are not in [2^-20, 1] or whose write strengths are not in [0, 2]
- * run token by token, so what a later token holds never reaches an earlier one.
+ * single precision or better (of the output products, where the output is
+ * bf16, 16 bits).  Chunks whose keys or queries are not finite, whose gates are
+ * not in [2^-20, 1] or whose write strengths are not in [0, 2] run token by
+ * token, and so do the state rows whose values, or what the state predicts of
+ * them, are not finite or above 2^96: what a later token holds never reaches an
+ * earlier one, nor one row of a state another.
  *
  * Conventions as in moe_layer.h: device pointers owned by the caller, work
  * enqueued on `stream`, every argument checked before anything is enqueued,
