@@ -527,10 +527,10 @@ __device__ __forceinline__ bool find_scan(const GdcArgs& a, int dk, Scan& s) {
 // in three.  What a product takes of the next chunk is requested a chunk ahead,
 // between the products: the memory unit takes 64 bytes a cycle.
 //
-// Its own chain bounds it, 2.4 us a chunk alone on a CU, in cycles: first product
-// 900 with its requests, X and its split 600, second 700 to 900, third 900,
-// S and K into LDS 500, waits at barriers and for the memory unit the rest (one
-// sequence of 2048 tokens, 32 heads of 128 x 128: 78 us).
+// Its own chain bounds it, 2.2 us a chunk alone on a CU, of which a wave's 50
+// products are a sixth: the rest are their operands' way through LDS, the splits and
+// three barriers (one sequence of 2048 tokens, 32 heads of 128 x 128: 68 us; 78 with
+// every address formed from the chunk's number).
 template <int DK, int OUT>
 __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
   constexpr int OP = o_planes(OUT);
@@ -584,24 +584,28 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
   const int64_t st = static_cast<int64_t>(a.nk) * DK;
   const int64_t vst = static_cast<int64_t>(a.nv) * a.dv;
   constexpr int kOut = OUT == kF32 ? 4 : 2;
-  const uint16_t* const kb = static_cast<const uint16_t*>(a.k) + sc.begin * st + static_cast<int64_t>(sc.kh) * DK;
-  const uint16_t* const qb = static_cast<const uint16_t*>(a.q) + sc.begin * st + static_cast<int64_t>(sc.kh) * DK;
-  const uint16_t* const vb = static_cast<const uint16_t*>(a.v) + sc.begin * vst + static_cast<int64_t>(sc.h) * a.dv + sc.dv0;
-  uint8_t* const ob = static_cast<uint8_t*>(a.out) + (sc.begin * vst + static_cast<int64_t>(sc.h) * a.dv + sc.dv0) * kOut;
+  // where the chunks to request next begin, and the one to write
+  const int kst = static_cast<int>(st) * 2, vbytes = static_cast<int>(vst) * 2, ost = static_cast<int>(vst) * kOut;
+  const int64_t row = static_cast<int64_t>(sc.begin) + static_cast<int64_t>(sc.c0) * kC, to_v = static_cast<int64_t>(sc.h) * a.dv + sc.dv0;
+  const uint8_t* kn = static_cast<const uint8_t*>(a.k) + row * kst + static_cast<int64_t>(sc.kh) * DK * 2;
+  const uint8_t* qn = static_cast<const uint8_t*>(a.q) + row * kst + static_cast<int64_t>(sc.kh) * DK * 2;
+  const uint8_t* vn = static_cast<const uint8_t*>(a.v) + row * vbytes + to_v * 2;
+  const uint8_t* mn = a.ws + (slot_of(a, sc.b, sc.begin, sc.c0) * a.nv + sc.h) * slot_bytes(kBF16, OUT);
+  uint8_t* on = static_cast<uint8_t*>(a.out) + row * ost + to_v * kOut;
   // Offsets within a chunk.  The descriptors end with the last token: rows behind
   // it arrive as zeros, and are not written.
   uint32_t koff[kKl], voff[4];
 #pragma unroll
   for (int i = 0; i < kKl; ++i) {
     const int p = threadIdx.x + 256 * i;
-    koff[i] = (p / kPer) * static_cast<uint32_t>(st) * 2u + (p % kPer) * 16;
+    koff[i] = (p / kPer) * static_cast<uint32_t>(kst) + (p % kPer) * 16;
   }
-  const uint32_t qoff = token_of(w, n16) * static_cast<uint32_t>(st) * 2u + g * 16;
+  const uint32_t qoff = token_of(w, n16) * static_cast<uint32_t>(kst) + g * 16;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) voff[r] = (t4 + r) * static_cast<uint32_t>(vst) * 2u + n16 * 2;
+  for (int r = 0; r < 4; ++r) voff[r] = (t4 + r) * static_cast<uint32_t>(vbytes) + n16 * 2;
   const auto length = [&](int c) { return sc.n - c * kC < kC ? sc.n - c * kC : kC; };
-  const auto buffer = [](const void* base, int64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, static_cast<int>(bytes), 0x00020000);
+  const auto buffer = [](const void* base, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);
   };
   const auto load = [](auto rs, uint32_t off, int at) { return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, at, 0)); };
   u32x4 Kn[kKl];
@@ -613,9 +617,8 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
     float2 gc;                                 // g_C, and whether the chunk runs token by token
   };
   First even, odd;                             // by the chunk's number
-  const auto slot = [&](int c) { return a.ws + (slot_of(a, sc.b, sc.begin, c) * a.nv + sc.h) * slot_bytes(kBF16, OUT); };
   const auto ask_k = [&](int c) {
-    const auto rs = buffer(kb + static_cast<int64_t>(c) * kC * st, ((length(c) - 1) * st + DK) * 2);
+    const auto rs = buffer(kn, (length(c) - 1) * kst + DK * 2);
 #pragma unroll
     for (int i = 0; i < kKl; ++i) Kn[i] = load(rs, koff[i], 0);
   };
@@ -627,20 +630,20 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
     }
   };
   const auto ask_q = [&](int c, First& o, int s) {
-    const auto rq = buffer(qb + static_cast<int64_t>(c) * kC * st, ((length(c) - 1) * st + DK) * 2);
+    const auto rq = buffer(qn, (length(c) - 1) * kst + DK * 2);
     o.Q[s] = __builtin_bit_cast(bf16x8, load(rq, qoff + 64 * s, 0));
   };
   const auto ask_rest = [&](int c, First& o) {
-    const auto rv = buffer(vb + static_cast<int64_t>(c) * kC * vst, ((length(c) - 1) * vst + kRowsS) * 2);
-    const auto rf = buffer(slot(c), kVec * 4);
+    const auto rv = buffer(vn, (length(c) - 1) * vbytes + kRowsS * 2);
+    const auto rf = buffer(mn, kVec * 4);
 #pragma unroll
     for (int r = 0; r < 4; ++r) o.V[r] = __builtin_amdgcn_raw_buffer_load_b16(rv, voff[r], 0, 0);
     o.e = __builtin_bit_cast(f32x4, load(rf, t4 * 4, 0));
     o.f = __builtin_bit_cast(f32x4, load(rf, t4 * 4, kC * 4));
     o.gc = __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(rf, 0, 2 * kC * 4, 0));
   };
-  const auto ask_second = [&](int c, int s) {  // for the second, 32 columns of the matrices
-    const auto rm = buffer(slot(c), slot_bytes(kBF16, OUT));
+  const auto ask_second = [&](int s) {         // for the second, 32 columns of the matrices
+    const auto rm = buffer(mn, slot_bytes(kBF16, OUT));
     if (s <= w / 2)
 #pragma unroll
       for (int x = 0; x < 3; ++x) {
@@ -656,9 +659,10 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
     }
     ask_k(sc.c0);
     ask_rest(sc.c0, even);
-    ask_second(sc.c0, 0);
-    ask_second(sc.c0, 1);
+    ask_second(0);
+    ask_second(1);
     put_k(0);
+    if (sc.c0 + 1 < sc.c1) kn += static_cast<int64_t>(kC) * kst;
     ask_k(sc.c0 + 1 < sc.c1 ? sc.c0 + 1 : sc.c0);
   }
   __syncthreads();
@@ -668,6 +672,11 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
     const int len = sc.n - c * kC < kC ? sc.n - c * kC : kC;
     // requests without a condition (the last chunk asks for itself again), so that no copy of a register waits for one
     const int next = c + 1 < sc.c1 ? c + 1 : c;
+    if (c + 1 < sc.c1) {
+      qn += static_cast<int64_t>(kC) * kst;
+      vn += static_cast<int64_t>(kC) * vbytes;
+      mn += static_cast<int64_t>(a.nv) * slot_bytes(kBF16, OUT);
+    }
     const uint8_t* K = Kp[half];
     const float gC = one.gc.x;
     bool by_token = __builtin_amdgcn_readfirstlane(__float_as_int(one.gc.y)) != 0;
@@ -745,14 +754,14 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
         }
       put_x(Zp, zt + zt2);
     }
-    ask_second(next, 0);
+    ask_second(0);
     __syncthreads();
     if (!by_token) {
-      const auto ro = buffer(ob + static_cast<int64_t>(c) * kC * vst * kOut, ((len - 1) * vst + kRowsS) * kOut);
+      const auto ro = buffer(on, (len - 1) * ost + kRowsS * kOut);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         if constexpr (OUT == kF32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(qs[r]), ro, voff[r] * 2, 0, 0);
-        else __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(qs[r]), ro, voff[r], 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, static_cast<__bf16>(qs[r])), ro, voff[r], 0, 0);
       }
       // S^T, the columns of this wave
       bf16x8 Zb[2][3];
@@ -764,7 +773,7 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
       for (int t = 0; t < NT; ++t) {
         const int piece = 2 * (NT * w + t) + ((n16 & 3) >> 1);
         f32x4 d[2] = {};
-        if (t == 0) ask_second(next, 1);
+        if (t == 0) ask_second(1);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           bf16x8 Ka;                           // column n16 of the tile, tokens 32 s + 8 g + 0 .. 7
@@ -783,10 +792,12 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
         for (int i = 0; i < 4; ++i) S[t][i] = fmaf(gC, S[t][i], d[0][i] + d[1][i]);
       }
     } else {
-      ask_second(next, 1);
+      ask_second(1);
     }
     put_s();
     put_k(half ^ 1);
+    if (c + 2 < sc.c1) kn += static_cast<int64_t>(kC) * kst;
+    on += static_cast<int64_t>(kC) * ost;
     ask_k(c + 2 < sc.c1 ? c + 2 : sc.c1 - 1);  // a chunk ahead: what has to come from HBM takes half of one
     __syncthreads();
   };
@@ -809,9 +820,22 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
 //
 // A wave's 216 products of 16 x 16 x 32 a chunk, 16 cycles each, and the 80 KB of
 // operands that it reads from LDS bound it; two waves on a SIMD overlap them in
-// part: a chunk of 128 rows takes 6.6 us, of which the products are 2.9 and the reads
-// 2.1 (128 x 128 states; 8 sequences of 1024 tokens by 32 heads 106 us, 150 TF/s
-// of the recurrence's operations).
+// part: a chunk of 128 rows takes 6.0 us, of which the products are 2.9 and the reads
+// 2.1 (128 x 128 states; 8 sequences of 1024 tokens by 32 heads 96 us, 16 prompts of
+// 60 to 4000 tokens 286; 106 and 324 with pointers converted and addresses formed anew
+// for every load).
+// lds_load<16> to an address as a number: no conversion of a pointer, with its check for NULL, before each load.
+__device__ __forceinline__ void lds_load16(u32x4 rs, uint32_t to, uint32_t voff, uint32_t soff) {
+  const uint32_t la = __builtin_amdgcn_readfirstlane(to), so = __builtin_amdgcn_readfirstlane(soff);
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(la), "v"(voff), "s"(rs), "s"(so)
+      : "memory");
+}
+
 template <int DK, int OUT, int NW>
 struct ScanLds {
   static constexpr int kK = 0, kQ = kC * DK * 2, kV = 2 * kC * DK * 2, kF = kV + kC * 16 * NW * 2, kM = kF + kVec * 4;
@@ -868,26 +892,36 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_gdc_scan_bf16(GdcArgs a) {
   // all at once would hold the wave up.  The descriptors end with the last token:
   // rows behind it arrive as zeros.
   constexpr int kParts = 4;
-  const auto request = [&](int c, uint8_t* to, int part) {
+  const int kst = static_cast<int>(st) * 2, vbytes = static_cast<int>(vst) * 2;      // from token to token
+  const uint8_t* kn = reinterpret_cast<const uint8_t*>(kb) + static_cast<int64_t>(sc.c0) * kC * kst;   // of the chunk to request
+  const uint8_t* qn = reinterpret_cast<const uint8_t*>(qb) + static_cast<int64_t>(sc.c0) * kC * kst;
+  const uint8_t* vn = reinterpret_cast<const uint8_t*>(vb) + static_cast<int64_t>(sc.c0) * kC * vbytes;
+  const uint8_t* mn = a.ws + (slot_of(a, sc.b, sc.begin, sc.c0) * a.nv + sc.h) * slot_bytes(kBF16, OUT);
+  const auto request = [&](int c, uint32_t to, int part) {
     const int len = length(c);
-    const int64_t r = static_cast<int64_t>(c) * kC;
     if (part == 0) {
-      const u32x4 rk = raw_rsrc(kb + r * st, ((len - 1) * st + DK) * 2);
+      const u32x4 rk = raw_rsrc(kn, (len - 1) * kst + DK * 2);
 #pragma unroll
-      for (int i = 0; i < kKq; ++i) lds_load<16>(rk, to + L::kK + (NW * i + w) * 1024, koff[i], 0);
+      for (int i = 0; i < kKq; ++i) lds_load16(rk, to + L::kK + (NW * i + w) * 1024, koff[i], 0);
     } else if (part == 1) {
-      const u32x4 rq = raw_rsrc(qb + r * st, ((len - 1) * st + DK) * 2), rv = raw_rsrc(vb + r * vst, ((len - 1) * vst + vcols) * 2);
+      const u32x4 rq = raw_rsrc(qn, (len - 1) * kst + DK * 2), rv = raw_rsrc(vn, (len - 1) * vbytes + vcols * 2);
 #pragma unroll
-      for (int i = 0; i < kKq; ++i) lds_load<16>(rq, to + L::kQ + (NW * i + w) * 1024, koff[i], 0);
+      for (int i = 0; i < kKq; ++i) lds_load16(rq, to + L::kQ + (NW * i + w) * 1024, koff[i], 0);
 #pragma unroll
-      for (int i = 0; i < kVl; ++i) lds_load<16>(rv, to + L::kV + (NW * i + w) * 1024, voff[i], 0);
+      for (int i = 0; i < kVl; ++i) lds_load16(rv, to + L::kV + (NW * i + w) * 1024, voff[i], 0);
     } else {
       // the factors and the matrices lie as they do in the slot
-      const u32x4 rm = raw_rsrc(a.ws + (slot_of(a, sc.b, sc.begin, c) * a.nv + sc.h) * slot_bytes(kBF16, OUT), slot_bytes(kBF16, OUT));
+      const u32x4 rm = raw_rsrc(mn, slot_bytes(kBF16, OUT));
       constexpr int kEach = (kMl + NW - 1) / NW, kHalf = kEach / 2;
 #pragma unroll
       for (int i = part == 2 ? 0 : kHalf; i < (part == 2 ? kHalf : kEach); ++i)
-        if (NW * i + w < kMl) lds_load<16>(rm, to + L::kF + (NW * i + w) * 1024, lane * 16, (NW * i + w) * 1024);
+        if (NW * i + w < kMl) lds_load16(rm, to + L::kF + (NW * i + w) * 1024, lane * 16, (NW * i + w) * 1024);
+      if (part == kParts - 1) {
+        kn += static_cast<int64_t>(kC) * kst;
+        qn += static_cast<int64_t>(kC) * kst;
+        vn += static_cast<int64_t>(kC) * vbytes;
+        mn += static_cast<int64_t>(a.nv) * slot_bytes(kBF16, OUT);
+      }
     }
   };
   typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -950,15 +984,20 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_gdc_scan_bf16(GdcArgs a) {
     }
   };
 
+  const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_u8*)smem));
   int stage = 0;
   if (sc.c0 < sc.c1)
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) request(sc.c0, smem, i);
-  const uint32_t ooff = (static_cast<uint32_t>(8 * g) * static_cast<uint32_t>(vst) + n16) * (OUT == kF32 ? 4u : 2u);
+    for (int i = 0; i < kParts; ++i) request(sc.c0, base, i);
+  constexpr int kOut = OUT == kF32 ? 4 : 2;
+  const int ost = static_cast<int>(vst) * kOut;
+  const uint32_t ooff = 8 * g * static_cast<uint32_t>(ost) + n16 * kOut;
+  uint8_t* on = static_cast<uint8_t*>(a.out) +
+                ((static_cast<int64_t>(sc.begin) + static_cast<int64_t>(sc.c0) * kC) * vst + static_cast<int64_t>(sc.h) * a.dv + dv0) * kOut;
   for (int c = sc.c0; c < sc.c1; ++c) {
     uint8_t* const in = smem + stage * L::kStage;
     stage ^= 1;
-    uint8_t* const other = smem + stage * L::kStage;
+    const uint32_t other = base + stage * L::kStage;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();                           // the chunk is there, and nobody reads the other stage any more
     const bool more = c + 1 < sc.c1;
@@ -1012,6 +1051,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_gdc_scan_bf16(GdcArgs a) {
     }
     if (by_token || __ballot(far)) {           // outside the range of the matrices, or not finite
       tokens(c, in);
+      on += static_cast<int64_t>(kC) * ost;
       continue;
     }
     // (Z-matrix) X and (O-matrix) X, the smallest terms first
@@ -1036,29 +1076,17 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void k_gdc_scan_bf16(GdcArgs a) {
           }
       }
     }
-    {
-      // rows 32 s + 8 g + 4 y + r: a base for each (s, y, r), one offset for all
-      const int64_t osz = OUT == kF32 ? 4 : 2;
-      uint8_t* const ob = static_cast<uint8_t*>(a.out) +
-                          ((static_cast<int64_t>(sc.begin) + static_cast<int64_t>(c) * kC) * vst + static_cast<int64_t>(sc.h) * a.dv + dv0) * osz;
-      const auto store = [&](int i, int r) {
-        uint8_t* p = ob + (32 * (i >> 1) + 4 * (i & 1) + r) * vst * osz + ooff;
-        if constexpr (OUT == kF32) *reinterpret_cast<float*>(p) = o[i][r];
-        else *reinterpret_cast<uint16_t*>(p) = f32_to_bf16(o[i][r]);
-      };
-      if (len == kC) {
+    // rows 32 s + 8 g + 4 y + r; those behind the last token are beyond the descriptor's end
+    const auto ro = __builtin_amdgcn_make_buffer_rsrc(on, 0, (len - 1) * ost + kRowsS * kOut, 0x00020000);
+    on += static_cast<int64_t>(kC) * ost;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) store(i, r);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (token_of(i, 4 * g + r) < len) store(i, r);
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t off = ooff + static_cast<uint32_t>((32 * (i >> 1) + 4 * (i & 1) + r) * ost);
+        if constexpr (OUT == kF32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(o[i][r]), ro, off, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, static_cast<__bf16>(o[i][r])), ro, off, 0, 0);
       }
-    }
     // S^T
     bf16x8 Zp[2][3];
 #pragma unroll
@@ -1277,12 +1305,12 @@ bool launch_scan(const GdcArgs& a, uint32_t blocks, hipStream_t s) {
   return true;
 }
 
-// State rows a block of the scan takes.  A chunk takes a block of 16 rows 3.3 us
-// (two on a CU; 2.4 alone), one of 64 rows 4.3 and one of 128 rows 6.6 (128 x 128
+// State rows a block of the scan takes.  A chunk takes a block of 16 rows 3.0 us
+// (two on a CU; 2.2 alone), one of 64 rows 4.0 and one of 128 rows 6.2 (128 x 128
 // states, one on a CU).  The longest sequence's chunks run one after the other, and
 // all of them share the chip: the larger of the two is what a width takes, and the
-// smallest wins.  1, 2, 3, 4 and 8 sequences of 1024 tokens by 32 heads: 16 rows 40,
-// 53, 99, 106 and 208 us; 64 rows 66, 67, 70, 72 and 140; 128 rows 105 each.
+// smallest wins.  1, 2, 3, 4 and 8 sequences of 1024 tokens by 32 heads: 16 rows 35,
+// 47, 75, 86 and 196 us; 64 rows 59, 62, 62, 64 and 126; 128 rows 79, 81, 83, 83 and 96.
 int scan_width(const gdn_desc* d, int32_t B, int32_t N, int T_max) {
   if (d->act_dtype == MOE_F32) return kRowsS;
   const bool fits = d->d_k == 64 ? kHasWide<64, kF32> : (d->out_dtype == MOE_F32 ? kHasWide<128, kF32> : kHasWide<128, kBF16>);
@@ -1291,9 +1319,9 @@ int scan_width(const gdn_desc* d, int32_t B, int32_t N, int T_max) {
   double least = 1e300;
   for (const int w : {16, 64, 128}) {
     if (w == 128 && (!fits || d->d_v <= 64)) continue;
-    const double t = w == 16 ? 3.3 : (w == 64 ? 4.3 : 6.6), slots = w == 16 ? 512 : 256;
+    const double t = w == 16 ? 3.0 : (w == 64 ? 4.0 : 6.2), slots = w == 16 ? 512 : 256;
     const double blocks = heads * ((d->d_v + w - 1) / w);
-    const double one = w == 16 && blocks <= 256 ? 2.4 : t;
+    const double one = w == 16 && blocks <= 256 ? 2.2 : t;
     const double took = std::max(chain * one, std::ceil(blocks / slots) * mean * t);
     if (took < least) {
       least = took;
