@@ -1107,14 +1107,18 @@ __global__ __launch_bounds__(256, RT == 1 ? 2 : 1) void k_attn_f32(AttnArgs a) {
 
 // ---------------------------------------------------------------------------
 // The parts of a row joined, where blocks shared its keys, and zeros for rows
-// without any.  A wave takes 64 dims of a row, 16 lanes a part (four parts at
-// once, four loads each on the way); WIDE: the block's four waves share them.  Bound
+// without any.  A wave takes 128 dims of a row (heads of 64 dims: 64), 32 or 16 lanes a
+// part, two or four parts at once, four loads each on the way; WIDE, for many parts of few
+// rows: the block's four waves share those of 64 dims.  Bound
 // by the parts' reads, and by the launch where there are few (1 token of 16 heads
-// 4.0 us; 248 tokens of 32 heads, 32 MB of parts, 14).
+// 4.0 us; 248 tokens of 32 heads of 128, 32 MB of parts, 9.4, and 14 with 64 dims a wave).
+constexpr int join_dims(int D, bool wide) { return wide || D == 64 ? 64 : 128; }
+
 template <int DT, int D, int ROWS, int STEP, bool WIDE>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-  constexpr int kSlices = D / 64;
-  __shared__ f32x4 sums[4][16];
+  constexpr int W = join_dims(D, WIDE), LP = W / 4;    // dims a wave, lanes a part
+  constexpr int kSlices = D / W;
+  __shared__ f32x4 sums[4][LP];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
   const int64_t item = WIDE ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * 4 + wave;
   const int64_t per = static_cast<int64_t>(a.new_max) * a.nq * kSlices;
@@ -1125,9 +1129,9 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   Rows r;
   if (!sequence(a, b, r) || row >= r.n * a.each) return;
   const int steps = steps_of<STEP>(r);
-  const int64_t o = ((r.begin + static_cast<int64_t>(row / a.each)) * a.nq + h * a.each + row % a.each) * D + slice * 64 + (lane & 15) * 4;
+  const int64_t o = ((r.begin + static_cast<int64_t>(row / a.each)) * a.nq + h * a.each + row % a.each) * D + slice * W + lane % LP * 4;
   if (steps == 0) {
-    if (lane < 16 && (!WIDE || wave == 0)) put_row<DT>(a.out, o, f32x4{0.f, 0.f, 0.f, 0.f}, 0.f);
+    if (lane < LP && (!WIDE || wave == 0)) put_row<DT>(a.out, o, f32x4{0.f, 0.f, 0.f, 0.f}, 0.f);
     return;
   }
   const int share = a.shares[0], before = b > 0 ? a.shares[b] : 0;
@@ -1142,10 +1146,14 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
   for (int p = lane; p < parts; p += kWave) M = fmaxf(M, a.ml[place(p) * 2]);
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) M = fmaxf(M, __shfl_xor(M, d));
+  const auto over_parts = [&](float x) {     // lanes that hold the same dims of other parts
+    if constexpr (LP == 16) x += __uint_as_float(lane_xor<16>(__float_as_uint(x), lane));
+    return x + __uint_as_float(lane_xor<32>(__float_as_uint(x), lane));
+  };
   f32x4 sum = {0.f, 0.f, 0.f, 0.f};
   float l = 0.f;
-  constexpr int kGroups = WIDE ? 16 : 4;
-  for (int p0 = (WIDE ? wave * 4 : 0) + (lane >> 4); p0 < parts; p0 += 4 * kGroups) {
+  constexpr int kGroups = (WIDE ? 4 : 1) * (kWave / LP);
+  for (int p0 = (WIDE ? wave * (kWave / LP) : 0) + lane / LP; p0 < parts; p0 += 4 * kGroups) {
     f32x4 v[4];
     float2 ml[4];
 #pragma unroll
@@ -1153,7 +1161,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
       const int p = p0 + kGroups * i < parts ? p0 + kGroups * i : p0;
       const int64_t at = place(p);
       ml[i] = *reinterpret_cast<const float2*>(a.ml + at * 2);
-      v[i] = *reinterpret_cast<const f32x4*>(a.part + at * D + slice * 64 + (lane & 15) * 4);
+      v[i] = *reinterpret_cast<const f32x4*>(a.part + at * D + slice * W + lane % LP * 4);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -1165,18 +1173,18 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
       }
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) sum[j] = xor_add(sum[j], lane);
-  l = xor_add(l, lane);
+  for (int j = 0; j < 4; ++j) sum[j] = over_parts(sum[j]);
+  l = over_parts(l);
   if constexpr (WIDE) {
     __shared__ float ls[4];
-    if (lane < 16) sums[wave][lane] = sum;
+    if (lane < LP) sums[wave][lane] = sum;
     if (lane == 0) ls[wave] = l;
     __syncthreads();
-    sum = sums[0][lane & 15] + sums[1][lane & 15] + sums[2][lane & 15] + sums[3][lane & 15];
+    sum = sums[0][lane % LP] + sums[1][lane % LP] + sums[2][lane % LP] + sums[3][lane % LP];
     l = ls[0] + ls[1] + ls[2] + ls[3];
     if (wave != 0) return;
   }
-  if (lane < 16) put_row<DT>(a.out, o, sum, l);
+  if (lane < LP) put_row<DT>(a.out, o, sum, l);
 }
 
 // ---------------------------------------------------------------------------
@@ -1216,8 +1224,11 @@ int attn_plan(const attn_desc* d, int32_t B, int32_t N, int32_t new_max, int32_t
   if (p->even) {
     if (units * steps < slots) p->blocks = units * steps;
     else p->blocks = slots;
-    p->wide = p->blocks > 32 * units;
-    const int64_t items = static_cast<int64_t>(B) * rows * d->n_kv_heads * (D / 64);
+    // 32 parts of few rows: 6.8 us by four waves and 8.1 by one (4 sequences of 8
+    // tokens, 16 heads of 256), 4.5 and 7.8 (2 of 6, 32 heads of 128); 8 parts of
+    // 7936 rows take one wave each 9.4.
+    p->wide = p->blocks > 12 * units;
+    const int64_t items = static_cast<int64_t>(B) * rows * d->n_kv_heads * (D / join_dims(D, p->wide));
     p->join = p->wide ? items : (items + 3) / 4;
     const size_t at = static_cast<size_t>(p->blocks) * 2 * 16 * p->rt;
     p->part = at * D * 4;

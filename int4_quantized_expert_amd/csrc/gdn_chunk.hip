@@ -711,7 +711,7 @@ __global__ __launch_bounds__(256, 2) void k_gdc_scan_few(GdcArgs a) {
         for (int x = 2; x >= 0; --x) {
           const bf16x8 Sb = *reinterpret_cast<const bf16x8*>(Sp + x * kPlaneS + s_at(n16, 32 * s + 8 * g));
           f32x4& kd = s & 1 ? ks2 : ks;
-          f32x4& qd = s & 1 ? qs2 : qs;
+          f32x4& qd = (s & 1) && OP == 2 ? qs2 : qs;       // with three planes its chain is as long as the other
           kd = __builtin_amdgcn_mfma_f32_16x16x32_bf16(Ka, Sb, kd, 0, 0, 0);
           if (x < OP) qd = __builtin_amdgcn_mfma_f32_16x16x32_bf16(one.Q[s], Sb, qd, 0, 0, 0);
         }
@@ -1417,7 +1417,8 @@ extern "C" int gdn_chunk_forward(const gdn_desc* d, int32_t B, int32_t N, int32_
   const int width = scan_width(d, B, N, a.T_max);
   const int64_t heads = static_cast<int64_t>(B) * d->n_v_heads;
   const int64_t scan = (heads + 7) / 8 * 8 * ((d->d_v + width - 1) / width), prep = static_cast<int64_t>(p.slots) * d->n_v_heads;
-  if (scan >= (1 << 24) || prep >= (1 << 24)) return bad("B=%lld sequences of N=%lld tokens are too many blocks for one launch", B, N);
+  // a launch takes fewer than 2^32 threads
+  if (scan >= (width == 128 ? 1 << 23 : 1 << 24) || prep >= (1 << 24)) return bad("B=%lld sequences of N=%lld tokens are too many blocks for one launch", B, N);
   const int chunks = (a.T_max + kC - 1) / kC;
   hipStream_t s = static_cast<hipStream_t>(stream);
   for (a.first = 0; a.first == 0 || a.first < chunks; a.first += a.per_pass) {
